@@ -64,7 +64,9 @@ typedef enum mm_type {
     MM_TYPE_F16 = 1,
     MM_TYPE_Q4_0 = 2,
     MM_TYPE_Q8_0 = 3,
-    MM_TYPE_Q4_0R = 4      /* Q4_0 weights in the repacked layout (mm_repack_q4_0) */
+    MM_TYPE_Q4_0R = 4,     /* Q4_0 weights in the repacked layout (mm_repack_q4_0) */
+    MM_TYPE_F8 = 5         /* OCP e4m3 codes with one f32 scale per block of 128
+                              (mm_quantize_f8); products: mm_mul_mat_f8_*, mm_moe_f32 */
 } mm_type;
 
 /*
@@ -261,8 +263,102 @@ mm_status mm_mul_mat_f32(const float* src0, const float* src1, float* dst,
                          int64_t M, int64_t N, int64_t K,
                          void* ws, size_t ws_bytes, void* stream);
 
-/* Bytes of workspace the product of `type` (F32, F16, Q4_0, Q8_0 or Q4_0R)
- * needs at this shape; 0 for an invalid shape or type.  Pure host function. */
+/*
+ * The F8 type: OCP 8-bit floating point e4m3 (sign, 4 exponent bits with
+ * bias 7, 3 fraction bits, largest value 448, 0x7f and 0xff NaN, no
+ * infinity) with one f32 scale per block of 128 values along K, for
+ * activations per row, for weights shared by 128 rows.  Codes and scales are
+ * two arrays:
+ *   codes:  [rows][K] bytes, contiguous, 16-byte aligned; K % 32 == 0,
+ *           K <= 2^23 (a last block of 32, 64 or 96 values is allowed);
+ *   scales: f32 [ceil(rows / R)][ceil(K / 128)], R = 1 or 128, 4-byte
+ *           aligned (the last row of blocks may be short too).
+ *   value = scale * code.
+ *
+ * mm_quantize_f8 -- x[nrows][k] (f32, 16-byte aligned) -> codes and scales,
+ *   block_rows R = 1 or 128 (else MM_ERR_ARG):
+ *     d = max(fl32(amax / 448), 2^-126), amax over the block (a NaN does not
+ *     count); id = fl32(1 / d); code = e4m3(fl32(x * id)), round to nearest
+ *     even, a NaN stays one.  An infinity makes its block's scale infinite and
+ *     its own code NaN (the products of that block are NaN).
+ *   No overlap between the three arrays.
+ */
+mm_status mm_quantize_f8(const float* x, void* codes, float* scales, int64_t nrows, int64_t k,
+                         int block_rows, void* stream);
+
+/*
+ * mm_mul_mat_f8_f32 -- dst[M][N] (f32) = F8(src1)[M][K] . F8 src0[N][K]^T.
+ *   src0, scale0: weight codes [N][K] and scales [ceil(N/128)][ceil(K/128)].
+ *   src1: f32 [M][K], 16-byte aligned; quantized within the call as
+ *         mm_quantize_f8 with block_rows 1 does (same codes and scales).
+ *   dst: f32 [M][N], 4-byte aligned (16 and N % 4 == 0: wider stores).
+ *   ws:  mm_mul_mat_f8_workspace_size(M, N, K, 0) bytes, 256-byte aligned
+ *        (the quantized src1 and any split-K partial sums).
+ * mm_mul_mat_f8_f8 -- the same product of a src1 that is quantized already
+ *   (one mm_quantize_f8, block_rows 1, ahead of several products): src1 codes
+ *   [M][K], scale1 [M][ceil(K/128)].  ws: mm_mul_mat_f8_workspace_size(M, N,
+ *   K, 1) bytes.
+ * dst[m][n] = sum_b scale1[m][b] * scale0[n/128][b] * S_b[m][n], S_b the
+ * fp32 sum of the block's code products (each exact); a NaN code or a
+ * non-finite scale makes the outputs it enters NaN or infinite and no other.
+ * mm_mul_mat_workspace_size(MM_TYPE_F8, ...) is the size for f32 src1 (which
+ * is the larger one), mm_row_bytes(MM_TYPE_F8, K) the bytes of a row of
+ * codes; mm_dispatch and mm_debug_mul_mat do not take this type.
+ */
+mm_status mm_mul_mat_f8_f32(const void* src0, const float* scale0, const float* src1, float* dst,
+                            int64_t M, int64_t N, int64_t K, void* ws, size_t ws_bytes,
+                            void* stream);
+mm_status mm_mul_mat_f8_f8(const void* src0, const float* scale0, const void* src1,
+                           const float* scale1, float* dst, int64_t M, int64_t N, int64_t K,
+                           void* ws, size_t ws_bytes, void* stream);
+size_t mm_mul_mat_f8_workspace_size(int64_t M, int64_t N, int64_t K, int src1_quantized);
+
+/*
+ * mm_moe_f32 -- a mixture-of-experts layer for a few tokens (decode), whole:
+ *   l[t][e] = sum_d x[t][d] router[e][d]       (summed in fp64)
+ *   p[t] = softmax over e of l[t]
+ *   ids[t][j], j < top_k: the experts of the largest l[t], in descending
+ *     order, ties to the lower index (a NaN logit counts as the lowest)
+ *   weights[t][j] = p[t][ids[t][j]], divided by their sum over j if norm
+ *   h[t][j] = silu(gate_e x[t]) * (up_e x[t]) for e = ids[t][j],
+ *     silu(v) = v / (1 + exp(-v))
+ *   dst[t] = sum_j weights[t][j] * down_e h[t][j]
+ * The activations are not rounded to 8 bits (unlike the quantized products'
+ * src1): x and h enter the products with 22 significant bits relative to
+ * their block of 32 values, every product is exact and sums are fp32.
+ *
+ * The layer (a host struct; the library keeps no reference to it):
+ *   type    of the expert matrices:
+ *     MM_TYPE_Q4_0R  each expert's matrix as mm_repack_q4_0 writes it
+ *                    (mm_repacked_q4_0_bytes(rows, K) bytes), experts in a row
+ *     MM_TYPE_F8     codes [E][rows][K], scales [E][ceil(rows/128)][ceil(K/128)]
+ *     MM_TYPE_F16    binary16 [E][rows][K]
+ *   gate, up: rows = F, K = D; down: rows = D, K = F; 16-byte aligned
+ *   gate_scale, up_scale, down_scale: F8 only (4-byte aligned), else unused
+ *   router: f32 [E][D], 16-byte aligned
+ *   D, F: multiples of 32, at most 2^20; 1 <= E <= 512; 1 <= top_k <= 16, E
+ * x: f32 [T][D], 16-byte aligned; dst: f32 [T][D]; 0 <= T <= 128 (larger
+ *   batches amortise the weights in the products above).
+ * ids (int32) and weights (f32) [T][top_k]: outputs, either may be NULL.
+ * ws: mm_moe_workspace_size(layer, T) bytes, 256-byte aligned.
+ * A token whose x holds an infinity or NaN (or whose logits do, or whose h
+ * overflows) gets NaN in dst; other tokens are unaffected, as they are by a
+ * non-finite weight of an expert that they do not use.
+ */
+typedef struct mm_moe_layer {
+    int type, top_k, norm;
+    int64_t D, F, E;
+    const float* router;
+    const void *gate, *up, *down;
+    const float *gate_scale, *up_scale, *down_scale;
+} mm_moe_layer;
+
+mm_status mm_moe_f32(const mm_moe_layer* layer, const float* x, float* dst, int32_t* ids,
+                     float* weights, int64_t T, void* ws, size_t ws_bytes, void* stream);
+size_t mm_moe_workspace_size(const mm_moe_layer* layer, int64_t T);
+
+/* Bytes of workspace the product of `type` (F32, F16, Q4_0, Q8_0, Q4_0R or F8)
+ * needs at this shape (F8: with f32 src1); 0 for an invalid shape or type.  Pure host function. */
 size_t mm_mul_mat_workspace_size(int type, int64_t M, int64_t N, int64_t K);
 
 /* Bytes of one row of K values of `type`; -1 if K is invalid for it. */

@@ -11,6 +11,10 @@ there is no CPU fallback.
     dst = mul_mat_f32(w_f32, x)          # w_f32: float32 [N, K]
     w_q4 = quantize_q4_0(w_f32)          # Q4_0 blocks of 18 bytes
     a_q8 = quantize_q8_0(x)              # Q8_0 blocks of 34 bytes (the wdata content)
+    w_f8, w_scale = quantize_f8(w_f32, 128)       # e4m3 codes, a scale per 128 x 128 block
+    dst = mul_mat_f8_f32(w_f8, w_scale, x)        # x quantized per row and 128 values within
+    layer = MoeLayer(MM_TYPE_F16, router, gate, up, down, F, top_k)
+    dst, ids, weights = moe_f32(layer, x)         # mixture-of-experts layer, a few tokens
 """
 from __future__ import annotations
 
@@ -26,12 +30,14 @@ __all__ = [
     "mul_mat_f16_f32",
     "mul_mat_f32", "workspace_size", "debug_workspace_size", "row_bytes", "dispatch",
     "debug_mul_mat", "status_string", "q4_0_init", "q4_0_compute", "mul_mat_q4_0_f32_group",
-    "group_workspace_size",
+    "group_workspace_size", "MM_TYPE_F8", "quantize_f8", "mul_mat_f8_f32", "mul_mat_f8_f8",
+    "f8_workspace_size", "MoeLayer", "moe_f32",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libqsgemm.so")
 
 MM_TYPE_F32, MM_TYPE_F16, MM_TYPE_Q4_0, MM_TYPE_Q8_0, MM_TYPE_Q4_0R = 0, 1, 2, 3, 4
+MM_TYPE_F8 = 5
 
 if not os.path.exists(LIB_PATH):
     raise ImportError(
@@ -53,6 +59,12 @@ for _name, _args, _res in [
     ("mm_repacked_q4_0_bytes", [_i64, _i64], _i64),
     ("mm_mul_mat_f16_f32", [_vp, _vp, _vp, _i64, _i64, _i64, _vp, _sz, _vp], _int),
     ("mm_mul_mat_f32", [_vp, _vp, _vp, _i64, _i64, _i64, _vp, _sz, _vp], _int),
+    ("mm_quantize_f8", [_vp, _vp, _vp, _i64, _i64, _int, _vp], _int),
+    ("mm_mul_mat_f8_f32", [_vp, _vp, _vp, _vp, _i64, _i64, _i64, _vp, _sz, _vp], _int),
+    ("mm_mul_mat_f8_f8", [_vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _vp, _sz, _vp], _int),
+    ("mm_mul_mat_f8_workspace_size", [_i64, _i64, _i64, _int], _sz),
+    ("mm_moe_f32", [_vp, _vp, _vp, _vp, _vp, _i64, _vp, _sz, _vp], _int),
+    ("mm_moe_workspace_size", [_vp, _i64], _sz),
     ("mm_q4_0_init", [_vp, _vp, _i64, _i64, _i64, _sz, _vp], _int),
     ("mm_q4_0_compute", [_vp, _vp, _i64, _i64, _i64, _vp, _sz, _vp], _int),
     ("mm_mul_mat_q4_0_f32_group", [_int, ctypes.POINTER(_vp), ctypes.POINTER(_vp),
@@ -266,6 +278,168 @@ def mul_mat_f32(w: torch.Tensor, x: torch.Tensor, out=None, ws=None) -> torch.Te
     if w.shape[1] != x.shape[1]:
         raise ValueError("K mismatch")
     return _mul_mat(lib.mm_mul_mat_f32, MM_TYPE_F32, w, x, out, ws, "mm_mul_mat_f32")
+
+
+def _ceil128(v: int) -> int:
+    return (v + 127) // 128
+
+
+def quantize_f8(x: torch.Tensor, block_rows: int = 1, out=None):
+    """float32 [rows, K] -> (codes float8_e4m3fn [rows, K], scales float32
+    [ceil(rows / block_rows), ceil(K / 128)]); block_rows 1 (activations) or 128 (weights)."""
+    x = _dev(x, "x", torch.float32)
+    rows, k = x.shape
+    if out is None:
+        nb = rows if block_rows == 1 else _ceil128(rows)
+        out = (torch.empty((rows, k), dtype=torch.float8_e4m3fn, device=x.device),
+               torch.empty((nb, _ceil128(k)), dtype=torch.float32, device=x.device))
+    else:
+        _f8(out[0], out[1], rows, k, 1 if block_rows == 1 else 128, "out")
+    codes, scales = out
+    _same_device(x, codes=codes, scales=scales)
+    with torch.cuda.device(x.device):
+        _check(lib.mm_quantize_f8(x.data_ptr(), codes.data_ptr(), scales.data_ptr(), rows, k, block_rows,
+                                  _stream(x)), "mm_quantize_f8")
+    return codes, scales
+
+
+def _f8(codes, scales, rows, k, block_rows, name):
+    """Checks one e4m3 operand: codes [rows, k] (float8_e4m3fn or uint8) and its scales."""
+    _dev(codes, name)
+    _dev(scales, f"{name} scales", torch.float32)
+    if codes.dtype not in (torch.float8_e4m3fn, torch.uint8):
+        raise TypeError(f"{name} must be float8_e4m3fn or uint8, got {codes.dtype}")
+    if tuple(codes.shape) != (rows, k):
+        raise ValueError(f"{name} must be [{rows}, {k}], got {list(codes.shape)}")
+    if tuple(scales.shape) != ((rows + block_rows - 1) // block_rows, _ceil128(k)):
+        raise ValueError(f"{name} scales must be [ceil({rows} / {block_rows}), ceil({k} / 128)], "
+                         f"got {list(scales.shape)}")
+
+
+def f8_workspace_size(m: int, n: int, k: int, src1_quantized: bool = False) -> int:
+    return int(lib.mm_mul_mat_f8_workspace_size(int(m), int(n), int(k), int(src1_quantized)))
+
+
+def _same_device(x, **others):
+    for name, t in others.items():
+        if t is not None and t.device != x.device:
+            raise ValueError(f"{name} is on {t.device}, expected {x.device}")
+
+
+def _out(out, m, n, device):
+    if out is None:
+        return torch.empty((m, n), dtype=torch.float32, device=device)
+    _dev(out, "out", torch.float32)
+    if tuple(out.shape) != (m, n):
+        raise ValueError(f"out must be [{m}, {n}], got {list(out.shape)}")
+    return out
+
+
+def mul_mat_f8_f32(w: torch.Tensor, w_scale: torch.Tensor, x: torch.Tensor, out=None, ws=None) -> torch.Tensor:
+    """dst[M, N] = F8(x)[M, K] . F8(w)[N, K]^T; w e4m3 [N, K] with scales [ceil(N/128), ceil(K/128)],
+    x float32 [M, K], quantized within (one scale per row and 128 values)."""
+    x = _dev(x, "x", torch.float32)
+    m, k = x.shape
+    n = w.shape[0]
+    _f8(w, w_scale, n, k, 128, "w")
+    out = _out(out, m, n, x.device)
+    ws = _workspace(f8_workspace_size(m, n, k, False), x.device, ws)
+    _same_device(x, w=w, w_scale=w_scale, out=out, ws=ws)
+    with torch.cuda.device(x.device):
+        _check(lib.mm_mul_mat_f8_f32(w.data_ptr(), w_scale.data_ptr(), x.data_ptr(), out.data_ptr(), m, n, k,
+                                     _ptr(ws), 0 if ws is None else ws.numel(), _stream(x)),
+               "mm_mul_mat_f8_f32")
+    return out
+
+
+def mul_mat_f8_f8(w: torch.Tensor, w_scale: torch.Tensor, a: torch.Tensor, a_scale: torch.Tensor,
+                  out=None, ws=None) -> torch.Tensor:
+    """mul_mat_f8_f32 with src1 quantized already: a e4m3 [M, K], a_scale [M, ceil(K/128)]
+    (quantize_f8 with block_rows 1)."""
+    a = _dev(a, "a")
+    m, k = a.shape
+    n = w.shape[0]
+    _f8(w, w_scale, n, k, 128, "w")
+    _f8(a, a_scale, m, k, 1, "a")
+    out = _out(out, m, n, a.device)
+    ws = _workspace(f8_workspace_size(m, n, k, True), a.device, ws)
+    _same_device(a, w=w, w_scale=w_scale, a_scale=a_scale, out=out, ws=ws)
+    with torch.cuda.device(a.device):
+        _check(lib.mm_mul_mat_f8_f8(w.data_ptr(), w_scale.data_ptr(), a.data_ptr(), a_scale.data_ptr(),
+                                    out.data_ptr(), m, n, k, _ptr(ws), 0 if ws is None else ws.numel(),
+                                    _stream(a)), "mm_mul_mat_f8_f8")
+    return out
+
+
+class _MoeStruct(ctypes.Structure):
+    _fields_ = [("type", _int), ("top_k", _int), ("norm", _int), ("D", _i64), ("F", _i64), ("E", _i64),
+                ("router", _vp), ("gate", _vp), ("up", _vp), ("down", _vp),
+                ("gate_scale", _vp), ("up_scale", _vp), ("down_scale", _vp)]
+
+
+class MoeLayer:
+    """The weights of a mixture-of-experts layer, for moe_f32 (holds the tensors and the C struct).
+
+    router float32 [E, D]; gate, up (F x D per expert) and down (D x F) by mm_type:
+    MM_TYPE_Q4_0R uint8 [E, repacked_bytes(rows, K)] (repack_q4_0 of each expert), MM_TYPE_F8
+    e4m3 [E, rows, K] with float32 scales [E, ceil(rows/128), ceil(K/128)], MM_TYPE_F16 float16
+    [E, rows, K].  norm: the top_k probabilities are divided by their sum."""
+
+    def __init__(self, mm_type, router, gate, up, down, f, top_k, gate_scale=None, up_scale=None,
+                 down_scale=None, norm=True):
+        _dev(router, "router", torch.float32)
+        e, d = router.shape
+        f, top_k = int(f), int(top_k)
+        dtypes = {MM_TYPE_Q4_0R: (torch.uint8,), MM_TYPE_F8: (torch.float8_e4m3fn, torch.uint8),
+                  MM_TYPE_F16: (torch.float16,)}
+        if mm_type not in dtypes:
+            raise ValueError("mm_type must be MM_TYPE_Q4_0R, MM_TYPE_F8 or MM_TYPE_F16")
+        scales = {"gate": gate_scale, "up": up_scale, "down": down_scale}
+        for name, w, rows, k in (("gate", gate, f, d), ("up", up, f, d), ("down", down, d, f)):
+            _dev(w, name)
+            if w.dtype not in dtypes[mm_type]:
+                raise TypeError(f"{name} must be {dtypes[mm_type][0]}, got {w.dtype}")
+            shape = (e, repacked_bytes(rows, k)) if mm_type == MM_TYPE_Q4_0R else (e, rows, k)
+            if tuple(w.shape) != shape:
+                raise ValueError(f"{name} must be {list(shape)}, got {list(w.shape)}")
+            _same_device(router, **{name: w})
+            if mm_type == MM_TYPE_F8:
+                s = _dev(scales[name], f"{name}_scale", torch.float32)
+                if tuple(s.shape) != (e, _ceil128(rows), _ceil128(k)):
+                    raise ValueError(f"{name}_scale must be [{e}, {_ceil128(rows)}, {_ceil128(k)}], got {list(s.shape)}")
+                _same_device(router, **{f"{name}_scale": s})
+            else:
+                scales[name] = None
+        self.device, self.d, self.f, self.e, self.top_k = router.device, d, f, e, top_k
+        self.tensors = (router, gate, up, down, *scales.values())
+        self.struct = _MoeStruct(mm_type, top_k, int(bool(norm)), d, f, e, *(_ptr(t) for t in self.tensors))
+        self._ref = ctypes.byref(self.struct)
+
+    def workspace_size(self, t: int) -> int:
+        return int(lib.mm_moe_workspace_size(self._ref, int(t)))
+
+
+def moe_f32(layer: MoeLayer, x: torch.Tensor, out=None, ids=None, weights=None, ws=None):
+    """(dst [T, D], ids int32 [T, top_k], weights [T, top_k]) of the layer on x float32 [T, D]."""
+    x = _dev(x, "x", torch.float32)
+    t, d = x.shape
+    if d != layer.d or x.device != layer.device:
+        raise ValueError(f"x must be [T, {layer.d}] on {layer.device}, got {list(x.shape)} on {x.device}")
+    out = _out(out, t, d, x.device)
+    if ids is None:
+        ids = torch.empty((t, layer.top_k), dtype=torch.int32, device=x.device)
+    if weights is None:
+        weights = torch.empty((t, layer.top_k), dtype=torch.float32, device=x.device)
+    for name, v, dtype in (("ids", ids, torch.int32), ("weights", weights, torch.float32)):
+        _dev(v, name, dtype)
+        if tuple(v.shape) != (t, layer.top_k):
+            raise ValueError(f"{name} must be [{t}, {layer.top_k}], got {list(v.shape)}")
+    ws = _workspace(layer.workspace_size(t), x.device, ws)
+    _same_device(x, out=out, ids=ids, weights=weights, ws=ws)
+    with torch.cuda.device(x.device):
+        _check(lib.mm_moe_f32(layer._ref, x.data_ptr(), out.data_ptr(), ids.data_ptr(), weights.data_ptr(), t,
+                              _ptr(ws), 0 if ws is None else ws.numel(), _stream(x)), "mm_moe_f32")
+    return out, ids, weights
 
 
 def q4_0_init(x: torch.Tensor, n: int, ws: torch.Tensor | None = None) -> torch.Tensor:

@@ -206,6 +206,24 @@ int repack(const void* src, void* dst, int64_t N, int64_t K, bool to_repacked, v
                         : launch_unpack_q4_0((const uint8_t*)src, (uint8_t*)dst, N, K, s));
 }
 
+// Product with e4m3 weights: src1 as f32 (x) or as codes and scales (a, asc).
+int f8_product(const void* src0, const float* scale0, const float* x, const void* a,
+               const float* asc, float* dst, int64_t M, int64_t N, int64_t K, void* ws,
+               size_t ws_bytes, void* stream, bool given) {
+  F8Plan p;
+  int st = make_f8_plan(M, N, K, given, &p);
+  if (st != MM_OK) return st;
+  st = validate_f8(src0, scale0, given ? a : (const void*)x, asc, dst, M, N, K, given, ws, ws_bytes, p);
+  if (st != MM_OK) return st;
+  if (p.kind == F8_NONE) return MM_OK;
+  st = check_device();
+  if (st != MM_OK) return st;
+  hipStream_t s = (hipStream_t)stream;
+  if (p.kind == F8_ZERO) return hip_status(launch_zero(dst, M * N, s));
+  return hip_status(launch_f8_product(p, (const uint8_t*)src0, scale0, x, (const uint8_t*)a, asc,
+                                      dst, (int)M, (int)N, (int)K, ws, s));
+}
+
 }  // namespace
 
 // Status codes travel as int inside the library; the C entry points return
@@ -277,6 +295,36 @@ mm_status mm_mul_mat_f16_f32(const uint16_t* src0, const float* src1, float* dst
                              int64_t N, int64_t K, void* ws, size_t ws_bytes, void* stream) {
   return as_status(
       mul_mat(MM_TYPE_F16, src0, src1, dst, nullptr, M, N, K, 0, 0, 0, ws, ws_bytes, stream));
+}
+
+mm_status mm_quantize_f8(const float* x, void* codes, float* scales, int64_t nrows, int64_t k,
+                         int block_rows, void* stream) {
+  int st = validate_f8_quantize(x, codes, scales, nrows, k, block_rows);
+  if (st != MM_OK || nrows == 0 || k == 0) return as_status(st);
+  st = check_device();
+  if (st != MM_OK) return as_status(st);
+  return as_status(hip_status(
+      launch_f8_quantize(x, (uint8_t*)codes, scales, nrows, k, block_rows, (hipStream_t)stream)));
+}
+
+mm_status mm_mul_mat_f8_f32(const void* src0, const float* scale0, const float* src1, float* dst,
+                            int64_t M, int64_t N, int64_t K, void* ws, size_t ws_bytes,
+                            void* stream) {
+  return as_status(f8_product(src0, scale0, src1, nullptr, nullptr, dst, M, N, K, ws, ws_bytes,
+                              stream, false));
+}
+
+mm_status mm_mul_mat_f8_f8(const void* src0, const float* scale0, const void* src1,
+                           const float* scale1, float* dst, int64_t M, int64_t N, int64_t K,
+                           void* ws, size_t ws_bytes, void* stream) {
+  return as_status(f8_product(src0, scale0, nullptr, src1, scale1, dst, M, N, K, ws, ws_bytes,
+                              stream, true));
+}
+
+size_t mm_mul_mat_f8_workspace_size(int64_t M, int64_t N, int64_t K, int src1_quantized) {
+  F8Plan p;
+  if (make_f8_plan(M, N, K, src1_quantized != 0, &p) != MM_OK) return 0;
+  return p.ws_bytes;
 }
 
 mm_status mm_mul_mat_f32(const float* src0, const float* src1, float* dst,
@@ -354,7 +402,78 @@ int group_plan(int count, const int64_t* Ns, int64_t M, int64_t K, Plan* whole, 
   return MM_OK;
 }
 
+// Bytes of one of the layer's matrices (all experts), and of its scales.
+size_t moe_matrix_bytes(const mm_moe_layer& l, int64_t rows, int64_t K) {
+  return (size_t)l.E * (size_t)(l.type == MM_TYPE_Q4_0R ? repacked_bytes(rows, K)
+                                                        : rows * row_bytes(l.type, K));
+}
+size_t moe_scale_bytes(const mm_moe_layer& l, int64_t rows, int64_t K) {
+  if (l.type != MM_TYPE_F8) return 0;
+  return (size_t)l.E * (size_t)((rows + kF8Block - 1) / kF8Block) *
+         (size_t)((K + kF8Block - 1) / kF8Block) * 4;
+}
+
 }  // namespace
+
+size_t mm_moe_workspace_size(const mm_moe_layer* layer, int64_t T) {
+  MoePlan p;
+  if (!layer || make_moe_plan(layer->type, T, layer->D, layer->F, layer->E, layer->top_k, &p) != MM_OK)
+    return 0;
+  return p.ws_bytes;
+}
+
+mm_status mm_moe_f32(const mm_moe_layer* layer, const float* x, float* dst, int32_t* ids,
+                     float* weights, int64_t T, void* ws, size_t ws_bytes, void* stream) {
+  if (!layer) return MM_ERR_NULL;
+  const mm_moe_layer& l = *layer;
+  MoePlan p;
+  int st = make_moe_plan(l.type, T, l.D, l.F, l.E, l.top_k, &p);
+  if (st != MM_OK) return as_status(st);
+  if (T == 0) return MM_OK;
+  const bool f8 = l.type == MM_TYPE_F8;
+  if (!x || !dst || !l.router || !l.gate || !l.up || !l.down) return MM_ERR_NULL;
+  if (f8 && (!l.gate_scale || !l.up_scale || !l.down_scale)) return MM_ERR_NULL;
+  const auto off = [](const void* v, uintptr_t a) { return (uintptr_t)v % a != 0; };
+  if (off(x, 16) || off(l.router, 16) || off(l.gate, 16) || off(l.up, 16) || off(l.down, 16) ||
+      off(dst, 4) || off(ids, 4) || off(weights, 4))
+    return MM_ERR_ALIGN;
+  if (f8 && (off(l.gate_scale, 4) || off(l.up_scale, 4) || off(l.down_scale, 4))) return MM_ERR_ALIGN;
+  if (!ws || ws_bytes < p.ws_bytes) return MM_ERR_WORKSPACE;
+  if (off(ws, 256)) return MM_ERR_ALIGN;
+  const size_t xb = (size_t)(T * l.D) * 4, kb = (size_t)(T * l.top_k) * 4;
+  const struct { const void* p; size_t n; } in[8] = {
+      {x, xb}, {l.router, (size_t)(l.E * l.D) * 4},
+      {l.gate, moe_matrix_bytes(l, l.F, l.D)}, {l.up, moe_matrix_bytes(l, l.F, l.D)},
+      {l.down, moe_matrix_bytes(l, l.D, l.F)},
+      {f8 ? l.gate_scale : nullptr, moe_scale_bytes(l, l.F, l.D)},
+      {f8 ? l.up_scale : nullptr, moe_scale_bytes(l, l.F, l.D)},
+      {f8 ? l.down_scale : nullptr, moe_scale_bytes(l, l.D, l.F)}};
+  const struct { const void* p; size_t n; } out[4] = {
+      {dst, xb}, {ids, kb}, {weights, kb}, {ws, p.ws_bytes}};
+  for (int i = 0; i < 4; ++i) {
+    for (const auto& v : in)
+      if (ranges_overlap(out[i].p, out[i].n, v.p, v.n)) return MM_ERR_ALIAS;
+    for (int j = 0; j < i; ++j)
+      if (ranges_overlap(out[i].p, out[i].n, out[j].p, out[j].n)) return MM_ERR_ALIAS;
+  }
+  st = check_device();
+  if (st != MM_OK) return as_status(st);
+  uint8_t* const b = (uint8_t*)ws;
+  MoeArgs a;
+  a.x = x;
+  a.router = l.router;
+  a.gate = (const uint8_t*)l.gate; a.up = (const uint8_t*)l.up; a.down = (const uint8_t*)l.down;
+  a.gate_scale = l.gate_scale; a.up_scale = l.up_scale; a.down_scale = l.down_scale;
+  a.dst = dst;
+  a.logits = (double*)(b + p.off_logits);
+  a.ids = ids ? ids : (int*)(b + p.off_ids);
+  a.weights = weights ? weights : (float*)(b + p.off_weights);
+  a.xp = b + p.off_xp; a.xs = (float*)(b + p.off_xs);
+  a.hp = b + p.off_hp; a.hs = (float*)(b + p.off_hs);
+  a.T = (int)T; a.D = (int)l.D; a.F = (int)l.F; a.E = (int)l.E;
+  a.top_k = l.top_k; a.norm = l.norm != 0;
+  return as_status(hip_status(launch_moe(l.type, a, (hipStream_t)stream)));
+}
 
 size_t mm_mul_mat_q4_0_group_workspace_size(int count, const int64_t* Ns, int64_t M, int64_t K) {
   Plan p;
@@ -436,6 +555,7 @@ mm_status mm_mul_mat_q4_0_f32_group(int count, const void* const* src0s, float* 
 }
 
 size_t mm_mul_mat_workspace_size(int type, int64_t M, int64_t N, int64_t K) {
+  if (type == MM_TYPE_F8) return mm_mul_mat_f8_workspace_size(M, N, K, 0);
   Plan p;
   if (make_plan(type, M, N, K, 0, &p) != MM_OK) return 0;
   return p.ws_bytes;

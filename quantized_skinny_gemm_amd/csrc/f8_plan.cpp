@@ -1,0 +1,133 @@
+// Host-only plan, workspace layout and argument checks of the e4m3 (F8)
+// quantizer and product.
+#include <stdint.h>
+
+#include "../../include/mm.h"
+#include "plan.h"
+
+namespace qsg {
+
+namespace {
+
+constexpr int64_t kMaxDim = 0x7fffffff;
+constexpr int64_t kMaxTiles = 1 << 23;       // workgroups x 256 threads stay below 2^32
+
+size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+bool overlaps(const void* a, size_t na, const void* b, size_t nb) {
+  if (!a || !b || na == 0 || nb == 0) return false;
+  const uintptr_t a0 = (uintptr_t)a, b0 = (uintptr_t)b;
+  return a0 < b0 + nb && b0 < a0 + na;
+}
+
+}  // namespace
+
+int make_f8_plan(int64_t M, int64_t N, int64_t K, bool given, F8Plan* p) {
+  *p = F8Plan();
+  if (M < 0 || N < 0 || K < 0 || M > kMaxDim || N > kMaxDim || K > kF8MaxK || K % kQK)
+    return MM_ERR_SHAPE;
+  if (M == 0 || N == 0) return MM_OK;
+  if (K == 0) { p->kind = F8_ZERO; return MM_OK; }
+  const int64_t nkb = ceil_div(K, kF8Block);
+
+  // src1 codes and scales (INIT), unless the caller gives them or the kernel
+  // quantizes src1 itself
+  const size_t fused_lds = (size_t)M * (size_t)nkb * (kF8Block + 4);
+  if (!given && M <= 4 && fused_lds <= (size_t)kF8FusedMaxLds) {
+    p->kind = F8_FUSED;
+    p->nt = 1;
+    p->rt = 1;
+    p->waves = 8;
+    while (p->waves > 1 && p->waves > nkb) p->waves /= 2;
+    p->grid_n = ceil_div(N, 16 * p->rt);
+    const size_t join = (size_t)p->waves * 1024 * p->rt;
+    p->lds = align_up(fused_lds > join ? fused_lds : join, 16);
+    return MM_OK;
+  }
+  size_t off = 0;
+  if (!given) {
+    p->off_a = off; off = align_up(off + (size_t)M * (size_t)K, 256);
+    p->off_as = off; off = align_up(off + (size_t)M * (size_t)nkb * 4, 256);
+  }
+  if (M <= 64) {
+    p->kind = F8_SKINNY;
+    p->nt = M <= 16 ? 1 : M <= 32 ? 2 : 4;
+    p->rt = 1;
+    p->waves = 8;
+    while (p->waves > 1 && p->waves > nkb) p->waves /= 2;
+    p->grid_n = ceil_div(N, 16 * p->rt);
+    p->grid_m = ceil_div(M, 16 * p->nt);
+    p->lds = (size_t)p->waves * 1024 * p->rt * p->nt;
+  } else {
+    p->kind = F8_WIDE;
+    p->bm = 128;
+    p->bn = 256;
+    p->tiles_m = ceil_div(M, p->bm);
+    p->tiles_n = ceil_div(N, p->bn);
+    const int64_t tiles = p->tiles_m * p->tiles_n;
+    if (tiles > kMaxTiles) return MM_ERR_SHAPE;
+    int64_t split = 1;
+    if (tiles < kCUs) {
+      split = kCUs / tiles;
+      if (split > nkb / 4) split = nkb / 4;
+      if (split > 16) split = 16;
+      if (split < 1) split = 1;
+    }
+    p->kchunk = ceil_div(nkb, split);
+    p->split = (int)ceil_div(nkb, p->kchunk);
+    if (p->split > 1) {
+      p->off_part = off;
+      off = align_up(off + (size_t)p->split * (size_t)M * (size_t)N * 4, 256);
+    }
+  }
+  p->ws_bytes = off;
+  return MM_OK;
+}
+
+int validate_f8(const void* src0, const void* scale0, const void* src1, const void* scale1,
+                const void* dst, int64_t M, int64_t N, int64_t K, bool given, const void* ws,
+                size_t ws_bytes, const F8Plan& p) {
+  if (p.kind == F8_NONE) return MM_OK;
+  if (!dst) return MM_ERR_NULL;
+  if ((uintptr_t)dst % 4) return MM_ERR_ALIGN;
+  if (K == 0) return MM_OK;
+  if (!src0 || !scale0 || !src1 || (given && !scale1)) return MM_ERR_NULL;
+  if ((uintptr_t)src0 % 16 || (uintptr_t)scale0 % 4 || (uintptr_t)src1 % 16 ||
+      (given && (uintptr_t)scale1 % 4))
+    return MM_ERR_ALIGN;
+  if (p.ws_bytes > 0) {
+    if (!ws || ws_bytes < p.ws_bytes) return MM_ERR_WORKSPACE;
+    if ((uintptr_t)ws % 256) return MM_ERR_ALIGN;
+  }
+  const size_t nkb = (size_t)ceil_div(K, kF8Block);
+  const struct { const void* p; size_t n; } in[4] = {
+      {src0, (size_t)N * (size_t)K},
+      {scale0, (size_t)ceil_div(N, kF8Block) * nkb * 4},
+      {src1, (size_t)M * (size_t)K * (given ? 1 : 4)},
+      {given ? scale1 : nullptr, (size_t)M * nkb * 4}};
+  const size_t db = (size_t)M * (size_t)N * 4;
+  for (const auto& i : in)
+    if (overlaps(dst, db, i.p, i.n) || (p.ws_bytes > 0 && overlaps(ws, p.ws_bytes, i.p, i.n)))
+      return MM_ERR_ALIAS;
+  if (p.ws_bytes > 0 && overlaps(ws, p.ws_bytes, dst, db)) return MM_ERR_ALIAS;
+  return MM_OK;
+}
+
+int validate_f8_quantize(const void* x, const void* codes, const void* scales, int64_t nrows,
+                         int64_t k, int block_rows) {
+  if (block_rows != 1 && block_rows != kF8Block) return MM_ERR_ARG;
+  if (nrows < 0 || k < 0 || nrows > kMaxDim || k > kF8MaxK || k % kQK) return MM_ERR_SHAPE;
+  if (nrows == 0 || k == 0) return MM_OK;
+  const int64_t nkb = ceil_div(k, kF8Block), nrb = ceil_div(nrows, block_rows);
+  if (block_rows != 1 && nrb * nkb > kMaxTiles) return MM_ERR_SHAPE;
+  if (!x || !codes || !scales) return MM_ERR_NULL;
+  if ((uintptr_t)x % 16 || (uintptr_t)codes % 16 || (uintptr_t)scales % 4) return MM_ERR_ALIGN;
+  const size_t xb = (size_t)nrows * (size_t)k * 4, cb = (size_t)nrows * (size_t)k;
+  const size_t sb = (size_t)nrb * (size_t)nkb * 4;
+  if (overlaps(x, xb, codes, cb) || overlaps(x, xb, scales, sb) || overlaps(codes, cb, scales, sb))
+    return MM_ERR_ALIAS;
+  return MM_OK;
+}
+
+}  // namespace qsg

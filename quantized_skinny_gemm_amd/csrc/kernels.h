@@ -90,6 +90,33 @@ hipError_t launch_f16_wide(const Plan& p, const uint16_t* w, const float* x, flo
 bool f_mma_ok(int type, const void* w, const float* x, int64_t K);
 hipError_t launch_f_mma(const Plan& p, int type, const void* w, const float* x, float* dst, int M,
                         int N, int K, hipStream_t s);
+// e4m3 quantizer: codes [nrows][k], scales [ceil(nrows/block_rows)][ceil(k/128)],
+// block_rows 1 or 128.
+hipError_t launch_f8_quantize(const float* x, uint8_t* codes, float* scales, int64_t nrows,
+                              int64_t k, int block_rows, hipStream_t s);
+// Product with e4m3 weights; x != NULL: src1 as f32 (a, asc unused), else as
+// codes a and scales asc.
+hipError_t launch_f8_product(const F8Plan& p, const uint8_t* w, const float* wsc, const float* x,
+                             const uint8_t* a, const float* asc, float* dst, int M, int N, int K,
+                             void* ws, hipStream_t s);
+// Mixture-of-experts layer; the pointers after `dst` lie in the workspace
+// (ids and weights possibly in the caller's arrays).
+struct MoeArgs {
+  const float* x;                    // [T][D]
+  const float* router;               // [E][D]
+  const uint8_t *gate, *up, *down;   // [E][F][D], [E][F][D], [E][D][F] in `type`
+  const float *gate_scale, *up_scale, *down_scale;   // F8: [E][ceil(rows/128)][ceil(K/128)]
+  float* dst;                        // [T][D]
+  double* logits;                    // [T][E]
+  int* ids;                          // [T][top_k]
+  float* weights;                    // [T][top_k]
+  uint8_t* xp;                       // split x: [T][D/32] blocks of 128 bytes
+  float* xs;                         // [T][D/32]
+  uint8_t* hp;                       // split h: [T][top_k][F/32] blocks
+  float* hs;                         // [T][top_k][F/32]
+  int T, D, F, E, top_k, norm;
+};
+hipError_t launch_moe(int type, const MoeArgs& a, hipStream_t s);
 hipError_t launch_zero(float* dst, int64_t n, hipStream_t s);
 // dst[i] = sum over z = 0..split-1, in that order, of part[z * n + i].
 hipError_t launch_splitk_reduce(const float* part, float* dst, int64_t n, int split, hipStream_t s);

@@ -1,0 +1,40 @@
+// Host-only checks and workspace layout of the mixture-of-experts layer.
+#include <stdint.h>
+
+#include "../../include/mm.h"
+#include "plan.h"
+
+namespace qsg {
+
+namespace {
+
+size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
+
+}  // namespace
+
+int make_moe_plan(int type, int64_t T, int64_t D, int64_t F, int64_t E, int64_t top_k, MoePlan* p) {
+  *p = MoePlan();
+  if (type != MM_TYPE_Q4_0R && type != MM_TYPE_F8 && type != MM_TYPE_F16) return MM_ERR_ARG;
+  if (T < 0 || T > kMoeMaxTokens || D < 1 || D > kMoeMaxDim || D % kQK || F < 1 || F > kMoeMaxDim ||
+      F % kQK || E < 1 || E > kMoeMaxExperts || top_k < 1 || top_k > kMoeMaxTopK || top_k > E)
+    return MM_ERR_SHAPE;
+  if (T == 0) return MM_OK;
+  size_t off = 0;
+  const auto take = [&off](size_t bytes) {
+    const size_t at = off;
+    off = align_up(off + bytes, 256);
+    return at;
+  };
+  const size_t slots = (size_t)(T * top_k);
+  p->off_logits = take((size_t)(T * E) * 8);
+  p->off_ids = take(slots * 4);
+  p->off_weights = take(slots * 4);
+  p->off_xp = take((size_t)(T * D) * 4);
+  p->off_xs = take((size_t)(T * D / kQK) * 4);
+  p->off_hp = take(slots * (size_t)F * 4);
+  p->off_hs = take(slots * (size_t)(F / kQK) * 4);
+  p->ws_bytes = off;
+  return MM_OK;
+}
+
+}  // namespace qsg

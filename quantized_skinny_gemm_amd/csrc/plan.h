@@ -31,6 +31,14 @@ constexpr int kMmaMaxM = 32;       // largest M the skinny MFMA kernel takes by 
 constexpr int kSkinnyPairs = 4;    // skinny kernel: block pairs per wave phase
 constexpr int64_t kFMmaMaxK = 1 << 23;  // skinny F kernel: 32-bit buffer offsets over 32 rows
 constexpr int64_t kMaxGridY = 65535; // documented limit of a grid's y dimension (workgroups)
+constexpr int64_t kMaxGridX = 1 << 20; // workgroups of the grid-stride F8 quantizer
+constexpr int kF8Block = 128;      // values per scale of the e4m3 type, along K and (weights) N
+constexpr int64_t kF8MaxK = 1 << 23;   // F8 kernels: 32-bit byte offsets over a tile's rows
+constexpr int kMoeMaxTokens = 128;     // mixture-of-experts layer: tokens per call,
+constexpr int kMoeMaxExperts = 512;    // experts,
+constexpr int kMoeMaxTopK = 16;        // experts per token,
+constexpr int64_t kMoeMaxDim = 1 << 20;  // model and hidden width
+constexpr int kF8FusedMaxLds = 65536;  // LDS bytes the fused F8 kernel may stage src1 codes in
 constexpr size_t kNoAllocScratchBytes = (size_t)64 << 20;  // mm_mul_mat_q4_0_f32_noalloc's array
 constexpr int kMmaWaves = 8;       // waves per workgroup of the skinny kernel for unaligned
                                    // weights or K % 64 != 0 (32 rows per workgroup)
@@ -118,6 +126,39 @@ int validate_mul_mat(int type, const void* src0, const void* src1, const void* d
 int validate_quantize(int out_type, const void* x, const void* y, int64_t nrows, int64_t k);
 
 int64_t row_bytes(int type, int64_t K);
+
+// Plan of the product with e4m3 weights (f8.hip).
+enum F8Kind { F8_NONE = 0, F8_ZERO = 1, F8_FUSED = 2, F8_SKINNY = 3, F8_WIDE = 4 };
+
+struct F8Plan {
+  int kind = F8_NONE;
+  int nt = 1, rt = 1;          // skinny, fused: tiles of 16 src1 / weight rows per wave
+  int waves = 8;               // skinny, fused: waves per workgroup (they split K)
+  int64_t grid_n = 1, grid_m = 1;
+  size_t lds = 0;              // skinny, fused: LDS bytes
+  int bm = 0, bn = 0;          // wide: output tile (src1 rows, weight rows)
+  int64_t tiles_m = 1, tiles_n = 1, kchunk = 0;   // wide: K blocks per split
+  int split = 1;
+  size_t off_a = 0, off_as = 0, off_part = 0;     // workspace: src1 codes, scales, partials
+  size_t ws_bytes = 0;
+};
+
+// given: src1 comes as codes and scales (no INIT).
+int make_f8_plan(int64_t M, int64_t N, int64_t K, bool given, F8Plan* p);
+
+int validate_f8(const void* src0, const void* scale0, const void* src1, const void* scale1,
+                const void* dst, int64_t M, int64_t N, int64_t K, bool given, const void* ws,
+                size_t ws_bytes, const F8Plan& p);
+
+int validate_f8_quantize(const void* x, const void* codes, const void* scales, int64_t nrows,
+                         int64_t k, int block_rows);
+
+// Plan of the mixture-of-experts layer (moe.hip): workspace layout only.
+struct MoePlan {
+  size_t off_logits = 0, off_ids = 0, off_weights = 0, off_xp = 0, off_xs = 0, off_hp = 0, off_hs = 0;
+  size_t ws_bytes = 0;
+};
+int make_moe_plan(int type, int64_t T, int64_t D, int64_t F, int64_t E, int64_t top_k, MoePlan* p);
 
 // Bytes of N x K Q4_0 weights in the repacked layout (repack.hip): tiles of
 // 16 rows x phases of 8 blocks, padded; -1 for an invalid shape.

@@ -1,0 +1,133 @@
+"""Host-side checks of the e4m3 and mixture-of-experts entry points: arguments are refused before any HIP call
+(the pointers here are never dereferenced), workspace sizes, the binding's own checks."""
+from __future__ import annotations
+
+import ctypes
+
+import pytest
+
+import quantized_skinny_gemm_amd as qs
+
+OK, NULL, SHAPE, ALIGN, WS, ALIAS, ARG = 0, -1, -2, -3, -4, -5, -8
+W, WSC, X, XSC, DST, WSP = (0x7f0000000000 + (i << 36) for i in range(6))
+G = 1 << 30
+
+
+def _f32(m=4, n=256, k=512, w=W, wsc=WSC, x=X, dst=DST, ws=WSP, wsb=None):
+    wsb = qs.f8_workspace_size(m, n, k) if wsb is None else wsb
+    return qs.lib.mm_mul_mat_f8_f32(w, wsc, x, dst, m, n, k, ws, wsb, None)
+
+
+def _f8(m=4, n=256, k=512, w=W, wsc=WSC, x=X, xsc=XSC, dst=DST, ws=WSP, wsb=None):
+    wsb = qs.f8_workspace_size(m, n, k, True) if wsb is None else wsb
+    return qs.lib.mm_mul_mat_f8_f8(w, wsc, x, xsc, dst, m, n, k, ws, wsb, None)
+
+
+def test_type_and_sizes():
+    assert qs.MM_TYPE_F8 == 5
+    assert qs.row_bytes(qs.MM_TYPE_F8, 4096) == 4096
+    assert qs.row_bytes(qs.MM_TYPE_F8, 48) == -1
+    assert qs.workspace_size(qs.MM_TYPE_F8, 100, 300, 512) == qs.f8_workspace_size(100, 300, 512)
+    # src1 as codes needs no more than src1 as f32
+    for m, n, k in ((1, 4096, 4096), (16, 14336, 4096), (128, 4096, 14336), (512, 14336, 4096)):
+        assert qs.f8_workspace_size(m, n, k, True) <= qs.f8_workspace_size(m, n, k)
+    assert qs.f8_workspace_size(-1, 4, 32) == 0 and qs.f8_workspace_size(1, 4, 33) == 0
+    # the type has entry points of its own
+    assert qs.lib.mm_dispatch(qs.MM_TYPE_F8, 1, 64, 64, None) == ARG
+    assert qs.lib.mm_debug_mul_mat(qs.MM_TYPE_F8, W, X, DST, None, 1, 64, 64, 0, 0, 0, None, 0, None) == ARG
+
+
+@pytest.mark.parametrize("call", [_f32, _f8])
+def test_product_refusals(call):
+    for bad in (dict(k=48), dict(m=-1), dict(n=-1), dict(k=-32), dict(n=2 ** 31), dict(m=2 ** 31), dict(k=2 ** 23 + 32)):
+        assert call(**{**dict(wsb=0), **bad}) == SHAPE, bad
+    for p in ("w", "wsc", "x", "dst"):
+        assert call(**{p: None}) == NULL, p
+    assert call(w=W + 8) == ALIGN and call(wsc=WSC + 2) == ALIGN and call(x=X + 4) == ALIGN and call(dst=DST + 2) == ALIGN
+    assert call(dst=W + 4096) == ALIAS and call(dst=X) == ALIAS and call(dst=WSC) == ALIAS
+    # empty products look at no pointer
+    assert call(m=0, w=None, x=None, dst=None, wsb=0) == OK and call(n=0, w=None, dst=None, wsb=0) == OK
+
+
+def test_product_workspace_refusals():
+    m, n, k = 100, 256, 4096
+    need = qs.f8_workspace_size(m, n, k)
+    assert need >= m * k + 4 * m * 32
+    assert _f32(m, n, k, wsb=need - 1) == WS and _f32(m, n, k, ws=None) == WS
+    assert _f32(m, n, k, ws=WSP + 64) == ALIGN
+    for p in (W, WSC, X, DST):
+        assert _f32(m, n, k, ws=p) == ALIAS
+    assert _f8(m, n, k, xsc=None) == NULL and _f8(m, n, k, xsc=XSC + 1) == ALIGN
+    assert _f8(m, n, k, dst=XSC) == ALIAS
+
+
+def test_quantize_refusals():
+    q = qs.lib.mm_quantize_f8
+    assert q(X, W, WSC, 4, 64, 2, None) == ARG
+    assert q(X, W, WSC, 4, 48, 1, None) == SHAPE and q(X, W, WSC, -1, 64, 1, None) == SHAPE
+    assert q(X, W, WSC, 4, 2 ** 23 + 32, 128, None) == SHAPE
+    for i in range(3):
+        p = [X, W, WSC]
+        p[i] = None
+        assert q(*p, 4, 64, 1, None) == NULL
+    assert q(X + 4, W, WSC, 4, 64, 1, None) == ALIGN and q(X, W + 8, WSC, 4, 64, 1, None) == ALIGN
+    assert q(X, W, WSC + 2, 4, 64, 128, None) == ALIGN
+    assert q(X, X + 256, WSC, 4, 64, 1, None) == ALIAS and q(X, W, X + 16, 4, 64, 1, None) == ALIAS
+    assert q(X, W, W, 4, 64, 1, None) == ALIAS
+    assert q(None, None, None, 0, 64, 1, None) == OK and q(None, None, None, 3, 0, 128, None) == OK
+
+
+class _L(qs._MoeStruct):
+    pass
+
+
+def _layer(**kw):
+    base = dict(type=qs.MM_TYPE_F8, top_k=2, norm=1, D=256, F=128, E=4, router=X + 8 * G, gate=W, up=W + G, down=W + 2 * G,
+                gate_scale=WSC, up_scale=WSC + G, down_scale=WSC + 2 * G)
+    base.update(kw)
+    return qs._MoeStruct(**base)
+
+
+def _moe(layer, t=3, x=X, dst=DST, ids=None, weights=None, ws=WSP, wsb=None):
+    wsb = qs.lib.mm_moe_workspace_size(ctypes.byref(layer), t) if wsb is None else wsb
+    return qs.lib.mm_moe_f32(ctypes.byref(layer), x, dst, ids, weights, t, ws, wsb, None)
+
+
+def test_moe_refusals():
+    assert qs.lib.mm_moe_f32(None, X, DST, None, None, 1, WSP, 0, None) == NULL
+    assert qs.lib.mm_moe_workspace_size(None, 1) == 0
+    for t in (qs.MM_TYPE_F32, qs.MM_TYPE_Q4_0, qs.MM_TYPE_Q8_0, 99):
+        assert _moe(_layer(type=t)) == ARG
+    for bad in (dict(D=48), dict(F=48), dict(D=0), dict(F=0), dict(E=0), dict(E=513), dict(top_k=0), dict(top_k=5),
+                dict(top_k=17, E=64), dict(D=2 ** 20 + 32), dict(F=2 ** 20 + 32)):
+        assert _moe(_layer(**bad)) == SHAPE, bad
+    assert _moe(_layer(), t=129) == SHAPE and _moe(_layer(), t=-1) == SHAPE
+    assert _moe(_layer(), t=0, x=None, dst=None, ws=None) == OK
+    for p in ("router", "gate", "up", "down", "gate_scale", "up_scale", "down_scale"):
+        assert _moe(_layer(**{p: None})) == NULL, p
+    assert _moe(_layer(), x=None) == NULL and _moe(_layer(), dst=None) == NULL
+    for p in ("router", "gate", "up", "down"):
+        assert _moe(_layer(**{p: getattr(_layer(), p) + 8})) == ALIGN, p
+    assert _moe(_layer(gate_scale=WSC + 2)) == ALIGN
+    assert _moe(_layer(), x=X + 4) == ALIGN and _moe(_layer(), dst=DST + 1) == ALIGN
+    assert _moe(_layer(), ids=DST + G + 2) == ALIGN and _moe(_layer(), ws=WSP + 64) == ALIGN
+    need = qs.lib.mm_moe_workspace_size(ctypes.byref(_layer()), 3)
+    assert _moe(_layer(), wsb=need - 1) == WS and _moe(_layer(), ws=None) == WS
+
+
+def test_moe_aliasing():
+    x_bytes, k_bytes = 3 * 256 * 4, 3 * 2 * 4
+    for dst in (X + x_bytes - 4, W, W + G, W + 2 * G, WSC, WSC + G, WSC + 2 * G, X + 8 * G, WSP):
+        assert _moe(_layer(), dst=dst) == ALIAS
+    assert _moe(_layer(), ids=DST + 4) == ALIAS and _moe(_layer(), weights=X) == ALIAS
+    assert _moe(_layer(), ids=DST + G, weights=DST + G + k_bytes - 4) == ALIAS
+    assert _moe(_layer(), ws=DST) == ALIAS and _moe(_layer(), ws=W) == ALIAS
+
+
+def test_binding_refuses_cpu_tensors_and_wrong_shapes():
+    import torch
+    x = torch.zeros((2, 64))
+    for f in (lambda: qs.quantize_f8(x), lambda: qs.mul_mat_f8_f32(x, x, x), lambda: qs.mul_mat_f8_f8(x, x, x, x),
+              lambda: qs.MoeLayer(qs.MM_TYPE_F16, x, x, x, x, 32, 1)):
+        with pytest.raises(TypeError):
+            f()

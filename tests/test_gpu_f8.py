@@ -1,0 +1,221 @@
+"""GPU parity of the e4m3 type: quantizer bytes and scales equal the oracle's, products within the bound
+that the operations' roundings allow and within the normwise bound of the quantized kinds."""
+from __future__ import annotations
+
+import numpy as np
+import pytest
+
+from oracle import f8
+from tests.gpu_util import TOL_Q4_0, assert_close, say, to_dev, to_host
+
+pytestmark = pytest.mark.gpu
+
+
+def _qs():
+    import quantized_skinny_gemm_amd as qs
+    return qs
+
+
+def _bytes(t):
+    import torch
+    return to_host(t.view(torch.uint8))
+
+
+def _act(rng, m, k):
+    x = rng.standard_normal((m, k)).astype(np.float32)
+    x[:, rng.random(k) < 0.02] *= 20
+    return x
+
+
+def _weights(rng, n, k):
+    return (rng.standard_normal((n, k)) * 0.02).astype(np.float32)
+
+
+def bound(mag, k):
+    """|error| of one output: a block's sum of at most 128 exact products, each addition off by at most one fp32
+    step of the magnitudes' sum (2^-23, which also covers truncation), the scale product, the fma of each
+    block, the join of at most 16 waves and 16 slices."""
+    return (128 + 2 * (-(-k // 128)) + 32) * 2.0 ** -23 * mag
+
+
+def check(y, w, ws, a, a_s, what):
+    ref, mag = f8.mul_mat(w, ws, a, a_s)
+    err = np.abs(y - ref)
+    assert np.all(err <= bound(mag, w.shape[1])), f"{what}: {np.max(err / np.maximum(mag, 1e-300)):.3e} of the terms' sum"
+    assert_close(y, ref, TOL_Q4_0, what)
+
+
+@pytest.mark.parametrize("rows,k", [(1, 32), (1, 4096), (3, 160), (5, 224), (37, 4128), (130, 128), (257, 288)])
+@pytest.mark.parametrize("r", [1, 128])
+def test_quantize_equals_oracle(rows, k, r):
+    qs = _qs()
+    say("quantize_f8", rows, k, r)
+    x = _act(np.random.default_rng(rows * 1000 + k), rows, k)
+    x[0, :min(k, 128)] = 0
+    codes, scales = qs.quantize_f8(to_dev(x), r)
+    wc, wsc = f8.quantize(x, r)
+    assert np.array_equal(to_host(scales), wsc)
+    assert np.array_equal(_bytes(codes), wc)
+
+
+def test_quantize_edge_values():
+    """Zero, subnormal, largest and non-finite blocks, every tie between two codes."""
+    qs = _qs()
+    say("quantize_f8 edges")
+    x = np.zeros((8, 160), np.float32)
+    x[1] = 2.0 ** -140
+    x[2] = np.float32(3e38) * np.linspace(-1, 1, 160).astype(np.float32)
+    x[3, 5] = np.inf
+    x[3, 6] = 2
+    x[4, 7] = np.nan
+    x[4, 8] = -5
+    x[5, :126] = f8._MID.astype(np.float32)[:126]         # 448 sets d = 1 below
+    x[5, 126] = 448
+    x[6] = -x[5]
+    x[7] = np.float32(2.0 ** -126) * np.arange(160)
+    codes, scales = qs.quantize_f8(to_dev(x), 1)
+    wc, wsc = f8.quantize(x, 1)
+    assert np.array_equal(to_host(scales), wsc)
+    got = _bytes(codes)
+    nan = wc & 0x7f == 0x7f
+    assert np.array_equal(got & 0x7f == 0x7f, nan) and np.array_equal(got[~nan], wc[~nan])
+
+
+# every src1 tile of the skinny kernels, the fused kernel's rows, both sides of the wide kernel's threshold,
+# ragged N, K ending inside a block, one block, one row
+@pytest.mark.parametrize("m,n,k", [
+    (1, 4096, 4096), (1, 1, 32), (1, 17, 96), (2, 300, 4128), (4, 129, 256), (5, 1000, 4128), (16, 257, 1024),
+    (17, 130, 2080), (32, 64, 4096), (33, 48, 160), (64, 333, 1056), (65, 129, 128), (100, 515, 2080),
+    (128, 256, 14336), (129, 257, 288), (300, 700, 1184), (512, 1024, 4096), (1, 40, 131072), (4, 40, 131072),
+])
+def test_products(m, n, k):
+    qs = _qs()
+    say("f8", m, n, k)
+    rng = np.random.default_rng(m * 1_000_003 + n * 17 + k)
+    w, ws = f8.quantize(_weights(rng, n, k), 128)
+    x = _act(rng, m, k)
+    a, a_s = f8.quantize(x, 1)
+    wd, wsd = to_dev(w), to_dev(ws)
+    y = to_host(qs.mul_mat_f8_f32(wd, wsd, to_dev(x)))
+    check(y, w, ws, a, a_s, f"f8_f32 {m}x{n}x{k}")
+    y8 = to_host(qs.mul_mat_f8_f8(wd, wsd, to_dev(a), to_dev(a_s)))
+    check(y8, w, ws, a, a_s, f"f8_f8 {m}x{n}x{k}")
+
+
+@pytest.mark.parametrize("m", [1, 3, 16, 40, 130])
+def test_rows_do_not_depend_on_their_batch_and_nan_stays_in_its_row(m):
+    """A src1 row with a NaN, one with an infinity: their outputs are NaN, every other row's finite; weight rows
+    past N and src1 rows past M are not read into results: dst behind the last row stays as it was."""
+    import torch
+    qs = _qs()
+    say("f8 nan rows", m)
+    rng = np.random.default_rng(m)
+    n, k = 200, 416
+    w, ws = f8.quantize(_weights(rng, n, k), 128)
+    x = _act(rng, m, k)
+    x[0, 3] = np.nan
+    if m > 2:
+        x[2, 400] = np.inf
+    buf = torch.full((m + 2, n), 7.0, device="cuda")
+    y = to_host(qs.mul_mat_f8_f32(to_dev(w), to_dev(ws), to_dev(x), out=buf[:m]))
+    bad = [0, 2] if m > 2 else [0]
+    good = [i for i in range(m) if i not in bad]
+    assert np.isnan(y[bad]).all() and np.isfinite(y[good]).all()
+    assert bool((buf[m:] == 7.0).all())
+    if good:
+        a, a_s = f8.quantize(x[good], 1)
+        check(y[good], w, ws, a, a_s, f"good rows of {m}")
+
+
+@pytest.mark.parametrize("m", [1, 16, 64, 130])
+def test_nan_weight_reaches_its_column_only(m):
+    qs = _qs()
+    say("f8 nan weight", m)
+    rng = np.random.default_rng(m + 50)
+    n, k = 300, 288
+    w, ws = f8.quantize(_weights(rng, n, k), 128)
+    w[77, 280] = 0x7f
+    w[150, 1] = 0xff
+    y = to_host(qs.mul_mat_f8_f32(to_dev(w), to_dev(ws), to_dev(_act(rng, m, k))))
+    cols = np.isnan(y).any(axis=0)
+    assert np.isnan(y[:, [77, 150]]).all() and cols.sum() == 2
+
+
+@pytest.mark.parametrize("m,n,k", [(1, 4096, 4096), (16, 1000, 4096), (64, 4096, 1024), (128, 4096, 14336)])
+def test_graph_replays_and_a_second_stream_give_the_eager_bits(m, n, k):
+    """Captured and replayed three times with eager work in between, and run on two streams with workspaces of
+    their own: the same bits every time."""
+    import torch
+    qs = _qs()
+    say("f8 graph", m, n, k)
+    rng = np.random.default_rng(m + n)
+    w, ws = (to_dev(v) for v in f8.quantize(_weights(rng, n, k), 128))
+    x = to_dev(_act(rng, m, k))
+    nbytes = max(qs.f8_workspace_size(m, n, k), 1)
+    want = qs.mul_mat_f8_f32(w, ws, x)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    out, wsp = torch.empty_like(want), torch.empty(nbytes, dtype=torch.uint8, device="cuda")
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):
+        qs.mul_mat_f8_f32(w, ws, x, out=out, ws=wsp)
+    for rep in range(3):
+        out.fill_(float("nan"))
+        other = qs.mul_mat_f8_f32(w, ws, x * 2)
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want), f"replay {rep}"
+    assert torch.isfinite(other).all()
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    got = []
+    torch.cuda.synchronize()
+    for st in (s1, s2):
+        with torch.cuda.stream(st):
+            got.append([qs.mul_mat_f8_f32(w, ws, x) for _ in range(4)])
+    torch.cuda.synchronize()
+    for ys in got:
+        for y in ys:
+            assert torch.equal(y, want)
+
+
+@pytest.mark.parametrize("m", [2, 20, 200])
+def test_unaligned_dst_and_k_zero(m):
+    import torch
+    qs = _qs()
+    say("f8 dst off 16", m)
+    rng = np.random.default_rng(m)
+    n, k = 264, 512
+    w, ws = f8.quantize(_weights(rng, n, k), 128)
+    x = _act(rng, m, k)
+    a, a_s = f8.quantize(x, 1)
+    buf = torch.full((m * n + 2,), 7.0, device="cuda")
+    out = buf[1:-1].view(m, n)                                # 4-byte aligned only
+    y = to_host(qs.mul_mat_f8_f32(to_dev(w), to_dev(ws), to_dev(x), out=out))
+    check(y, w, ws, a, a_s, "dst off 16")
+    assert float(buf[0]) == 7.0 and float(buf[-1]) == 7.0
+    z = qs.mul_mat_f8_f32(torch.empty((n, 0), dtype=torch.uint8, device="cuda"), torch.empty((3, 0), device="cuda"),
+                          torch.empty((m, 0), device="cuda"), out=out)
+    assert not to_host(z).any()
+
+
+def test_large_weights_past_4_gib():
+    """Weight bytes past 2^32: sampled rows against the oracle."""
+    import torch
+    qs = _qs()
+    n, k = 1_100_000, 4096
+    say("f8 large", n, k)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(1)
+    w = torch.randint(0, 0x7f, (n, k), dtype=torch.uint8, device="cuda", generator=g)
+    ws = torch.rand((-(-n // 128), k // 128), device="cuda", generator=g) * 1e-3
+    rows = np.r_[0:4, 524286:524290, 1048574:1048578, n - 4:n]
+    for m in (1, 16, 70):
+        x = torch.randn((m, k), device="cuda", generator=g)
+        y = to_host(qs.mul_mat_f8_f32(w, ws, x)[:, rows])
+        a, a_s = f8.quantize(to_host(x), 1)
+        wv = np.stack([f8.VALUES[to_host(w[int(r)])] * np.repeat(to_host(ws[int(r) // 128]).astype(np.float64), 128) for r in rows])
+        av = f8.dequantize(a, a_s, 1)
+        err = np.abs(y - av @ wv.T)
+        assert np.all(err <= bound(np.abs(av) @ np.abs(wv).T, k)), m

@@ -1,0 +1,216 @@
+"""GPU parity of the mixture-of-experts layer against the float64 oracle: chosen experts equal, weights and dst
+within the bound that its roundings allow."""
+from __future__ import annotations
+
+import numpy as np
+import pytest
+
+from oracle import codec, f8, moe
+from tests.gpu_util import say, to_dev, to_host
+
+pytestmark = pytest.mark.gpu
+
+ACT_EPS = 2.0 ** -21      # 22 significant bits relative to the block, with the power of two's slack
+
+
+def sum_eps(k):
+    """Sum of k exact products in fp32: 32 per block and its two parts, each addition off by at most one step
+    (2^-23), a scale product and an fma per block, the join of 8 waves."""
+    return (64 + 2 * (k // 32) + 16) * 2.0 ** -23
+
+
+def _qs():
+    import quantized_skinny_gemm_amd as qs
+    return qs
+
+
+class Layer:
+    def __init__(self, kind, t, d, f, e, top_k, seed, norm=True):
+        import torch
+        qs = _qs()
+        rng = np.random.default_rng(seed)
+        self.kind, self.top_k, self.norm = kind, top_k, norm
+        self.x = rng.standard_normal((t, d)).astype(np.float32)
+        self.x[:, rng.random(d) < 0.02] *= 10
+        self.router = (rng.standard_normal((e, d)) / np.sqrt(d)).astype(np.float32)
+        self.values, dev, scales = [], [], []
+        for n, k in ((f, d), (f, d), (d, f)):
+            w = (rng.standard_normal((e, n, k)) * 0.05).astype(np.float32)
+            if kind == "q4_0r":
+                q = [codec.quantize_q4_0(v) for v in w]
+                self.values.append(np.stack([codec.dequantize_q4_0(v, k) for v in q]).astype(np.float64))
+                dev.append(torch.stack([qs.repack_q4_0(to_dev(v), k) for v in q]))
+                scales.append(None)
+            elif kind == "f8":
+                q = [f8.quantize(v, 128) for v in w]
+                self.values.append(np.stack([f8.dequantize(c, s, 128) for c, s in q]))
+                dev.append(to_dev(np.stack([c for c, _ in q])))
+                scales.append(to_dev(np.stack([s for _, s in q])))
+            else:
+                self.values.append(w.astype(np.float16).astype(np.float64))
+                dev.append(to_dev(w.astype(np.float16)))
+                scales.append(None)
+        code = {"q4_0r": qs.MM_TYPE_Q4_0R, "f8": qs.MM_TYPE_F8, "f16": qs.MM_TYPE_F16}[kind]
+        self.dev = dev
+        self.layer = qs.MoeLayer(code, to_dev(self.router), *dev, f, top_k, *scales, norm=norm)
+
+    def oracle(self, x=None):
+        x = self.x if x is None else x
+        d, f = self.values[0].shape[2], self.values[0].shape[1]
+        return moe.layer(x, self.router, *self.values, self.top_k, self.norm, ACT_EPS, sum_eps(max(d, f)))
+
+    def check(self, got, x=None, what=""):
+        dst, ids, w = (to_host(v) for v in got)
+        rd, ri, rw, err = self.oracle(x)
+        assert np.array_equal(ids, ri), what
+        assert np.all(np.abs(w - rw) <= 2.0 ** -20 * rw), what
+        assert np.all(np.abs(dst - rd) <= err), f"{what}: {np.max(np.abs(dst - rd) / err):.3g} of the bound"
+        # and no more than the fp32 sums' own noise in the mean
+        assert np.linalg.norm(dst - rd) <= 3e-6 * np.linalg.norm(rd), what
+
+
+KINDS = ["q4_0r", "f8", "f16"]
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("t,d,f,e,top_k", [
+    (1, 256, 128, 4, 2), (1, 32, 32, 1, 1), (1, 2080, 1056, 12, 3), (2, 288, 160, 5, 5), (7, 416, 96, 12, 3),
+    (16, 512, 256, 8, 2), (17, 256, 288, 3, 1), (33, 160, 64, 40, 8), (64, 128, 96, 2, 2), (100, 96, 128, 16, 4),
+    (128, 64, 32, 512, 16),
+])
+def test_layer(kind, t, d, f, e, top_k):
+    say("moe", kind, t, d, f, e, top_k)
+    m = Layer(kind, t, d, f, e, top_k, t * 100 + d + f + e)
+    qs = _qs()
+    m.check(qs.moe_f32(m.layer, to_dev(m.x)), what=f"{kind} T={t} D={d} F={f} E={e} k={top_k}")
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_probabilities_without_normalisation(kind):
+    say("moe no norm", kind)
+    m = Layer(kind, 5, 256, 96, 10, 3, 77, norm=False)
+    m.check(_qs().moe_f32(m.layer, to_dev(m.x)), what=kind)
+
+
+def test_ties_take_the_lower_index():
+    import torch
+    qs = _qs()
+    say("moe ties")
+    m = Layer("f16", 3, 64, 32, 70, 4, 5)
+    m.router[:] = 0
+    m.router[33] = m.router[65] = m.router[69] = m.x[0] * 0.01
+    m.layer = qs.MoeLayer(qs.MM_TYPE_F16, to_dev(m.router), *m.dev, 32, 4)
+    _, ids, _ = qs.moe_f32(m.layer, to_dev(m.x))
+    assert to_host(ids)[0].tolist() == [33, 65, 69, 0]
+    _, ri, _, _ = m.oracle()
+    assert np.array_equal(to_host(ids), ri)
+    assert ids.dtype == torch.int32
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_all_tokens_on_one_expert_and_scale_range(kind):
+    """128 tokens that all take the same two experts (several passes of 16), activations from 2^-30 to 2^12."""
+    say("moe one expert", kind)
+    qs = _qs()
+    m = Layer(kind, 128, 96, 64, 9, 2, 31)
+    m.x = np.abs(m.x) * (2.0 ** np.linspace(-30, 6, 128))[:, None].astype(np.float32)
+    m.router = np.abs(m.router)
+    m.router[4] += 1
+    m.router[7] += 2
+    m.layer = qs.MoeLayer(m.layer.struct.type, to_dev(m.router), *m.dev, 64, 2, *m.layer.tensors[4:])
+    got = qs.moe_f32(m.layer, to_dev(m.x.astype(np.float32)))
+    assert np.array_equal(to_host(got[1])[-1], [7, 4])
+    dst, ids, _ = (to_host(v) for v in got)
+    rd, ri, _, err = m.oracle()
+    assert np.array_equal(ids, ri) and np.all(np.abs(dst - rd) <= err)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("t", [3, 40])
+def test_non_finite_values_stay_in_their_token(kind, t):
+    """A NaN token, an infinite token, and a NaN in a weight of one expert: NaN for the tokens concerned, the other
+    rows as the oracle has them; ids stay valid."""
+    import torch
+    say("moe nan", kind, t)
+    qs = _qs()
+    m = Layer(kind, t, 160, 96, 6, 2, 91)
+    x = m.x.copy()
+    x[0, 3] = np.nan
+    x[1, 100] = np.inf
+    dst, ids, w = qs.moe_f32(m.layer, to_dev(x))
+    y, i = to_host(dst), to_host(ids)
+    assert np.isnan(y[:2]).all() and np.isfinite(y[2:]).all()
+    assert ((i >= 0) & (i < 6)).all()
+    rd, ri, _, err = m.oracle()
+    assert np.all(np.abs(y[2:] - rd[2:]) <= err[2:])
+    if kind != "q4_0r":
+        bad = int(ri[2, 0])
+        m.dev[2][bad].view(torch.uint8)[5].fill_(0x7f)          # row 5 of down: NaN in both types
+        y = to_host(qs.moe_f32(m.layer, to_dev(m.x))[0])
+        uses = (ri == bad).any(axis=1)
+        assert np.isnan(y[uses][:, 5]).all()
+        ok = np.ones_like(y, bool)
+        ok[uses, 5] = False
+        assert np.isfinite(y[ok]).all() and np.all(np.abs(y - rd)[ok] <= err[ok])
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("t", [1, 20])
+def test_graph_streams_and_rows_behind_the_batch(kind, t):
+    """Replays of a captured call with eager work between them, two streams with their own workspaces, out-buffers
+    longer than the batch: the same bits, and nothing else written."""
+    import torch
+    say("moe graph", kind, t)
+    qs = _qs()
+    m = Layer(kind, t, 256, 160, 8, 3, 13)
+    x = to_dev(m.x)
+    want = [v.clone() for v in qs.moe_f32(m.layer, x)]
+    m.check(want, what="eager")
+    buf = torch.full((t + 1, 256), 7.0, device="cuda")
+    ids = torch.full((t + 1, 3), -5, dtype=torch.int32, device="cuda")
+    w = torch.full((t + 1, 3), 7.0, device="cuda")
+    ws = torch.full((m.layer.workspace_size(t),), 0xff, dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):
+        qs.moe_f32(m.layer, x, out=buf[:t], ids=ids[:t], weights=w[:t], ws=ws)
+    for rep in range(3):
+        buf[:t] = float("nan")
+        ws.fill_(0xff)
+        qs.moe_f32(m.layer, x * 3)
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(buf[:t], want[0]) and torch.equal(ids[:t], want[1]) and torch.equal(w[:t], want[2]), rep
+    assert bool((buf[t] == 7).all()) and bool((ids[t] == -5).all()) and bool((w[t] == 7).all())
+    got = []
+    for st in (torch.cuda.Stream(), torch.cuda.Stream()):
+        st.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(st):
+            got.append([qs.moe_f32(m.layer, x)[0] for _ in range(4)])
+    torch.cuda.synchronize()
+    assert all(torch.equal(y, want[0]) for ys in got for y in ys)
+
+
+def test_decode_step_quantize_project_route_and_project_again():
+    """The operators as a decode step uses them: projections with e4m3 weights on an activation quantized once,
+    the layer with e4m3 experts, the output projection; against the float64 composition."""
+    say("decode step f8")
+    qs = _qs()
+    rng = np.random.default_rng(8)
+    m = Layer("f8", 4, 256, 160, 8, 2, 21)
+    wq, wqs = f8.quantize((rng.standard_normal((256, 256)) * 0.06).astype(np.float32), 128)
+    wo, wos = f8.quantize((rng.standard_normal((500, 256)) * 0.06).astype(np.float32), 128)
+    a, a_s = qs.quantize_f8(to_dev(m.x), 1)
+    q = qs.mul_mat_f8_f8(to_dev(wq), to_dev(wqs), a, a_s)
+    x1 = to_host(q)
+    y, ids, w = qs.moe_f32(m.layer, q)
+    m.check((y, ids, w), x=x1, what="layer in the step")
+    logits = to_host(qs.mul_mat_f8_f32(to_dev(wo), to_dev(wos), y))
+    b, b_s = f8.quantize(to_host(y), 1)
+    ref, mag = f8.mul_mat(wo, wos, b, b_s)
+    assert np.all(np.abs(logits - ref) <= (128 + 4 + 32) * 2.0 ** -23 * mag)
+    ra, ras = f8.quantize(m.x, 1)
+    ref, mag = f8.mul_mat(wq, wqs, ra, ras)
+    assert np.all(np.abs(x1 - ref) <= (128 + 4 + 32) * 2.0 ** -23 * mag)
