@@ -19,6 +19,7 @@ there is no CPU fallback.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -280,6 +281,41 @@ def mul_mat_f32(w: torch.Tensor, x: torch.Tensor, out=None, ws=None) -> torch.Te
     return _mul_mat(lib.mm_mul_mat_f32, MM_TYPE_F32, w, x, out, ws, "mm_mul_mat_f32")
 
 
+# ---- e4m3 products and the mixture-of-experts layer: calls of a few microseconds, so their checks are
+# plain attribute comparisons, and sizes that only depend on the shape are computed once
+
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_F8_DTYPES = (torch.float8_e4m3fn, torch.uint8)
+
+
+def _launch(fn, what: str, dev: int, *args) -> None:
+    """fn(*args, current stream of device dev), with dev current during the call."""
+    if dev == torch.cuda.current_device():
+        status = fn(*args, _raw_stream(dev))
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, _raw_stream(dev))
+    if status != 0:
+        raise MMError(status, what)
+
+
+def _on(t, name: str, shape, dtypes, dev: int) -> None:
+    """t is a contiguous GPU tensor of this shape, one of dtypes, on device dev."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a GPU (HIP) tensor")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must be {dtypes[0]}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{dev}")
+
+
+_F32 = (torch.float32,)
+
+
 def _ceil128(v: int) -> int:
     return (v + 127) // 128
 
@@ -289,50 +325,47 @@ def quantize_f8(x: torch.Tensor, block_rows: int = 1, out=None):
     [ceil(rows / block_rows), ceil(K / 128)]); block_rows 1 (activations) or 128 (weights)."""
     x = _dev(x, "x", torch.float32)
     rows, k = x.shape
+    nb = rows if block_rows == 1 else _ceil128(rows)
+    dev = x.get_device()
     if out is None:
-        nb = rows if block_rows == 1 else _ceil128(rows)
-        out = (torch.empty((rows, k), dtype=torch.float8_e4m3fn, device=x.device),
-               torch.empty((nb, _ceil128(k)), dtype=torch.float32, device=x.device))
+        codes = torch.empty((rows, k), dtype=torch.float8_e4m3fn, device=x.device)
+        scales = torch.empty((nb, _ceil128(k)), dtype=torch.float32, device=x.device)
     else:
-        _f8(out[0], out[1], rows, k, 1 if block_rows == 1 else 128, "out")
-    codes, scales = out
-    _same_device(x, codes=codes, scales=scales)
-    with torch.cuda.device(x.device):
-        _check(lib.mm_quantize_f8(x.data_ptr(), codes.data_ptr(), scales.data_ptr(), rows, k, block_rows,
-                                  _stream(x)), "mm_quantize_f8")
+        codes, scales = out
+        _on(codes, "out codes", (rows, k), _F8_DTYPES, dev)
+        _on(scales, "out scales", (nb, _ceil128(k)), _F32, dev)
+    _launch(lib.mm_quantize_f8, "mm_quantize_f8", dev, x.data_ptr(), codes.data_ptr(), scales.data_ptr(),
+            rows, k, block_rows)
     return codes, scales
 
 
-def _f8(codes, scales, rows, k, block_rows, name):
-    """Checks one e4m3 operand: codes [rows, k] (float8_e4m3fn or uint8) and its scales."""
-    _dev(codes, name)
-    _dev(scales, f"{name} scales", torch.float32)
-    if codes.dtype not in (torch.float8_e4m3fn, torch.uint8):
-        raise TypeError(f"{name} must be float8_e4m3fn or uint8, got {codes.dtype}")
-    if tuple(codes.shape) != (rows, k):
-        raise ValueError(f"{name} must be [{rows}, {k}], got {list(codes.shape)}")
-    if tuple(scales.shape) != ((rows + block_rows - 1) // block_rows, _ceil128(k)):
-        raise ValueError(f"{name} scales must be [ceil({rows} / {block_rows}), ceil({k} / 128)], "
-                         f"got {list(scales.shape)}")
-
-
+@functools.lru_cache(maxsize=4096)
 def f8_workspace_size(m: int, n: int, k: int, src1_quantized: bool = False) -> int:
     return int(lib.mm_mul_mat_f8_workspace_size(int(m), int(n), int(k), int(src1_quantized)))
 
 
-def _same_device(x, **others):
-    for name, t in others.items():
-        if t is not None and t.device != x.device:
-            raise ValueError(f"{name} is on {t.device}, expected {x.device}")
+def _f8_weights(w, w_scale, k: int, dev: int) -> int:
+    if not isinstance(w, torch.Tensor) or w.dim() != 2:
+        raise TypeError("w must be a 2-d GPU (HIP) tensor")
+    n = w.shape[0]
+    _on(w, "w", (n, k), _F8_DTYPES, dev)
+    _on(w_scale, "w_scale", (_ceil128(n), _ceil128(k)), _F32, dev)
+    return n
 
 
-def _out(out, m, n, device):
+def _buffers(m, n, device, dev, out, need, ws):
+    """out (allocated if None, checked otherwise) and the workspace with its size."""
     if out is None:
-        return torch.empty((m, n), dtype=torch.float32, device=device)
-    _dev(out, "out", torch.float32)
-    if tuple(out.shape) != (m, n):
-        raise ValueError(f"out must be [{m}, {n}], got {list(out.shape)}")
-    return out
+        out = torch.empty((m, n), dtype=torch.float32, device=device)
+    else:
+        _on(out, "out", (m, n), _F32, dev)
+    if need == 0:
+        return out, None, 0
+    if ws is None or ws.numel() < need:
+        ws = torch.empty(need, dtype=torch.uint8, device=device)
+    elif not ws.is_cuda or ws.get_device() != dev or ws.dtype != torch.uint8 or not ws.is_contiguous():
+        raise ValueError(f"ws must be a contiguous uint8 tensor on cuda:{dev}")
+    return out, ws, ws.numel()
 
 
 def mul_mat_f8_f32(w: torch.Tensor, w_scale: torch.Tensor, x: torch.Tensor, out=None, ws=None) -> torch.Tensor:
@@ -340,15 +373,11 @@ def mul_mat_f8_f32(w: torch.Tensor, w_scale: torch.Tensor, x: torch.Tensor, out=
     x float32 [M, K], quantized within (one scale per row and 128 values)."""
     x = _dev(x, "x", torch.float32)
     m, k = x.shape
-    n = w.shape[0]
-    _f8(w, w_scale, n, k, 128, "w")
-    out = _out(out, m, n, x.device)
-    ws = _workspace(f8_workspace_size(m, n, k, False), x.device, ws)
-    _same_device(x, w=w, w_scale=w_scale, out=out, ws=ws)
-    with torch.cuda.device(x.device):
-        _check(lib.mm_mul_mat_f8_f32(w.data_ptr(), w_scale.data_ptr(), x.data_ptr(), out.data_ptr(), m, n, k,
-                                     _ptr(ws), 0 if ws is None else ws.numel(), _stream(x)),
-               "mm_mul_mat_f8_f32")
+    dev = x.get_device()
+    n = _f8_weights(w, w_scale, k, dev)
+    out, ws, nbytes = _buffers(m, n, x.device, dev, out, f8_workspace_size(m, n, k, False), ws)
+    _launch(lib.mm_mul_mat_f8_f32, "mm_mul_mat_f8_f32", dev, w.data_ptr(), w_scale.data_ptr(), x.data_ptr(),
+            out.data_ptr(), m, n, k, None if ws is None else ws.data_ptr(), nbytes)
     return out
 
 
@@ -358,16 +387,13 @@ def mul_mat_f8_f8(w: torch.Tensor, w_scale: torch.Tensor, a: torch.Tensor, a_sca
     (quantize_f8 with block_rows 1)."""
     a = _dev(a, "a")
     m, k = a.shape
-    n = w.shape[0]
-    _f8(w, w_scale, n, k, 128, "w")
-    _f8(a, a_scale, m, k, 1, "a")
-    out = _out(out, m, n, a.device)
-    ws = _workspace(f8_workspace_size(m, n, k, True), a.device, ws)
-    _same_device(a, w=w, w_scale=w_scale, a_scale=a_scale, out=out, ws=ws)
-    with torch.cuda.device(a.device):
-        _check(lib.mm_mul_mat_f8_f8(w.data_ptr(), w_scale.data_ptr(), a.data_ptr(), a_scale.data_ptr(),
-                                    out.data_ptr(), m, n, k, _ptr(ws), 0 if ws is None else ws.numel(),
-                                    _stream(a)), "mm_mul_mat_f8_f8")
+    dev = a.get_device()
+    _on(a, "a", (m, k), _F8_DTYPES, dev)
+    _on(a_scale, "a_scale", (m, _ceil128(k)), _F32, dev)
+    n = _f8_weights(w, w_scale, k, dev)
+    out, ws, nbytes = _buffers(m, n, a.device, dev, out, f8_workspace_size(m, n, k, True), ws)
+    _launch(lib.mm_mul_mat_f8_f8, "mm_mul_mat_f8_f8", dev, w.data_ptr(), w_scale.data_ptr(), a.data_ptr(),
+            a_scale.data_ptr(), out.data_ptr(), m, n, k, None if ws is None else ws.data_ptr(), nbytes)
     return out
 
 
@@ -390,55 +416,51 @@ class MoeLayer:
         _dev(router, "router", torch.float32)
         e, d = router.shape
         f, top_k = int(f), int(top_k)
-        dtypes = {MM_TYPE_Q4_0R: (torch.uint8,), MM_TYPE_F8: (torch.float8_e4m3fn, torch.uint8),
-                  MM_TYPE_F16: (torch.float16,)}
+        dev = router.get_device()
+        dtypes = {MM_TYPE_Q4_0R: (torch.uint8,), MM_TYPE_F8: _F8_DTYPES, MM_TYPE_F16: (torch.float16,)}
         if mm_type not in dtypes:
             raise ValueError("mm_type must be MM_TYPE_Q4_0R, MM_TYPE_F8 or MM_TYPE_F16")
         scales = {"gate": gate_scale, "up": up_scale, "down": down_scale}
         for name, w, rows, k in (("gate", gate, f, d), ("up", up, f, d), ("down", down, d, f)):
-            _dev(w, name)
-            if w.dtype not in dtypes[mm_type]:
-                raise TypeError(f"{name} must be {dtypes[mm_type][0]}, got {w.dtype}")
-            shape = (e, repacked_bytes(rows, k)) if mm_type == MM_TYPE_Q4_0R else (e, rows, k)
-            if tuple(w.shape) != shape:
-                raise ValueError(f"{name} must be {list(shape)}, got {list(w.shape)}")
-            _same_device(router, **{name: w})
+            _on(w, name, (e, repacked_bytes(rows, k)) if mm_type == MM_TYPE_Q4_0R else (e, rows, k),
+                dtypes[mm_type], dev)
             if mm_type == MM_TYPE_F8:
-                s = _dev(scales[name], f"{name}_scale", torch.float32)
-                if tuple(s.shape) != (e, _ceil128(rows), _ceil128(k)):
-                    raise ValueError(f"{name}_scale must be [{e}, {_ceil128(rows)}, {_ceil128(k)}], got {list(s.shape)}")
-                _same_device(router, **{f"{name}_scale": s})
+                _on(scales[name], f"{name}_scale", (e, _ceil128(rows), _ceil128(k)), _F32, dev)
             else:
                 scales[name] = None
-        self.device, self.d, self.f, self.e, self.top_k = router.device, d, f, e, top_k
+        self.dev, self.device, self.d, self.f, self.e, self.top_k = dev, router.device, d, f, e, top_k
         self.tensors = (router, gate, up, down, *scales.values())
         self.struct = _MoeStruct(mm_type, top_k, int(bool(norm)), d, f, e, *(_ptr(t) for t in self.tensors))
         self._ref = ctypes.byref(self.struct)
+        self._sizes = {}
 
     def workspace_size(self, t: int) -> int:
-        return int(lib.mm_moe_workspace_size(self._ref, int(t)))
+        """Bytes of workspace for t tokens (0: t is out of range, or the layer's sizes are)."""
+        if t not in self._sizes:
+            self._sizes[t] = int(lib.mm_moe_workspace_size(self._ref, int(t)))
+        return self._sizes[t]
+
+
+_I32 = (torch.int32,)
 
 
 def moe_f32(layer: MoeLayer, x: torch.Tensor, out=None, ids=None, weights=None, ws=None):
     """(dst [T, D], ids int32 [T, top_k], weights [T, top_k]) of the layer on x float32 [T, D]."""
     x = _dev(x, "x", torch.float32)
-    t, d = x.shape
-    if d != layer.d or x.device != layer.device:
-        raise ValueError(f"x must be [T, {layer.d}] on {layer.device}, got {list(x.shape)} on {x.device}")
-    out = _out(out, t, d, x.device)
+    t = x.shape[0]
+    dev, k = layer.dev, layer.top_k
+    _on(x, "x", (t, layer.d), _F32, dev)
     if ids is None:
-        ids = torch.empty((t, layer.top_k), dtype=torch.int32, device=x.device)
+        ids = torch.empty((t, k), dtype=torch.int32, device=layer.device)
+    else:
+        _on(ids, "ids", (t, k), _I32, dev)
     if weights is None:
-        weights = torch.empty((t, layer.top_k), dtype=torch.float32, device=x.device)
-    for name, v, dtype in (("ids", ids, torch.int32), ("weights", weights, torch.float32)):
-        _dev(v, name, dtype)
-        if tuple(v.shape) != (t, layer.top_k):
-            raise ValueError(f"{name} must be [{t}, {layer.top_k}], got {list(v.shape)}")
-    ws = _workspace(layer.workspace_size(t), x.device, ws)
-    _same_device(x, out=out, ids=ids, weights=weights, ws=ws)
-    with torch.cuda.device(x.device):
-        _check(lib.mm_moe_f32(layer._ref, x.data_ptr(), out.data_ptr(), ids.data_ptr(), weights.data_ptr(), t,
-                              _ptr(ws), 0 if ws is None else ws.numel(), _stream(x)), "mm_moe_f32")
+        weights = torch.empty((t, k), dtype=torch.float32, device=layer.device)
+    else:
+        _on(weights, "weights", (t, k), _F32, dev)
+    out, ws, nbytes = _buffers(t, layer.d, layer.device, dev, out, layer.workspace_size(t), ws)
+    _launch(lib.mm_moe_f32, "mm_moe_f32", dev, layer._ref, x.data_ptr(), out.data_ptr(), ids.data_ptr(),
+            weights.data_ptr(), t, None if ws is None else ws.data_ptr(), nbytes)
     return out, ids, weights
 
 

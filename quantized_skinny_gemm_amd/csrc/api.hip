@@ -472,7 +472,8 @@ mm_status mm_moe_f32(const mm_moe_layer* layer, const float* x, float* dst, int3
   a.hp = b + p.off_hp; a.hs = (float*)(b + p.off_hs);
   a.T = (int)T; a.D = (int)l.D; a.F = (int)l.F; a.E = (int)l.E;
   a.top_k = l.top_k; a.norm = l.norm != 0;
-  return as_status(hip_status(launch_moe(l.type, a, (hipStream_t)stream)));
+  a.fold = p.fold;
+  return as_status(hip_status(launch_moe(l.type, p, a, (float*)(b + p.off_part), (hipStream_t)stream)));
 }
 
 size_t mm_mul_mat_q4_0_group_workspace_size(int count, const int64_t* Ns, int64_t M, int64_t K) {

@@ -111,12 +111,14 @@ struct MoeArgs {
   int* ids;                          // [T][top_k]
   float* weights;                    // [T][top_k]
   uint8_t* xp;                       // split x: [T][D/32] blocks of 128 bytes
-  float* xs;                         // [T][D/32]
+  float* xs;                         // [T][D/32 rounded up to 4]
   uint8_t* hp;                       // split h: [T][top_k][F/32] blocks
-  float* hs;                         // [T][top_k][F/32]
+  float* hs;                         // [T][top_k][F/32 rounded up to 4]
   int T, D, F, E, top_k, norm;
+  int fold;                          // the selection is made by the gate / up launch
 };
-hipError_t launch_moe(int type, const MoeArgs& a, hipStream_t s);
+// part: slices of dst ([p.slices][T][D]; unused with one slice).
+hipError_t launch_moe(int type, const MoePlan& p, const MoeArgs& a, float* part, hipStream_t s);
 hipError_t launch_zero(float* dst, int64_t n, hipStream_t s);
 // dst[i] = sum over z = 0..split-1, in that order, of part[z * n + i].
 hipError_t launch_splitk_reduce(const float* part, float* dst, int64_t n, int split, hipStream_t s);

@@ -30,9 +30,25 @@ int make_moe_plan(int type, int64_t T, int64_t D, int64_t F, int64_t E, int64_t 
   p->off_ids = take(slots * 4);
   p->off_weights = take(slots * 4);
   p->off_xp = take((size_t)(T * D) * 4);
-  p->off_xs = take((size_t)(T * D / kQK) * 4);
+  p->off_xs = take((size_t)T * align_up((size_t)(D / kQK), 4) * 4);
   p->off_hp = take(slots * (size_t)F * 4);
-  p->off_hs = take(slots * (size_t)(F / kQK) * 4);
+  p->off_hs = take(slots * align_up((size_t)(F / kQK), 4) * 4);
+  // The selection costs each workgroup of the next launch about T E^2 / 512
+  // steps per thread where it makes it itself.
+  p->fold = T * E * E <= 65536;
+  // Down: 16 rows per workgroup while an expert serves few tokens; with more,
+  // 64 rows share each activation load (activations are 4 bytes a value, the
+  // weights as few as half a byte) and the sequence of (expert, unit) pairs
+  // is cut in slices to fill the device.
+  const int64_t used = T * top_k < E ? T * top_k : E;
+  const bool many = T * top_k > 2 * used;
+  const bool few = T <= kMoeFewTokens;
+  p->rt = few ? 1 : many && D % 64 == 0 && T <= 64 ? 4 : many && D % 32 == 0 ? 2 : 1;
+  const int64_t tiles = D / (16 * p->rt), units = used * ((F / kQK + 3) / 4);
+  int64_t slices = few ? 1 : p->rt > 1 ? (2 * kCUs + tiles - 1) / tiles : kCUs / tiles;
+  if (slices > units / 64) slices = units / 64;
+  p->slices = (int)(slices < 1 ? 1 : slices > 8 ? 8 : slices);
+  if (p->slices > 1) p->off_part = take((size_t)p->slices * (size_t)(T * D) * 4);
   p->ws_bytes = off;
   return MM_OK;
 }

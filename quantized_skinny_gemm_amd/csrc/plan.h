@@ -153,9 +153,14 @@ int validate_f8(const void* src0, const void* scale0, const void* src1, const vo
 int validate_f8_quantize(const void* x, const void* codes, const void* scales, int64_t nrows,
                          int64_t k, int block_rows);
 
-// Plan of the mixture-of-experts layer (moe.hip): workspace layout only.
+// Plan of the mixture-of-experts layer (moe.hip).
+constexpr int kMoeFewTokens = 4;      // up to this many tokens: kernels for passes of 4
+constexpr int kMoeMaxSums = 131072;    // LDS bytes of the down product's per-wave sums
 struct MoePlan {
+  bool fold = false;       // the selection is made by the gate / up launch
+  int rt = 1, slices = 1;  // down: 16-row tiles per workgroup, workgroups sharing a tile's sum
   size_t off_logits = 0, off_ids = 0, off_weights = 0, off_xp = 0, off_xs = 0, off_hp = 0, off_hs = 0;
+  size_t off_part = 0;
   size_t ws_bytes = 0;
 };
 int make_moe_plan(int type, int64_t T, int64_t D, int64_t F, int64_t E, int64_t top_k, MoePlan* p);
