@@ -73,6 +73,15 @@ __device__ __forceinline__ uint2 f8_row_block(const float4& a, const float4& b, 
   return make_uint2(f8_pack4(a.x, a.y, a.z, a.w, id), f8_pack4(b.x, b.y, b.z, b.w, id));
 }
 
+// Eight e4m3 codes as binary16 (exact; a NaN code becomes a NaN).
+__device__ __forceinline__ v8h widen(uint32_t lo, uint32_t hi) {
+  const v2h a = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.0f, false);
+  const v2h b = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.0f, true);
+  const v2h c = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.0f, false);
+  const v2h d = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.0f, true);
+  return (v8h){a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+}
+
 // ---------------------------------------------------------------- quantizer
 
 // 1 x 128 blocks: 16 lanes per block, one 32-byte load and one 8-byte store
@@ -95,6 +104,43 @@ __global__ __launch_bounds__(256) void k_f8_quantize_rows(const float* __restric
     const uint2 c = f8_row_block(a, b, d);
     if (k < K) *reinterpret_cast<uint2*>(codes + row * K + k) = c;
     if (i == 0) scales[blk] = d;
+  }
+}
+
+// The same codes as binary16 values for the tiled product, rows padded with
+// zeros to whole blocks.
+__global__ __launch_bounds__(256) void k_f8_quantize_rows_f16(const float* __restrict__ x,
+                                                              uint16_t* __restrict__ values,
+                                                              float* __restrict__ scales, int K,
+                                                              int nkb, int64_t nblocks) {
+  const int i = threadIdx.x & 15;
+  for (int64_t blk = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4); blk < nblocks;
+       blk += (int64_t)gridDim.x * 16) {
+    const int64_t row = blk / nkb;
+    const int k = (int)(blk - row * nkb) * kBlk + 8 * i;
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
+    if (k < K) {
+      const float4* p = reinterpret_cast<const float4*>(x + row * K + k);
+      a = p[0]; b = p[1];
+    }
+    float d;
+    const uint2 c = f8_row_block(a, b, d);
+    *reinterpret_cast<v8h*>(values + blk * kBlk + 8 * i) = widen(c.x, c.y);
+    if (i == 0) scales[blk] = d;
+  }
+}
+
+// Codes given by the caller in that form, 16 per thread.
+__global__ __launch_bounds__(256) void k_f8_widen(const uint8_t* __restrict__ codes,
+                                                  uint16_t* __restrict__ values, int K, int nkb,
+                                                  int64_t pieces) {
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < pieces; i += 256 * (int64_t)gridDim.x) {
+    const int64_t row = i / (8 * nkb);
+    const int k = (int)(i - row * 8 * nkb) * 16;
+    const uint4 c = k < K ? *reinterpret_cast<const uint4*>(codes + row * K + k) : make_uint4(0, 0, 0, 0);
+    v8h* const p = reinterpret_cast<v8h*>(values + 16 * i);
+    p[0] = widen(c.x, c.y);
+    p[1] = widen(c.z, c.w);
   }
 }
 
@@ -140,15 +186,6 @@ __global__ __launch_bounds__(256) void k_f8_quantize_tiles(const float* __restri
 
 // ---------------------------------------------------------------- product, few src1 rows
 
-// Eight e4m3 codes as binary16 (exact; a NaN code becomes a NaN).
-__device__ __forceinline__ v8h widen(uint32_t lo, uint32_t hi) {
-  const v2h a = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.0f, false);
-  const v2h b = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.0f, true);
-  const v2h c = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.0f, false);
-  const v2h d = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.0f, true);
-  return (v8h){a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
-}
-
 // A lane's two 16-byte pieces of block kb of a row; pieces past K are zero
 // (both operands' are: an e4m3 NaN times zero is not zero).
 __device__ __forceinline__ void load_block(const uint8_t* __restrict__ row, int kb, int g, int K,
@@ -165,56 +202,43 @@ __device__ __forceinline__ void load_block(const uint8_t* __restrict__ row, int 
   }
 }
 
-// Each wave takes 16 RT weight rows and NT tiles of 16 src1 rows over the K
-// blocks wave, wave + W, ... (the workgroup together reads W * 128
-// consecutive bytes of each weight row); the waves' partial tiles are added
-// in LDS in wave order.  Weights go from memory to the matrix core's
-// operand registers as loaded.  kFused: src1 is f32 and every workgroup
-// quantizes it into LDS first (16 lanes per block), which saves the INIT
-// launch while M is small.
-template <int NT, int RT, bool kFused>
+__device__ __forceinline__ void widen_block(const uint4& lo, const uint4& hi, v8h (&v)[4]) {
+  v[0] = widen(lo.x, lo.y);
+  v[1] = widen(lo.z, lo.w);
+  v[2] = widen(hi.x, hi.y);
+  v[3] = widen(hi.z, hi.w);
+}
+
+// acc += s * (the block dot of 16 weight rows and 16 src1 rows).
+__device__ __forceinline__ void block_fma(const v8h (&w)[4], const v8h (&a)[4], float s, v4f& acc) {
+  v4f c = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) c = __builtin_amdgcn_mfma_f32_16x16x32_f16(w[i], a[i], c, 0, 0, 0);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) acc[e] = fmaf(c[e], s, acc[e]);
+}
+
+// Each workgroup takes 16 weight rows and NT tiles of 16 src1 rows (codes and
+// scales as INIT or the caller left them), its waves the K blocks wave,
+// wave + W, ... (together they read W * 128 consecutive bytes of each weight
+// row); the waves' partial tiles are added in LDS in wave order.  32 rows
+// per workgroup, sharing each src1 operand, measured slower wherever this
+// kernel is used (4096 x 4096, M = 5 / 16 / 32: 11.9 / 13.2 / 17.9 us against
+// 10.0 / 11.3 / 14.1).
+template <int NT>
 __global__ __launch_bounds__(512) void k_f8_skinny(
     const uint8_t* __restrict__ w, const float* __restrict__ wsc, const uint8_t* __restrict__ a,
     const float* __restrict__ asc, int M, int N, int K, float* __restrict__ dst) {
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
-  constexpr int U = RT * NT >= 4 ? 2 : 4;           // blocks in flight per wave
+  constexpr int U = 4;                              // blocks in flight per wave
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int W = blockDim.x >> 6;
   const int g = lane >> 4, i16 = lane & 15;
   const int nkb = (K + kBlk - 1) / kBlk;
-  const int n0 = blockIdx.x * 16 * RT, m0 = blockIdx.y * 16 * NT;
+  const int n0 = blockIdx.x * 16, m0 = blockIdx.y * 16 * NT;
 
-  const uint8_t* wrow[RT];
-  const float* wscr[RT];
-#pragma unroll
-  for (int r = 0; r < RT; ++r) {
-    const int n = n0 + 16 * r + i16;
-    wrow[r] = w + (int64_t)(n < N ? n : N - 1) * K;
-    const int nt = n0 + 16 * r;
-    wscr[r] = wsc + (int64_t)((nt < N ? nt : N - 1) / kBlk) * nkb;
-  }
-
-  // kFused: codes [m][nkb * 128] then scales [m][nkb], M <= 16 rows
-  const int pitch = nkb * kBlk;
-  float* const sscale = reinterpret_cast<float*>(lds + M * pitch);
-  if constexpr (kFused) {
-    const float* x = reinterpret_cast<const float*>(a);
-    const int total = M * nkb;
-    for (int b0 = (tid >> 4); b0 < total; b0 += blockDim.x >> 4) {
-      const int m = b0 / nkb, kb = b0 - m * nkb;
-      const int k = kb * kBlk + 8 * i16;
-      float4 p = make_float4(0.f, 0.f, 0.f, 0.f), q = p;
-      if (k < K) {
-        const float4* s = reinterpret_cast<const float4*>(x + (int64_t)m * K + k);
-        p = s[0]; q = s[1];
-      }
-      float d;
-      const uint2 c = f8_row_block(p, q, d);
-      *reinterpret_cast<uint2*>(lds + m * pitch + k) = c;
-      if (i16 == 0) sscale[b0] = d;
-    }
-  }
-
+  const uint8_t* const wrow = w + (int64_t)min(n0 + i16, N - 1) * K;
+  const float* const wscr = wsc + (int64_t)(n0 / kBlk) * nkb;
   const uint8_t* arow[NT];
   const float* ascr[NT];
   bool live[NT];
@@ -226,110 +250,218 @@ __global__ __launch_bounds__(512) void k_f8_skinny(
     ascr[t] = asc + (int64_t)(live[t] ? m : 0) * nkb;
   }
 
-  v4f acc[RT][NT];
+  v4f acc[NT];
 #pragma unroll
-  for (int r = 0; r < RT; ++r)
-#pragma unroll
-    for (int t = 0; t < NT; ++t) acc[r][t] = (v4f){0.f, 0.f, 0.f, 0.f};
+  for (int t = 0; t < NT; ++t) acc[t] = (v4f){0.f, 0.f, 0.f, 0.f};
 
-  // every wave runs the same number of rounds: the barrier inside is met by all
-  for (int r0 = 0; r0 < nkb; r0 += W * U) {
-    const int kb0 = r0 + wave;
-    uint4 wl[U][RT], wh[U][RT], al[U][NT], ah[U][NT];
-    float sa[U][NT];
+  for (int kb0 = wave; kb0 < nkb; kb0 += W * U) {
+    uint4 wl[U], wh[U], al[U][NT], ah[U][NT];
+    float sa[U][NT], sw[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int kb = min(kb0 + u * W, nkb - 1);       // valid addresses throughout
+      load_block(wrow, kb, g, K, wl[u], wh[u]);
+      sw[u] = wscr[kb];
 #pragma unroll
-      for (int r = 0; r < RT; ++r) load_block(wrow[r], kb, g, K, wl[u][r], wh[u][r]);
-      if constexpr (!kFused) {
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          al[u][t] = ah[u][t] = make_uint4(0, 0, 0, 0);
-          sa[u][t] = 0.0f;
-          if (live[t]) {
-            load_block(arow[t], kb, g, K, al[u][t], ah[u][t]);
-            sa[u][t] = ascr[t][kb];
-          }
+      for (int t = 0; t < NT; ++t) {
+        al[u][t] = ah[u][t] = make_uint4(0, 0, 0, 0);
+        sa[u][t] = 0.0f;
+        if (live[t]) {
+          load_block(arow[t], kb, g, K, al[u][t], ah[u][t]);
+          sa[u][t] = ascr[t][kb];
         }
       }
     }
-    if (kFused && r0 == 0) lds_barrier();             // the first weights are on their way by now
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int kb = kb0 + u * W;
-      if (kb >= nkb) continue;                       // uniform
-      if constexpr (kFused) {
-        al[u][0] = ah[u][0] = make_uint4(0, 0, 0, 0);
-        sa[u][0] = 0.0f;
-        if (i16 < M) {
-          const uint8_t* p = lds + i16 * pitch + kb * kBlk + 16 * g;
-          al[u][0] = *reinterpret_cast<const uint4*>(p);
-          ah[u][0] = *reinterpret_cast<const uint4*>(p + 64);
-          sa[u][0] = sscale[i16 * nkb + kb];
-        }
-      }
+      if (kb0 + u * W >= nkb) continue;                // uniform
+      v8h wv[4];
+      widen_block(wl[u], wh[u], wv);
 #pragma unroll
-      for (int r = 0; r < RT; ++r) {
-        const v8h w0 = widen(wl[u][r].x, wl[u][r].y), w1 = widen(wl[u][r].z, wl[u][r].w);
-        const v8h w2 = widen(wh[u][r].x, wh[u][r].y), w3 = widen(wh[u][r].z, wh[u][r].w);
-        const float sw = wscr[r][kb];
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          v4f s = {0.f, 0.f, 0.f, 0.f};
-          s = __builtin_amdgcn_mfma_f32_16x16x32_f16(w0, widen(al[u][t].x, al[u][t].y), s, 0, 0, 0);
-          s = __builtin_amdgcn_mfma_f32_16x16x32_f16(w1, widen(al[u][t].z, al[u][t].w), s, 0, 0, 0);
-          s = __builtin_amdgcn_mfma_f32_16x16x32_f16(w2, widen(ah[u][t].x, ah[u][t].y), s, 0, 0, 0);
-          s = __builtin_amdgcn_mfma_f32_16x16x32_f16(w3, widen(ah[u][t].z, ah[u][t].w), s, 0, 0, 0);
-          const float sc = sw * sa[u][t];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) acc[r][t][e] = fmaf(s[e], sc, acc[r][t][e]);
-        }
+      for (int t = 0; t < NT; ++t) {
+        v8h av[4];
+        widen_block(al[u][t], ah[u][t], av);
+        block_fma(wv, av, sw[u] * sa[u][t], acc[t]);
       }
     }
   }
 
-  // join the waves' partial tiles: [wave][tile][m][n], n fastest
-  __syncthreads();                                   // kFused: the codes are done with
+  // join the waves' partial tiles: [wave][m][n], n fastest
   float* const part = reinterpret_cast<float*>(lds);
-  constexpr int TILE = 256 * RT * NT;
+  constexpr int TILE = 256 * NT;
 #pragma unroll
-  for (int r = 0; r < RT; ++r)
-#pragma unroll
-    for (int t = 0; t < NT; ++t)
-      *reinterpret_cast<v4f*>(part + wave * TILE + (16 * t + i16) * 16 * RT + 16 * r + 4 * g) = acc[r][t];
+  for (int t = 0; t < NT; ++t)
+    *reinterpret_cast<v4f*>(part + wave * TILE + (16 * t + i16) * 16 + 4 * g) = acc[t];
   __syncthreads();
   for (int e = tid; e < TILE; e += blockDim.x) {
     float s = part[e];
     for (int v = 1; v < W; ++v) s += part[v * TILE + e];
-    const int m = m0 + e / (16 * RT), n = n0 + e % (16 * RT);
+    const int m = m0 + e / 16, n = n0 + e % 16;
     if (m < M && n < N) dst[(int64_t)m * N + n] = s;
+  }
+}
+
+// A few src1 rows given as f32: every workgroup quantizes them into LDS itself
+// (16 lanes per block; no INIT launch, no workspace), then walks groups of
+// 16 weight rows, blockIdx.x, blockIdx.x + gridDim.x, ...  The first group's
+// weights are requested before the quantization waits for src1, each next
+// round's before the current one is computed; the barriers wait for LDS only,
+// so that these loads stay under way.  Rounds of U blocks per wave.
+template <int ROUNDS>
+__global__ __launch_bounds__(512) void k_f8_fused(
+    const float* __restrict__ x, const uint8_t* __restrict__ w, const float* __restrict__ wsc,
+    float* __restrict__ dst, int M, int N, int K, int groups) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+  constexpr int U = 4, W = 8;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int g = lane >> 4, i16 = lane & 15;
+  const int nkb = (K + kBlk - 1) / kBlk, pitch = nkb * kBlk + 16;   // 16: rows in different banks
+  // codes [M][pitch], scales [M][nkb], the waves' partial tiles
+  float* const sscale = reinterpret_cast<float*>(lds + M * pitch);
+  float* const part = reinterpret_cast<float*>(lds + M * pitch + (M * nkb * 4 + 15) / 16 * 16);
+
+  // src1: M * nkb <= 32 ROUNDS blocks of 128, all requested at once
+  const int total = M * nkb;
+  float4 p[ROUNDS], q[ROUNDS];
+#pragma unroll
+  for (int r = 0; r < ROUNDS; ++r) {
+    const int b = min((tid >> 4) + 32 * r, total - 1), m = b / nkb;
+    const int k = (b - m * nkb) * kBlk + 8 * i16;
+    p[r] = q[r] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (k < K) {
+      const float4* s = reinterpret_cast<const float4*>(x + (int64_t)m * K + k);
+      p[r] = s[0]; q[r] = s[1];
+    }
+  }
+  struct Round { uint4 lo[U], hi[U]; float s[U]; };
+  const auto load = [&](Round& r, int group, int kb0) {
+    const uint8_t* const row = w + (int64_t)min(16 * group + i16, N - 1) * K;
+    const float* const sc = wsc + (int64_t)(16 * group / kBlk) * nkb;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int kb = min(kb0 + wave + u * W, nkb - 1);
+      load_block(row, kb, g, K, r.lo[u], r.hi[u]);
+      r.s[u] = sc[kb];
+    }
+  };
+  int group = blockIdx.x, kb0 = 0;
+  Round cur;
+  load(cur, group, 0);
+  __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+  for (int r = 0; r < ROUNDS; ++r) {
+    const int b = (tid >> 4) + 32 * r;
+    float d;
+    const uint2 c = f8_row_block(p[r], q[r], d);
+    if (b < total) {
+      const int m = b / nkb;
+      *reinterpret_cast<uint2*>(lds + m * pitch + (b - m * nkb) * kBlk + 8 * i16) = c;
+      if (i16 == 0) sscale[b] = d;
+    }
+  }
+  lds_barrier();
+
+  v4f acc = {0.f, 0.f, 0.f, 0.f};
+  while (group < groups) {
+    const bool last = kb0 + W * U >= nkb;
+    const int ngroup = last ? group + (int)gridDim.x : group, nkb0 = last ? 0 : kb0 + W * U;
+    Round next;
+    if (ngroup < groups) load(next, ngroup, nkb0);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int kb = kb0 + wave + u * W;
+      if (kb >= nkb) continue;                         // uniform
+      uint4 al = make_uint4(0, 0, 0, 0), ah = al;
+      float sa = 0.0f;
+      if (i16 < M) {
+        const uint8_t* const c = lds + i16 * pitch + kb * kBlk + 16 * g;
+        al = *reinterpret_cast<const uint4*>(c);
+        ah = *reinterpret_cast<const uint4*>(c + 64);
+        sa = sscale[i16 * nkb + kb];
+      }
+      v8h wv[4], av[4];
+      widen_block(cur.lo[u], cur.hi[u], wv);
+      widen_block(al, ah, av);
+      block_fma(wv, av, cur.s[u] * sa, acc);
+    }
+    if (last) {
+      if (i16 < M) *reinterpret_cast<v4f*>(part + (wave * M + i16) * 16 + 4 * g) = acc;
+      lds_barrier();
+      for (int e = tid; e < 16 * M; e += 512) {
+        float s = part[e];
+#pragma unroll
+        for (int v = 1; v < W; ++v) s += part[v * 16 * M + e];
+        const int n = 16 * group + e % 16;
+        if (n < N) dst[(int64_t)(e / 16) * N + n] = s;
+      }
+      lds_barrier();                                   // the partial tiles are read
+      acc = (v4f){0.f, 0.f, 0.f, 0.f};
+    }
+    cur = next;
+    group = ngroup;
+    kb0 = nkb0;
   }
 }
 
 // ---------------------------------------------------------------- product, many src1 rows
 
-typedef __attribute__((address_space(1))) const void gvoid;
-typedef __attribute__((address_space(3))) void lvoid;
+// Asynchronous copies of 16 (4) bytes per lane from base + off into LDS at
+// dst + 16 (4) * lane, dst uniform.  Written as assembly without outputs, so
+// that the compiler does not drain them ahead of every LDS read: the code
+// below waits for the oldest stage only, by count (copies complete in the
+// order they were issued).
+__device__ __forceinline__ uint32_t lds_offset(const void* p) {
+  return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void*)p;
+}
+__device__ __forceinline__ void copy16(uint32_t dst, const void* base, uint32_t off) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+               :: "s"(dst), "v"(off), "s"(base) : "memory", "m0");
+}
+__device__ __forceinline__ void copy4(uint32_t dst, const void* base, uint32_t off) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2"
+               :: "s"(dst), "v"(off), "s"(base) : "memory", "m0");
+}
+// At most N of this wave's copies still under way; its LDS reads are done.
+template <int N>
+__device__ __forceinline__ void wait_copies() {
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" :: "n"(N) : "memory");
+}
 
-// Output tile of BN weight rows x BM src1 rows per workgroup,
-// one block of 128 k per stage.  Both operands' stages go from memory
-// straight into LDS (16 bytes per lane), kStages buffers deep, the rows'
-// eight 16-byte chunks permuted by the row's low three bits so that the
-// operand reads (32 rows at one chunk) spread over the banks.
-template <int BM, int BN, int WAVES_M, int WAVES_N, int kStages>
+constexpr int STAGES = 4;      // (8 for the 64-row tiles measured no faster)
+
+// Output tile of BN weight rows x BM src1 rows per workgroup, half a block of
+// 128 k per stage, STAGES stages in LDS, copied there straight from memory: the
+// weights as e4m3 codes, src1 as binary16 (widened once by INIT, so that the
+// vector units only widen the weights).  A wave holds 2 x 2 tiles of 32 x 32.
+//
+// A block is eight steps of 16 k (q), four to a stage; each MFMA adds to the
+// block dot c, and the fp32 sums take c * (dw * ds).  Operands are read one q
+// ahead.  The one
+// barrier per stage stands before its last q's MFMAs: there every wave has
+// read the whole stage, so the copy of the stage STAGES further can start, and
+// the next stage has arrived, so its first operands are read behind those
+// MFMAs.
+//
+// In LDS a row's 16-byte chunks are permuted so that the 16 rows of an
+// operand read lie in different banks: chunk ^ (row / 4) % 4 of the 4 of a
+// weight row's half block, chunk ^ (row / 2) % 8 of the 8 of a src1 row's.
+// Lane half h of an MFMA holds k 32 p + 16 h + 8 (q % 2) .. + 7, p = q / 2: one
+// chunk of codes serves two q.
+template <int BM, int BN, int WAVES_M, int WAVES_N>
 __global__ __launch_bounds__(64 * WAVES_M * WAVES_N, 1) void k_f8_wide(
-    const uint8_t* __restrict__ w, const float* __restrict__ wsc, const uint8_t* __restrict__ a,
+    const uint8_t* __restrict__ w, const float* __restrict__ wsc, const uint16_t* __restrict__ a,
     const float* __restrict__ asc, int M, int N, int K, float* __restrict__ dst, int tiles_m,
     int tiles, int split, int kchunk) {
-  constexpr int NW = WAVES_M * WAVES_N;
+  constexpr int NW = WAVES_M * WAVES_N, HB = kBlk / 2;         // k per stage
   constexpr int WTM = BM / WAVES_M, WTN = BN / WAVES_N;
   constexpr int TM = WTM / 32, TN = WTN / 32;
+  constexpr int kA = BN * HB, kS = kA + BM * 2 * HB;           // stage: weights, src1, its scales
+  constexpr int STAGE = kS + BM * 4;
+  constexpr int WL = BN / 16 / NW, AL = BM / 8 / NW;  // 1 KB pieces per wave: 16 weight, 8 src1 rows
+  constexpr int kCopies = WL + AL + 1;
+  static_assert((STAGES & (STAGES - 1)) == 0 && (STAGES - 1) * kCopies < 64, "wait counts");
   static_assert(kBlk % WTN == 0, "one weight scale per wave and stage");
-  constexpr int ROWS = BM + BN;
-  constexpr int STAGE = ROWS * kBlk + BM * 4;        // codes, then the src1 rows' scales
-  constexpr int LOADS = ROWS / 8 / NW;               // 8-row pieces per wave and stage
-  static_assert(ROWS % (8 * NW) == 0 && BM % 64 == 0, "whole pieces");
+  static_assert(BN % (16 * NW) == 0 && BM % (8 * NW) == 0 && BM % 64 == 0 && NW % 2 == 0, "whole pieces");
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
 
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -341,37 +473,40 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N, 1) void k_f8_wide(
   const int tm = tt % tiles_m, tn = tt / tiles_m;    // m fastest: same weight tile adjacent
   const int m0 = tm * BM, n0 = tn * BN;
   const int kb0 = z * kchunk, kb1 = min(kb0 + kchunk, nkb);
+  const int s1 = 2 * (kb1 - kb0);                    // stages
 
-  // this lane's part of each 8-row piece: row base + lane / 8, the chunk that
-  // belongs at position lane % 8
+  // this lane's part of each piece
   const uint8_t* const wbase = w + (int64_t)n0 * K;
-  const uint8_t* const abase = a + (int64_t)m0 * K;
-  const int chunk = (lane & 7) ^ (lane >> 3);
-  uint32_t off[LOADS];
+  const uint16_t* const abase = a + (int64_t)m0 * nkb * kBlk;
+  const int wchunk = (lane & 3) ^ ((lane >> 4) & 3);
+  const int achunk = (lane & 7) ^ ((4 * (wave & 1) + (lane >> 4)) & 7);
+  uint32_t woff[WL], aoff[AL];
 #pragma unroll
-  for (int i = 0; i < LOADS; ++i) {
-    const int r = (i * NW + wave) * 8 + (lane >> 3);
-    const int rr = r < BN ? min(r, N - 1 - n0) : min(r - BN, M - 1 - m0);
-    off[i] = (uint32_t)rr * (uint32_t)K;
-  }
-
-  auto load = [&](int kb, int buf) {
-    uint8_t* const base = lds + buf * STAGE;
-    int k = kb * kBlk + chunk * 16;
-    if (k >= K) k = 0;                               // past the row: any valid bytes, zeroed below
+  for (int i = 0; i < WL; ++i)
+    woff[i] = (uint32_t)min((i * NW + wave) * 16 + (lane >> 2), N - 1 - n0) * (uint32_t)K;
 #pragma unroll
-    for (int i = 0; i < LOADS; ++i) {
-      const int r = (i * NW + wave) * 8;             // uniform
-      const uint8_t* const src = (r < BN ? wbase : abase) + (off[i] + (uint32_t)k);
-      __builtin_amdgcn_global_load_lds((gvoid*)src, (lvoid*)(base + r * kBlk), 16, 0, 0);
-    }
-    if (wave < BM / 64) {
-      const int m = min(m0 + 64 * wave + lane, M - 1);
-      __builtin_amdgcn_global_load_lds((gvoid*)(asc + (int64_t)m * nkb + kb),
-                                       (lvoid*)(base + ROWS * kBlk + 256 * wave), 4, 0, 0);
-    }
+  for (int i = 0; i < AL; ++i)
+    aoff[i] = (uint32_t)min((i * NW + wave) * 8 + (lane >> 3), M - 1 - m0) * (uint32_t)nkb * (2 * kBlk);
+  // every wave issues the same number of copies (the rows' scales are copied
+  // by several waves, to the same place)
+  const int sm = (wave % (BM / 64)) * 64;
+  const float* const sbase = asc + (int64_t)m0 * nkb;
+  const uint32_t soff = (uint32_t)min(sm + lane, M - 1 - m0) * (uint32_t)nkb;
+  const uint32_t lds0 = lds_offset(lds);
+  auto copy_stage = [&](int s) {
+    const uint32_t base = lds0 + (s % STAGES) * STAGE;
+    const int k0 = kb0 * kBlk + s * HB;
+    // past a weight row: its own first codes, which meet the zeros that src1
+    // is padded with (if one is a NaN, so is the whole row's result)
+    uint32_t kw = k0 + wchunk * 16;
+    const uint32_t ka = k0 + achunk * 8;
+    if ((int)kw >= K) kw = 0;
+#pragma unroll
+    for (int i = 0; i < WL; ++i) copy16(base + (i * NW + wave) * 1024, wbase, woff[i] + kw);
+#pragma unroll
+    for (int i = 0; i < AL; ++i) copy16(base + kA + (i * NW + wave) * 1024, abase, aoff[i] + 2 * ka);
+    copy4(base + kS + 4 * sm, sbase, 4 * (soff + kb0 + (s >> 1)));
   };
-
   const int nrow = min(n0 + wn * WTN, N - 1);
   const float* const wscr = wsc + (int64_t)(nrow / kBlk) * nkb;
 
@@ -383,61 +518,76 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N, 1) void k_f8_wide(
 #pragma unroll
       for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
 
-  const int ksteps = kb1 - kb0;
-  for (int s = 0; s < kStages - 1; ++s)
-    if (s < ksteps) load(kb0 + s, s);
-
-  int buf = 0;
-  for (int s = 0; s < ksteps; ++s) {
-    const int kb = kb0 + s;
-    __syncthreads();
-    const int next = s + kStages - 1;
-    if (next < ksteps) load(kb0 + next, buf == 0 ? kStages - 1 : buf - 1);
-    uint8_t* const base = lds + buf * STAGE;
-    if ((kb + 1) * kBlk > K) {                       // the chunks past K become zero in both operands
-      const int valid = (K - kb * kBlk) / 16;
-      for (int r = tid; r < ROWS; r += 64 * NW)
-        for (int c = valid; c < 8; ++c)
-          *reinterpret_cast<uint4*>(base + r * kBlk + 16 * (c ^ (r & 7))) = make_uint4(0, 0, 0, 0);
-      __syncthreads();
+  const int wrow = (wn * WTN + l32) * HB, arow = kA + (wm * WTM + l32) * 2 * HB;
+  const int wx = (l32 >> 2) & 3, ax = (l32 >> 1) & 7;
+  uint4 wr[2][TN];
+  v8h av[2][TM];
+  // the operands of step q (0..3) of a stage into register set q % 2 (weights:
+  // of p = q / 2)
+  auto read = [&](const uint8_t* base, int q) {
+    if (q % 2 == 0) {
+#pragma unroll
+      for (int i = 0; i < TN; ++i)
+        wr[(q / 2) % 2][i] = *reinterpret_cast<const uint4*>(base + wrow + 32 * i * HB + 16 * ((q + h) ^ wx));
     }
-    const float sw = wscr[kb];
-    // lane half h holds chunk 2 q + h of its row: 8 k for each of two MFMAs
-    auto operand_at = [&](int row, int q, v8h& x, v8h& y) {
-      const uint4 v = *reinterpret_cast<const uint4*>(base + row * kBlk + 16 * ((2 * q + h) ^ (row & 7)));
-      x = widen(v.x, v.y);
-      y = widen(v.z, v.w);
-    };
-    v8h av[TM][8];
+#pragma unroll
+    for (int j = 0; j < TM; ++j)
+      av[q % 2][j] = *reinterpret_cast<const v8h*>(base + arow + 64 * j * HB + 16 * ((4 * (q / 2) + 2 * h + q % 2) ^ ax));
+  };
+
+#pragma unroll
+  for (int s = 0; s < STAGES; ++s)
+    if (s < s1) copy_stage(s);
+  if (s1 >= STAGES) wait_copies<(STAGES - 1) * kCopies>();
+  else wait_copies<0>();
+  __builtin_amdgcn_s_barrier();
+  read(lds, 0);
+
+  float sw = wscr[kb0];
+  for (int s = 0; s < s1; s += 2) {
+    v16f c[TN][TM];
     float sc[TM];
 #pragma unroll
-    for (int j = 0; j < TM; ++j) {
-      const int row = wm * WTM + 32 * j + l32;
+    for (int q = 0; q < 8; ++q) {
+      const int st = s + q / 4;                      // stage of this q
+      const uint8_t* const base = lds + (st % STAGES) * STAGE;
+      if (q % 4 < 3) {
+        read(base, q % 4 + 1);
+      } else {
+        // the next stage is here and this wave's reads of this one are done
+        if (st + STAGES - 1 < s1) wait_copies<(STAGES - 2) * kCopies>();
+        else wait_copies<0>();
+        __builtin_amdgcn_s_barrier();
+        if (st + STAGES < s1) copy_stage(st + STAGES);
+        read(lds + ((st + 1) % STAGES) * STAGE, 0);
+      }
+      __builtin_amdgcn_sched_barrier(0);             // the reads stay ahead of the products
+      if (q == 1) {
+        const float* const ss = reinterpret_cast<const float*>(base + kS) + wm * WTM + l32;
 #pragma unroll
-      for (int q = 0; q < 4; ++q) operand_at(BN + row, q, av[j][2 * q], av[j][2 * q + 1]);
-      sc[j] = sw * *reinterpret_cast<const float*>(base + ROWS * kBlk + 4 * row);
+        for (int j = 0; j < TM; ++j) sc[j] = sw * ss[32 * j];
+        sw = wscr[min(kb0 + s / 2 + 1, nkb - 1)];
+      }
+#pragma unroll
+      for (int i = 0; i < TN; ++i) {
+        const uint4 v = wr[(q / 2) % 2][i];
+        const v8h wv = q % 2 == 0 ? widen(v.x, v.y) : widen(v.z, v.w);
+#pragma unroll
+        for (int j = 0; j < TM; ++j) {
+          if (q == 0) {
+#pragma unroll
+            for (int r = 0; r < 16; ++r) c[i][j][r] = 0.0f;
+          }
+          c[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(wv, av[q % 2][j], c[i][j], 0, 0, 0);
+        }
+      }
     }
 #pragma unroll
-    for (int i = 0; i < TN; ++i) {
-      v8h wv[8];
-#pragma unroll
-      for (int q = 0; q < 4; ++q) operand_at(wn * WTN + 32 * i + l32, q, wv[2 * q], wv[2 * q + 1]);
-      v16f c[TM];
+    for (int i = 0; i < TN; ++i)
 #pragma unroll
       for (int j = 0; j < TM; ++j)
 #pragma unroll
-        for (int r = 0; r < 16; ++r) c[j][r] = 0.0f;
-#pragma unroll
-      for (int q = 0; q < 8; ++q)
-#pragma unroll
-        for (int j = 0; j < TM; ++j)
-          c[j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(wv[q], av[j][q], c[j], 0, 0, 0);
-#pragma unroll
-      for (int j = 0; j < TM; ++j)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) acc[i][j][r] = fmaf(c[j][r], sc[j], acc[i][j][r]);
-    }
-    buf = buf + 1 == kStages ? 0 : buf + 1;
+        for (int r = 0; r < 16; ++r) acc[i][j][r] = fmaf(c[i][j][r], sc[j], acc[i][j][r]);
   }
 
   // lane: src1 row of column l32, weight rows 8 q + 4 h + 0..3
@@ -465,7 +615,37 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N, 1) void k_f8_wide(
     }
 }
 
+// dst = the sum of its slices, in order; the loads of four slices are under way at once.
+template <bool kVec>
+__global__ __launch_bounds__(256) void k_join_slices(const float* __restrict__ part,
+                                                     float* __restrict__ dst, int64_t n, int slices) {
+  constexpr int V = kVec ? 4 : 1;
+  typedef float vec __attribute__((ext_vector_type(V)));
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i * V < n; i += (int64_t)gridDim.x * 256) {
+    vec s = *reinterpret_cast<const vec*>(part + i * V);
+    for (int z0 = 1; z0 < slices; z0 += 4) {
+      vec v[4];
+#pragma unroll
+      for (int z = 0; z < 4; ++z)
+        v[z] = *reinterpret_cast<const vec*>(part + (int64_t)min(z0 + z, slices - 1) * n + i * V);
+#pragma unroll
+      for (int z = 0; z < 4; ++z)
+        if (z0 + z < slices) s += v[z];
+    }
+    *reinterpret_cast<vec*>(dst + i * V) = s;
+  }
+}
+
 }  // namespace
+
+hipError_t launch_join_slices(const float* part, float* dst, int64_t n, int slices, hipStream_t s) {
+  const bool vec = n % 4 == 0 && (uintptr_t)dst % 16 == 0;       // part is 256-byte aligned
+  const int64_t items = vec ? n / 4 : n, grid = (items + 255) / 256;
+  const dim3 g((unsigned)(grid < 4096 ? grid : 4096));
+  if (vec) hipLaunchKernelGGL((k_join_slices<true>), g, dim3(256), 0, s, part, dst, n, slices);
+  else hipLaunchKernelGGL((k_join_slices<false>), g, dim3(256), 0, s, part, dst, n, slices);
+  return hipGetLastError();
+}
 
 hipError_t launch_f8_quantize(const float* x, uint8_t* codes, float* scales, int64_t nrows,
                               int64_t k, int block_rows, hipStream_t s) {
@@ -485,22 +665,30 @@ hipError_t launch_f8_quantize(const float* x, uint8_t* codes, float* scales, int
 
 namespace {
 
-template <int NT, int RT, bool kFused>
+template <int NT>
 hipError_t skinny(const F8Plan& p, const uint8_t* w, const float* wsc, const uint8_t* a,
                   const float* asc, float* dst, int M, int N, int K, hipStream_t s) {
-  hipLaunchKernelGGL((k_f8_skinny<NT, RT, kFused>), dim3((unsigned)p.grid_n, (unsigned)p.grid_m),
+  hipLaunchKernelGGL((k_f8_skinny<NT>), dim3((unsigned)p.grid_n, (unsigned)p.grid_m),
                      dim3(64 * p.waves), p.lds, s, w, wsc, a, asc, M, N, K, dst);
   return hipGetLastError();
 }
 
-template <int BM, int BN, int WAVES_M, int WAVES_N, int kStages>
-hipError_t wide(const F8Plan& p, const uint8_t* w, const float* wsc, const uint8_t* a,
+template <int ROUNDS>
+hipError_t fused(const F8Plan& p, const float* x, const uint8_t* w, const float* wsc, float* dst,
+                 int M, int N, int K, hipStream_t s) {
+  hipLaunchKernelGGL((k_f8_fused<ROUNDS>), dim3((unsigned)p.grid_n), dim3(512), p.lds, s, x, w,
+                     wsc, dst, M, N, K, (N + 15) / 16);
+  return hipGetLastError();
+}
+
+template <int BM, int BN, int WAVES_M, int WAVES_N>
+hipError_t wide(const F8Plan& p, const uint8_t* w, const float* wsc, const uint16_t* a,
                 const float* asc, float* dst, int M, int N, int K, void* ws, hipStream_t s) {
-  constexpr int kLds = kStages * ((BM + BN) * kBlk + BM * 4);
-  auto* const kern = k_f8_wide<BM, BN, WAVES_M, WAVES_N, kStages>;
+  constexpr int kLds = STAGES * (BN * kBlk / 2 + BM * kBlk + BM * 4);
+  auto* const kern = k_f8_wide<BM, BN, WAVES_M, WAVES_N>;
   if (kLds > 65536) {
-    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kern),
-                                             hipFuncAttributeMaxDynamicSharedMemorySize, kLds);
+    static std::atomic<uint64_t> raised{0};          // devices whose limit is set already
+    const hipError_t e = raise_lds(reinterpret_cast<const void*>(kern), kLds, raised);
     if (e != hipSuccess) return e;
   }
   float* const out = p.split > 1 ? reinterpret_cast<float*>((uint8_t*)ws + p.off_part) : dst;
@@ -508,7 +696,7 @@ hipError_t wide(const F8Plan& p, const uint8_t* w, const float* wsc, const uint8
                      dim3(64 * WAVES_M * WAVES_N), kLds, s, w, wsc, a, asc, M, N, K, out,
                      (int)p.tiles_m, (int)(p.tiles_m * p.tiles_n), p.split, (int)p.kchunk);
   hipError_t e = hipGetLastError();
-  if (e == hipSuccess && p.split > 1) e = launch_splitk_reduce(out, dst, (int64_t)M * N, p.split, s);
+  if (e == hipSuccess && p.split > 1) e = launch_join_slices(out, dst, (int64_t)M * N, p.split, s);
   return e;
 }
 
@@ -517,9 +705,35 @@ hipError_t wide(const F8Plan& p, const uint8_t* w, const float* wsc, const uint8
 hipError_t launch_f8_product(const F8Plan& p, const uint8_t* w, const float* wsc, const float* x,
                              const uint8_t* a, const float* asc, float* dst, int M, int N, int K,
                              void* ws, hipStream_t s) {
-  if (p.kind == F8_FUSED)
-    return p.rt == 2 ? skinny<1, 2, true>(p, w, wsc, (const uint8_t*)x, nullptr, dst, M, N, K, s)
-                     : skinny<1, 1, true>(p, w, wsc, (const uint8_t*)x, nullptr, dst, M, N, K, s);
+  if (p.kind == F8_FUSED) {
+    if (p.nt == 1) return fused<1>(p, x, w, wsc, dst, M, N, K, s);
+    if (p.nt == 2) return fused<2>(p, x, w, wsc, dst, M, N, K, s);
+    if (p.nt == 4) return fused<4>(p, x, w, wsc, dst, M, N, K, s);
+    if (p.nt == 8) return fused<8>(p, x, w, wsc, dst, M, N, K, s);
+    return hipErrorInvalidValue;
+  }
+  if (p.kind == F8_WIDE) {
+    uint16_t* const values = reinterpret_cast<uint16_t*>((uint8_t*)ws + p.off_a);
+    const int64_t nkb = (K + kBlk - 1) / kBlk, nblocks = M * nkb;
+    if (x) {
+      float* const scales = reinterpret_cast<float*>((uint8_t*)ws + p.off_as);
+      const int64_t grid = (nblocks + 15) / 16;
+      hipLaunchKernelGGL(k_f8_quantize_rows_f16, dim3((unsigned)(grid < kMaxGridX ? grid : kMaxGridX)),
+                         dim3(256), 0, s, x, values, scales, K, (int)nkb, nblocks);
+      asc = scales;
+    } else {
+      const int64_t pieces = 8 * nblocks, grid = (pieces + 255) / 256;
+      hipLaunchKernelGGL(k_f8_widen, dim3((unsigned)(grid < kMaxGridX ? grid : kMaxGridX)), dim3(256),
+                         0, s, a, values, K, (int)nkb, pieces);
+    }
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    if (p.bm == 128 && p.bn == 256) return wide<128, 256, 2, 4>(p, w, wsc, values, asc, dst, M, N, K, ws, s);
+    if (p.bm == 128 && p.bn == 128) return wide<128, 128, 2, 4>(p, w, wsc, values, asc, dst, M, N, K, ws, s);
+    if (p.bm == 64 && p.bn == 128) return wide<64, 128, 2, 4>(p, w, wsc, values, asc, dst, M, N, K, ws, s);
+    if (p.bm == 64 && p.bn == 64) return wide<64, 64, 2, 2>(p, w, wsc, values, asc, dst, M, N, K, ws, s);
+    return hipErrorInvalidValue;
+  }
   if (x) {                                            // INIT
     uint8_t* codes = (uint8_t*)ws + p.off_a;
     float* scales = reinterpret_cast<float*>((uint8_t*)ws + p.off_as);
@@ -528,16 +742,8 @@ hipError_t launch_f8_product(const F8Plan& p, const uint8_t* w, const float* wsc
     a = codes;
     asc = scales;
   }
-  if (p.kind == F8_WIDE) {
-    if (p.bm == 128 && p.bn == 256) return wide<128, 256, 2, 4, 3>(p, w, wsc, a, asc, dst, M, N, K, ws, s);
-    if (p.bm == 128 && p.bn == 128) return wide<128, 128, 2, 2, 2>(p, w, wsc, a, asc, dst, M, N, K, ws, s);
-    if (p.bm == 64 && p.bn == 128) return wide<64, 128, 1, 4, 2>(p, w, wsc, a, asc, dst, M, N, K, ws, s);
-    return hipErrorInvalidValue;
-  }
-#define QSG_F8(NT_, RT_) \
-  if (p.nt == NT_ && p.rt == RT_) return skinny<NT_, RT_, false>(p, w, wsc, a, asc, dst, M, N, K, s);
-  QSG_F8(1, 1) QSG_F8(1, 2) QSG_F8(2, 1) QSG_F8(2, 2) QSG_F8(4, 1) QSG_F8(4, 2)
-#undef QSG_F8
+  if (p.nt == 1) return skinny<1>(p, w, wsc, a, asc, dst, M, N, K, s);
+  if (p.nt == 2) return skinny<2>(p, w, wsc, a, asc, dst, M, N, K, s);
   return hipErrorInvalidValue;
 }
 

@@ -31,38 +31,52 @@ int make_f8_plan(int64_t M, int64_t N, int64_t K, bool given, F8Plan* p) {
   if (K == 0) { p->kind = F8_ZERO; return MM_OK; }
   const int64_t nkb = ceil_div(K, kF8Block);
 
-  // src1 codes and scales (INIT), unless the caller gives them or the kernel
-  // quantizes src1 itself
-  const size_t fused_lds = (size_t)M * (size_t)nkb * (kF8Block + 4);
-  if (!given && M <= 4 && fused_lds <= (size_t)kF8FusedMaxLds) {
+  // Up to 8 rounds of 32 blocks of 128: every workgroup quantizes src1 itself
+  // (at M = 8 and K = 4096 in about the time of an INIT launch).
+  const int64_t blocks = M * nkb;
+  if (!given && M <= 16 && blocks <= 256) {
     p->kind = F8_FUSED;
-    p->nt = 1;
-    p->rt = 1;
-    p->waves = 8;
-    while (p->waves > 1 && p->waves > nkb) p->waves /= 2;
-    p->grid_n = ceil_div(N, 16 * p->rt);
-    const size_t join = (size_t)p->waves * 1024 * p->rt;
-    p->lds = align_up(fused_lds > join ? fused_lds : join, 16);
+    p->nt = blocks <= 32 ? 1 : blocks <= 64 ? 2 : blocks <= 128 ? 4 : 8;
+    const int64_t groups = ceil_div(N, 16);
+    // workgroups along N, each walking groups of 16 rows (us per call, 14336 x
+    // 4096, 512 / 768 workgroups: M = 1 16.5 / 16.0, M = 8 20.3 / 21.7)
+    const int64_t most = M <= 2 ? 3 * kCUs : 2 * kCUs;
+    p->grid_n = groups < most ? groups : most;
+    p->lds = (size_t)(M * (nkb * kF8Block + 16)) + align_up((size_t)blocks * 4, 16) + (size_t)M * 512;
     return MM_OK;
   }
+  // the tiled kernel takes src1 as binary16 values in rows of whole blocks,
+  // whoever quantized it.
+  // The tiled kernel from 9 src1 rows on matrices of 32 MiB or more, else from
+  // 33 (us per call with INIT, M = 8 / 16 / 32, skinny against 64 x 128 tiles:
+  // 14336 x 4096 23.2 / 26.4 / 42.5 against 22.8 / 22.6 / 25.0, 4096 x 4096
+  // 10.4 / 11.3 / 14.1 against 13.6 / 13.9 / 15.1).
+  const bool wide = M > (N * K >= ((int64_t)1 << 25) ? 8 : 32);
   size_t off = 0;
+  if (wide || !given) {
+    p->off_a = off;
+    off = align_up(off + (size_t)M * (wide ? (size_t)nkb * kF8Block * 2 : (size_t)K), 256);
+  }
   if (!given) {
-    p->off_a = off; off = align_up(off + (size_t)M * (size_t)K, 256);
     p->off_as = off; off = align_up(off + (size_t)M * (size_t)nkb * 4, 256);
   }
-  if (M <= 64) {
+  if (!wide) {
     p->kind = F8_SKINNY;
-    p->nt = M <= 16 ? 1 : M <= 32 ? 2 : 4;
-    p->rt = 1;
+    p->nt = M <= 16 ? 1 : 2;
     p->waves = 8;
     while (p->waves > 1 && p->waves > nkb) p->waves /= 2;
-    p->grid_n = ceil_div(N, 16 * p->rt);
+    p->grid_n = ceil_div(N, 16);
     p->grid_m = ceil_div(M, 16 * p->nt);
-    p->lds = (size_t)p->waves * 1024 * p->rt * p->nt;
+    p->lds = (size_t)p->waves * 1024 * p->nt;
   } else {
     p->kind = F8_WIDE;
-    p->bm = 128;
-    p->bn = 256;
+    // Output tile by M (us per call, 64 x 128, 128 x 128 and 128 x 256 tiles:
+    // 14336 x 4096, M = 128 40.1 / 41.1 / 44.1, M = 256 65.8 / 56.8 / 59.0,
+    // M = 512 117.5 / 107.8 / 81.1; 4096 x 4096, M = 128 22.3 / 27.9 / 33.9,
+    // M = 512 39.5 / 41.7 / 43.9).
+    p->bm = M <= 128 ? 64 : 128;
+    p->bn = M > 256 && (ceil_div(M, 128) * ceil_div(N, 256) >= kCUs / 2 || nkb >= 64) ? 256 : 128;
+    if (M <= 64 && N * K < ((int64_t)1 << 25)) p->bn = 64;     // 4096 x 4096, M = 64: 16.0 against 18.7
     p->tiles_m = ceil_div(M, p->bm);
     p->tiles_n = ceil_div(N, p->bn);
     const int64_t tiles = p->tiles_m * p->tiles_n;

@@ -4,9 +4,22 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "plan.h"
 
 namespace qsg {
+
+// Lets `kern` use `bytes` of dynamic LDS (past 64 KB) on the current device;
+// asked of the runtime once per device and kernel (`raised`, a bit each).
+inline hipError_t raise_lds(const void* kern, int bytes, std::atomic<uint64_t>& raised) {
+  int dev = 0;
+  hipError_t e = hipGetDevice(&dev);
+  if (e != hipSuccess || (dev < 64 && raised.load(std::memory_order_relaxed) >> dev & 1)) return e;
+  e = hipFuncSetAttribute(kern, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == hipSuccess && dev < 64) raised.fetch_or(1ull << dev, std::memory_order_relaxed);
+  return e;
+}
 
 // Q8_0 activation quantisation.  Writes the canonical 34-byte blocks to
 // `canon` (may be NULL) and/or the library's internal wdata layout
@@ -99,6 +112,9 @@ hipError_t launch_f8_quantize(const float* x, uint8_t* codes, float* scales, int
 hipError_t launch_f8_product(const F8Plan& p, const uint8_t* w, const float* wsc, const float* x,
                              const uint8_t* a, const float* asc, float* dst, int M, int N, int K,
                              void* ws, hipStream_t s);
+// dst[i] = sum over z = 0..slices-1, in that order, of part[z * n + i]; part 16-byte
+// aligned.  (k_splitk_reduce with several slices' loads under way.)
+hipError_t launch_join_slices(const float* part, float* dst, int64_t n, int slices, hipStream_t s);
 // Mixture-of-experts layer; the pointers after `dst` lie in the workspace
 // (ids and weights possibly in the caller's arrays).
 struct MoeArgs {

@@ -35,8 +35,6 @@
 //   a lane's operand is two 16-byte loads and four blocks' scales are one.
 // * Work moves in units of 4 blocks (128 k); a wave holds one unit while the
 //   next one's loads are in flight.
-#include <atomic>
-
 #include "device.h"
 #include "kernels.h"
 #include "../../include/mm.h"
@@ -692,33 +690,13 @@ __global__ __launch_bounds__(64 * W) void k_moe_down(MoeArgs a, float* __restric
   }
 }
 
-// dst = the sum of its slices, in order; eight loads in flight.
-__global__ __launch_bounds__(256) void k_moe_join(const float* __restrict__ part,
-                                                  float* __restrict__ dst, int n, int slices) {
-  const int i = blockIdx.x * 256 + threadIdx.x;
-  if (i >= n) return;
-  float v[8];
-#pragma unroll
-  for (int z = 0; z < 8; ++z) v[z] = z < slices ? part[(int64_t)z * n + i] : 0.0f;
-  float s = v[0];
-#pragma unroll
-  for (int z = 1; z < 8; ++z) s += v[z];
-  dst[i] = s;
-}
-
 template <int TY, int RT, int W, bool kFew>
 hipError_t down(const MoePlan& p, const MoeArgs& a, float* out, hipStream_t s) {
   const int lds = W * a.T * 16 * RT * 4;
   auto* const kern = k_moe_down<TY, RT, W, kFew>;
   static std::atomic<uint64_t> raised{0};            // devices whose limit is set already
-  int dev = 0;
-  if (hipGetDevice(&dev) != hipSuccess) return hipErrorInvalidDevice;
-  if (!(raised.load(std::memory_order_relaxed) >> dev & 1)) {
-    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kern),
-                                             hipFuncAttributeMaxDynamicSharedMemorySize, kMoeMaxSums);
-    if (e != hipSuccess) return e;
-    raised.fetch_or(1ull << dev, std::memory_order_relaxed);
-  }
+  const hipError_t e = raise_lds(reinterpret_cast<const void*>(kern), kMoeMaxSums, raised);
+  if (e != hipSuccess) return e;
   hipLaunchKernelGGL(kern, dim3(a.D / (16 * RT), p.slices), dim3(64 * W), lds, s, a, out);
   return hipGetLastError();
 }
@@ -749,11 +727,7 @@ hipError_t run(const MoePlan& p, const MoeArgs& a, float* part, hipStream_t s) {
   else if (p.rt == 4) e = down<TY, 4, 8, false>(p, a, out, s);
   else if (p.rt == 2) e = down<TY, 2, 8, false>(p, a, out, s);
   else e = down<TY, 1, 8, false>(p, a, out, s);
-  if (e == hipSuccess && p.slices > 1) {
-    const int n = a.T * a.D;
-    hipLaunchKernelGGL(k_moe_join, dim3((n + 255) / 256), dim3(256), 0, s, part, a.dst, n, p.slices);
-    e = hipGetLastError();
-  }
+  if (e == hipSuccess && p.slices > 1) e = launch_join_slices(part, a.dst, (int64_t)a.T * a.D, p.slices, s);
   return e;
 }
 

@@ -38,7 +38,6 @@ constexpr int kMoeMaxTokens = 128;     // mixture-of-experts layer: tokens per c
 constexpr int kMoeMaxExperts = 512;    // experts,
 constexpr int kMoeMaxTopK = 16;        // experts per token,
 constexpr int64_t kMoeMaxDim = 1 << 20;  // model and hidden width
-constexpr int kF8FusedMaxLds = 65536;  // LDS bytes the fused F8 kernel may stage src1 codes in
 constexpr size_t kNoAllocScratchBytes = (size_t)64 << 20;  // mm_mul_mat_q4_0_f32_noalloc's array
 constexpr int kMmaWaves = 8;       // waves per workgroup of the skinny kernel for unaligned
                                    // weights or K % 64 != 0 (32 rows per workgroup)
@@ -132,8 +131,9 @@ enum F8Kind { F8_NONE = 0, F8_ZERO = 1, F8_FUSED = 2, F8_SKINNY = 3, F8_WIDE = 4
 
 struct F8Plan {
   int kind = F8_NONE;
-  int nt = 1, rt = 1;          // skinny, fused: tiles of 16 src1 / weight rows per wave
-  int waves = 8;               // skinny, fused: waves per workgroup (they split K)
+  int nt = 1;                  // skinny: tiles of 16 src1 rows per pass; fused: rounds of the
+                               // quantization (32 blocks of 128 each)
+  int waves = 8;               // skinny: waves per workgroup (they split K)
   int64_t grid_n = 1, grid_m = 1;
   size_t lds = 0;              // skinny, fused: LDS bytes
   int bm = 0, bn = 0;          // wide: output tile (src1 rows, weight rows)
