@@ -336,7 +336,7 @@ size_t mm_mul_mat_f8_workspace_size(int64_t M, int64_t N, int64_t K, int src1_qu
  *   gate, up: rows = F, K = D; down: rows = D, K = F; 16-byte aligned
  *   gate_scale, up_scale, down_scale: F8 only (4-byte aligned), else unused
  *   router: f32 [E][D], 16-byte aligned
- *   D, F: multiples of 32, at most 2^20; 1 <= E <= 512; 1 <= top_k <= 16, E
+ *   D, F: multiples of 32, at most 2^18; 1 <= E <= 512; 1 <= top_k <= 16, E
  * x: f32 [T][D], 16-byte aligned; dst: f32 [T][D]; 0 <= T <= 128 (larger
  *   batches amortise the weights in the products above).
  * ids (int32) and weights (f32) [T][top_k]: outputs, either may be NULL.

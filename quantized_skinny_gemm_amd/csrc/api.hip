@@ -473,6 +473,7 @@ mm_status mm_moe_f32(const mm_moe_layer* layer, const float* x, float* dst, int3
   a.T = (int)T; a.D = (int)l.D; a.F = (int)l.F; a.E = (int)l.E;
   a.top_k = l.top_k; a.norm = l.norm != 0;
   a.fold = p.fold;
+  a.up_groups = p.up_groups;
   return as_status(hip_status(launch_moe(l.type, p, a, (float*)(b + p.off_part), (hipStream_t)stream)));
 }
 

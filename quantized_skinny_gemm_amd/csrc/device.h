@@ -116,4 +116,26 @@ __device__ __forceinline__ void lds_barrier() {
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
 }
 
+// Asynchronous copies of 16 (4) bytes per lane from base + off into LDS at
+// dst + 16 (4) * lane, dst uniform.  Written as assembly without outputs, so
+// that the compiler does not drain them ahead of every LDS read: the code
+// below waits for the oldest stage only, by count (copies complete in the
+// order they were issued).
+__device__ __forceinline__ uint32_t lds_offset(const void* p) {
+  return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void*)p;
+}
+__device__ __forceinline__ void copy16(uint32_t dst, const void* base, uint32_t off) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+               :: "s"(dst), "v"(off), "s"(base) : "memory", "m0");
+}
+__device__ __forceinline__ void copy4(uint32_t dst, const void* base, uint32_t off) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2"
+               :: "s"(dst), "v"(off), "s"(base) : "memory", "m0");
+}
+// At most N of this wave's copies still under way; its LDS reads are done.
+template <int N>
+__device__ __forceinline__ void wait_copies() {
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" :: "n"(N) : "memory");
+}
+
 }  // namespace qsg

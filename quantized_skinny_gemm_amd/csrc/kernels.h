@@ -131,6 +131,7 @@ struct MoeArgs {
   uint8_t* hp;                       // split h: [T][top_k][F/32] blocks
   float* hs;                         // [T][top_k][F/32 rounded up to 4]
   int T, D, F, E, top_k, norm;
+  int up_groups;                     // gate / up: workgroups along F per expert
   int fold;                          // the selection is made by the gate / up launch
 };
 // part: slices of dst ([p.slices][T][D]; unused with one slice).

@@ -33,8 +33,14 @@
 //   row and block 128 bytes, [lane group g][hi 16 bytes | lo 16 bytes], and
 //   one scale (a row's scales padded with zeros to a multiple of 4), so that
 //   a lane's operand is two 16-byte loads and four blocks' scales are one.
-// * Work moves in units of 4 blocks (128 k); a wave holds one unit while the
-//   next one's loads are in flight.
+// * Work moves in units of 4 blocks (128 k) per wave: while one unit is
+//   computed from registers, the next one's weights are on their way to
+//   registers and its activations (512 consecutive bytes per row; e4m3
+//   weights too) to the wave's own piece of LDS, from which a lane takes its
+//   operand.  Loading operands straight from memory costs one 16-byte access
+//   per lane, since neighbouring lanes belong to different rows: the address
+//   units were 67% busy and the gate / up launch at 2.9 TB/s (32 tokens, 8
+//   experts of 4096 x 14336).
 #include "device.h"
 #include "kernels.h"
 #include "../../include/mm.h"
@@ -221,14 +227,16 @@ __global__ __launch_bounds__(512) void k_moe_select(const double* __restrict__ l
 // ---------------------------------------------------------------- weights
 
 // One 16-row tile of weights, a unit of 4 blocks of 32 k at a time.  bind():
-// expert e's matrix of N rows of K; load(): issues a unit's loads;
-// operand(j): block j as binary16, row lane % 16, in lane group order;
+// expert e's matrix of N rows of K; load(): issues a unit's loads; fetch():
+// takes what load() sent through LDS (kLds bytes at lds), or tells the
+// compiler that its loads have arrived; operand(j): block j as binary16, row lane % 16, in lane group order;
 // scale(j): its dw.
 template <int TY>
 struct Tile;
 
 template <>
 struct Tile<MM_TYPE_Q4_0R> {
+  static constexpr int kLds = 0;
   const uint8_t* base;
   uint4 c;
   uint2 d;
@@ -238,7 +246,10 @@ struct Tile<MM_TYPE_Q4_0R> {
     base = w + (e * (N / 16) + row0 / 16) * phases * kQ4RChunk + 16 * lane;
   }
   // a unit is half of a repacked chunk of 8 blocks
-  __device__ __forceinline__ void load(int u, int, int lane) {
+  __device__ __forceinline__ void fetch(const uint8_t*, int) {
+    asm volatile("" : "+v"(c.x), "+v"(c.y), "+v"(c.z), "+v"(c.w), "+v"(d.x), "+v"(d.y));
+  }
+  __device__ __forceinline__ void load(int u, int, int lane, uint32_t) {
     const uint8_t* p = base + (int64_t)(u >> 1) * kQ4RChunk;
     c = *reinterpret_cast<const uint4*>(p + 1024 * (u & 1));
     d = *reinterpret_cast<const uint2*>(p - 16 * lane + 2048 + 16 * (lane & 15) + 8 * (u & 1));
@@ -262,23 +273,42 @@ struct Tile<MM_TYPE_Q4_0R> {
   }
 };
 
+// e4m3 goes through LDS (16 rows of 128 codes, the 16-byte chunks of a row
+// permuted by (row / 2) % 8): a lane's operand is 8 bytes of its row.
 template <>
 struct Tile<MM_TYPE_F8> {
-  const uint8_t* base;
+  static constexpr int kLds = 2048;
+  const uint8_t* base;           // uniform
   const float* sc;
+  uint32_t off[2];               // the rows this lane copies
+  int chunk, K;
   uint2 c[4];
-  float d;
-  __device__ __forceinline__ void bind(const uint8_t* w, const float* s, int64_t e, int N, int K,
+  float d, dnext;
+  __device__ __forceinline__ void bind(const uint8_t* w, const float* s, int64_t e, int N, int k,
                                        int row0, int lane) {
-    const int64_t nkb = (K + 127) / 128;
-    base = w + (e * N + row0 + (lane & 15)) * K + 8 * (lane >> 4);
+    const int64_t nkb = (k + 127) / 128;
+    K = k;
+    base = w + (e * N + row0) * k;
     sc = s + (e * ((N + 127) / 128) + row0 / 128) * nkb;
-  }
-  __device__ __forceinline__ void load(int u, int nb, int) {
-    d = sc[u];
+    // piece q: rows 8 q + lane / 8, position lane % 8; (row / 2) % 8
 #pragma unroll
-    for (int j = 0; j < 4; ++j)                      // past K: the last block, with s = 0
-      c[j] = *reinterpret_cast<const uint2*>(base + 32 * (int64_t)min(4 * u + j, nb - 1));
+    for (int q = 0; q < 2; ++q) off[q] = (uint32_t)(8 * q + (lane >> 3)) * (uint32_t)k;
+    chunk = lane & 7;
+  }
+  __device__ __forceinline__ void load(int u, int, int lane, uint32_t lds) {
+    dnext = sc[u];
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      const int k = 128 * u + 16 * (chunk ^ ((4 * q + (lane >> 4)) & 7));
+      copy16(lds + 1024 * q, base, off[q] + (uint32_t)min(k, K - 16));   // past K: meets s = 0
+    }
+  }
+  __device__ __forceinline__ void fetch(const uint8_t* lds, int lane) {
+    const int r = lane & 15, g = lane >> 4;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      c[j] = *reinterpret_cast<const uint2*>(lds + 128 * r + 16 * ((2 * j + (g >> 1)) ^ ((r >> 1) & 7)) + 8 * (g & 1));
+    d = dnext;
   }
   __device__ __forceinline__ v8h operand(int j) const {
     const v2h a = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(c[j].x, 1.0f, false);
@@ -292,13 +322,18 @@ struct Tile<MM_TYPE_F8> {
 
 template <>
 struct Tile<MM_TYPE_F16> {
+  static constexpr int kLds = 0;
   const uint8_t* base;
   uint4 c[4];
   __device__ __forceinline__ void bind(const uint8_t* w, const float*, int64_t e, int N, int K,
                                        int row0, int lane) {
     base = w + 2 * ((e * N + row0 + (lane & 15)) * K + 8 * (lane >> 4));
   }
-  __device__ __forceinline__ void load(int u, int nb, int) {
+  __device__ __forceinline__ void fetch(const uint8_t*, int) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) asm volatile("" : "+v"(c[j].x), "+v"(c[j].y), "+v"(c[j].z), "+v"(c[j].w));
+  }
+  __device__ __forceinline__ void load(int u, int nb, int, uint32_t) {
 #pragma unroll
     for (int j = 0; j < 4; ++j)
       c[j] = *reinterpret_cast<const uint4*>(base + 64 * (int64_t)min(4 * u + j, nb - 1));
@@ -307,27 +342,52 @@ struct Tile<MM_TYPE_F16> {
   __device__ __forceinline__ float scale(int) const { return 1.0f; }
 };
 
-// A unit's activations: this lane's operand pieces of its row (the token
-// 4 (i16 % 4) + i16 / 4 of the pass; zeros where there is none) and the
-// scales of the NR tokens 4 r + g whose results it holds.
+// The activations of a pass of up to 4 NR tokens, a unit at a time through
+// the wave's LDS: [row][512 bytes], the 16-byte chunks of a row permuted by
+// row % 16, then the rows' scales [row][4].  Rows past the pass repeat the
+// last one, lanes of rows that are not copied read what is there: no result
+// of theirs is kept.
 template <int NR>
 struct Acts {
+  static constexpr int kLds = 4 * NR * 528;
+  const uint8_t* base;           // uniform
+  const float* sbase;
+  uint32_t off[2 * NR], soff;    // the rows this lane copies
+  int last;                      // last chunk of a row
   uint4 hi[4], lo[4];
   float4 s[NR];
-  __device__ __forceinline__ void load(const uint8_t* row, bool live, const float* const (&sc)[NR],
-                                       int u, int nb) {
+  // row_of(m): the row of base that holds token m of the pass, m < n
+  template <class F>
+  __device__ __forceinline__ void bind(const uint8_t* split, const float* scales, int nb, int n,
+                                       int lane, F row_of) {
+    base = split;
+    sbase = scales;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) hi[j] = lo[j] = make_uint4(0, 0, 0, 0);
-    if (live) {
+    for (int q = 0; q < 2 * NR; ++q)
+      off[q] = (uint32_t)row_of(min(2 * q + (lane >> 5), n - 1)) * (uint32_t)(128 * nb);
+    soff = (uint32_t)row_of(min(lane >> 2, n - 1)) * (uint32_t)((nb + 3) & ~3) + (lane & 3);
+    last = 8 * nb - 1;
+  }
+  __device__ __forceinline__ void load(int u, int n, int lane, uint32_t lds) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const uint8_t* const p = row + 128 * (int64_t)min(4 * u + j, nb - 1);
-        hi[j] = *reinterpret_cast<const uint4*>(p);
-        lo[j] = *reinterpret_cast<const uint4*>(p + 16);
+    for (int q = 0; q < 2 * NR; ++q) {
+      if (2 * q < n) {                               // uniform
+        const int chunk = (lane & 31) ^ ((2 * q + (lane >> 5)) & 15);
+        copy16(lds + 1024 * q, base, off[q] + 16 * min(32 * u + chunk, last));
       }
     }
+    if (lane < 16 * NR) copy4(lds + 2048 * NR, sbase, 4 * (soff + 4 * u));
+  }
+  __device__ __forceinline__ void fetch(const uint8_t* lds, int lane) {
+    const int g = lane >> 4, row = 4 * (lane & 3) + ((lane & 15) >> 2);
 #pragma unroll
-    for (int r = 0; r < NR; ++r) s[r] = *reinterpret_cast<const float4*>(sc[r] + 4 * u);
+    for (int j = 0; j < 4; ++j) {
+      const uint8_t* const p = lds + 512 * (row & (4 * NR - 1));
+      hi[j] = *reinterpret_cast<const uint4*>(p + 16 * ((8 * j + 2 * g) ^ (row & (4 * NR - 1))));
+      lo[j] = *reinterpret_cast<const uint4*>(p + 16 * ((8 * j + 2 * g + 1) ^ (row & (4 * NR - 1))));
+    }
+#pragma unroll
+    for (int r = 0; r < NR; ++r) s[r] = *reinterpret_cast<const float4*>(lds + 2048 * NR + 16 * (4 * r + g));
   }
   __device__ __forceinline__ float scale(int r, int j) const {
     return j == 0 ? s[r].x : j == 1 ? s[r].y : j == 2 ? s[r].z : s[r].w;
@@ -355,6 +415,52 @@ __device__ __forceinline__ void unit_product(const Acts<NR>& x, const Tile<TY> (
 #pragma unroll
       for (int r = 0; r < NR; ++r) acc[i][r] = fmaf(c[r], dw * s[r], acc[i][r]);
     }
+    __builtin_amdgcn_sched_barrier(0);               // one block's operands in registers at a time
+  }
+}
+
+// Units u, u + step, ... < end of RT tiles for one pass: acc += ...  lds: the
+// wave's staging (activations, then the tiles').  The wait at the top finds
+// exactly the current unit's loads under way; its LDS is free again once the
+// operands are in registers.
+template <int TY, int NR, int RT>
+__device__ __forceinline__ void run_units(Acts<NR>& x, Tile<TY> (&w0)[RT], int u, int end, int step,
+                                          int n, int nb, const float (&p)[NR], float (&acc)[RT][NR],
+                                          uint8_t* lds, int lane) {
+  const uint32_t at = lds_offset(lds), tat = at + Acts<NR>::kLds;
+  const auto issue = [&](Tile<TY> (&w)[RT], int v) {
+    x.load(v, n, lane, at);
+#pragma unroll
+    for (int i = 0; i < RT; ++i) w[i].load(v, nb, lane, tat + i * Tile<TY>::kLds);
+  };
+  const auto take = [&](Tile<TY> (&w)[RT]) {
+    wait_copies<0>();
+    x.fetch(lds, lane);
+#pragma unroll
+    for (int i = 0; i < RT; ++i) w[i].fetch(lds + Acts<NR>::kLds + i * Tile<TY>::kLds, lane);
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+  };
+  if (u >= end) return;
+  issue(w0, u);
+  if constexpr (Tile<TY>::kLds > 0) {
+    for (; u < end; u += step) {
+      take(w0);
+      if (u + step < end) issue(w0, u + step);
+      unit_product<TY, NR, RT>(x, w0, p, acc);
+    }
+  } else {
+    Tile<TY> w1[RT];
+#pragma unroll
+    for (int i = 0; i < RT; ++i) w1[i] = w0[i];
+    for (; u < end; u += 2 * step) {
+      take(w0);
+      if (u + step < end) issue(w1, u + step);
+      unit_product<TY, NR, RT>(x, w0, p, acc);
+      if (u + step >= end) break;
+      take(w1);
+      if (u + 2 * step < end) issue(w0, u + 2 * step);
+      unit_product<TY, NR, RT>(x, w1, p, acc);
+    }
   }
 }
 
@@ -362,87 +468,143 @@ __device__ __forceinline__ void unit_product(const Acts<NR>& x, const Tile<TY> (
 
 constexpr int kUpWaves = 8;
 
-// kTwo: the next unit's loads are issued before the current one's product
-// (two units in registers); the other form leaves that to the other waves of
-// the SIMD.  K units wave, wave + W, ... of four tiles (32 rows of gate, the same of up)
-// for one pass of up to 4 NR tokens; the partial sums go to
-// part[wave][tile][token][16].
-template <int TY, int NR, bool kTwo>
-__device__ __forceinline__ void up_pass(const MoeArgs& a, int e, int row0, const int* list, int n,
-                                        float* part, int lane, int wave) {
+// Partial sums kept apart in the join: one per wave, or one per pair of waves
+// (w, w + 4) where e4m3's staging leaves no room for eight.
+template <int TY, bool kFew>
+constexpr int up_parts() { return Tile<TY>::kLds > 0 && !kFew ? kUpWaves / 2 : kUpWaves; }
+
+// Dynamic LDS of the gate / up kernel: the waves' staging, then their partial
+// sums (before both, the logits where it makes the selection).
+template <int TY, bool kFew>
+constexpr int up_lds() {
+  return kUpWaves * (Acts<kFew ? 1 : 4>::kLds + 4 * Tile<TY>::kLds) +
+         up_parts<TY, kFew>() * 4 * (kFew ? 4 : 16) * 64;
+}
+
+// One pass of up to 4 NR tokens over all K for the row groups rg0, rg0 + step,
+// ...: the waves take units in turn, across the groups, so that a group's
+// first loads are under way while the one before is joined.  The join: partial
+// sums to part[wave][tile][token][16] (kRows tokens), added in wave order,
+// h = silu(g) u, split per block of 32 rows.
+template <int TY, int NR, int kRows>
+__device__ __forceinline__ void up_pass(const MoeArgs& a, int e, int rg0, int step, const int* list,
+                                        int n, uint8_t* lds, float* part, int lane, int wave) {
+  constexpr int W = kUpWaves, P = up_parts<TY, kRows == 4>();
+  asm volatile("" : "+v"(lane));                     // keep a pass's addresses inside the pass
   const int g = lane >> 4, i16 = lane & 15;
-  const int nb = a.D / 32, nbp = (nb + 3) & ~3, units = nbp / 4;
-  const int mine = 4 * (i16 & 3) + (i16 >> 2);
-  const bool live = mine < n;
-  const uint8_t* const row = a.xp + (int64_t)(live ? list[mine] / a.top_k : 0) * nb * 128 + 32 * g;
-  const float* sc[NR];
-  float one[NR];
+  const int nb = a.D / 32, units = (nb + 3) / 4;
+  const int nfb = a.F / 32, nfp = (nfb + 3) & ~3;
+  Acts<NR> x;
+  x.bind(a.xp, a.xs, nb, n, lane, [&](int m) { return list[m] / a.top_k; });
+  float acc[4][NR], one[NR];
 #pragma unroll
-  for (int r = 0; r < NR; ++r) {
-    sc[r] = a.xs + (int64_t)(list[min(4 * r + g, n - 1)] / a.top_k) * nbp;
-    one[r] = 1.0f;
-  }
-  float acc[4][NR];
+  for (int r = 0; r < NR; ++r) one[r] = 1.0f;
 #pragma unroll
   for (int i = 0; i < 4; ++i)
 #pragma unroll
     for (int r = 0; r < NR; ++r) acc[i][r] = 0.0f;
-  Tile<TY> w0[4];
+  const uint32_t at = lds_offset(lds), tat = at + Acts<NR>::kLds;
+  const auto issue = [&](Tile<TY> (&w)[4], int rg, int u) {
+    x.load(u, n, lane, at);
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    w0[i].bind(i < 2 ? a.gate : a.up, i < 2 ? a.gate_scale : a.up_scale, e, a.F, a.D,
-               row0 + 16 * (i & 1), lane);
-  const auto load = [&](Tile<TY> (&w)[4], Acts<NR>& x, int u) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) w[i].load(u, nb, lane);
-    x.load(row, live, sc, u, nb);
-  };
-  int u = wave;
-  Acts<NR> x0;
-  if constexpr (!kTwo) {
-    for (; u < units; u += kUpWaves) {
-      load(w0, x0, u);
-      unit_product<TY, NR, 4>(x0, w0, one, acc);
+    for (int i = 0; i < 4; ++i) {
+      w[i].bind(i < 2 ? a.gate : a.up, i < 2 ? a.gate_scale : a.up_scale, e, a.F, a.D,
+                32 * rg + 16 * (i & 1), lane);
+      w[i].load(u, nb, lane, tat + i * Tile<TY>::kLds);
     }
+  };
+  const auto take = [&](Tile<TY> (&w)[4]) {
+    wait_copies<0>();
+    x.fetch(lds, lane);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i].fetch(lds + Acts<NR>::kLds + i * Tile<TY>::kLds, lane);
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+  };
+  const auto join = [&](int rg) {
+    const auto put = [&](bool add) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int r = 0; r < NR; ++r) {
+          float* const q = part + ((wave % P * 4 + i) * kRows + 4 * r + g) * 16 + i16;
+          *q = add ? *q + acc[i][r] : acc[i][r];
+          acc[i][r] = 0.0f;
+        }
+    };
+    if (wave < P) put(false);
+    lds_barrier();
+    if constexpr (P < W) {
+      if (wave >= P) put(true);
+      lds_barrier();
+    }
+    const int tid = 64 * wave + lane, m = tid >> 5, c = tid & 31;    // 16 tokens x 32 rows
+    if (m < n) {
+      const float* const p = part + ((c >> 4) * kRows + m) * 16 + (c & 15);
+      float gs = p[0], us = p[32 * kRows];
+#pragma unroll
+      for (int v = 1; v < P; ++v) {
+        gs += p[v * 64 * kRows];
+        us += p[v * 64 * kRows + 32 * kRows];
+      }
+      const float h = gs / (1.0f + expf(-gs)) * us;
+      const float amax = half_wave_max(fabsf(h));
+      const int64_t to = list[m];
+      const float s = split_store<TY>(a.hp + (to * nfb + rg) * 128, c, h, amax);
+      if (c == 0) a.hs[to * nfp + rg] = s;
+      // the last block's workgroup also writes the row's padding scales
+      if (rg == nfb - 1 && c > 0 && rg + c < nfp) a.hs[to * nfp + rg + c] = 0.0f;
+    }
+    lds_barrier();                                   // the partial sums are read
+  };
+  if (wave >= units) {                               // no units: only the joins
+    for (int rg = rg0; rg < nfb; rg += step) join(rg);
+    return;
+  }
+  // one unit of row group rg; the next one's loads; the join after the last
+  int rg = rg0, u = wave;
+  const auto body = [&](Tile<TY> (&w)[4], Tile<TY> (&next)[4]) {
+    take(w);
+    const bool last = u + W >= units;
+    const int nrg = last ? rg + step : rg, nu = last ? wave : u + W;
+    if (nrg < nfb) issue(next, nrg, nu);
+    unit_product<TY, NR, 4>(x, w, one, acc);
+    if (last) join(rg);
+    rg = nrg;
+    u = nu;
+  };
+  Tile<TY> w0[4];
+  issue(w0, rg, u);
+  if constexpr (Tile<TY>::kLds > 0) {
+    while (rg < nfb) body(w0, w0);
   } else {
     Tile<TY> w1[4];
-    Acts<NR> x1;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) w1[i] = w0[i];
-    if (u < units) load(w0, x0, u);
-    for (; u < units; u += 2 * kUpWaves) {
-      const bool more = u + kUpWaves < units;
-      if (more) load(w1, x1, u + kUpWaves);
-      unit_product<TY, NR, 4>(x0, w0, one, acc);
-      if (!more) break;
-      if (u + 2 * kUpWaves < units) load(w0, x0, u + 2 * kUpWaves);
-      unit_product<TY, NR, 4>(x1, w1, one, acc);
+    while (rg < nfb) {
+      body(w0, w1);
+      if (rg >= nfb) break;
+      body(w1, w0);
     }
   }
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int r = 0; r < NR; ++r) part[((wave * 4 + i) * 16 + 4 * r + g) * 16 + i16] = acc[i][r];
 }
 
-// One workgroup: 32 rows of gate and the same rows of up of the blockIdx.y-th
-// expert in use, over its tokens in passes of 16.  Eight waves split K; their
-// partial tiles are added in LDS in wave order, then h = silu(g) u, split per
-// block of 32 rows.  a.fold: every workgroup ranks the logits itself (a launch less), and one
-// writes ids and weights for the next launch.
+// One workgroup: groups of 32 rows of gate and the same rows of up (four 16-row
+// tiles that share the activations), every a.up_groups-th group of the
+// blockIdx.y-th expert in use, over its tokens in passes of 16.  a.fold: every
+// workgroup ranks the logits itself (a launch less), and one writes ids and
+// weights for the next launch.
 template <int TY, bool kFew>
-__global__ __launch_bounds__(64 * kUpWaves, kFew || TY != MM_TYPE_Q4_0R ? 2 : 4) void k_moe_up(MoeArgs a) {
-  constexpr int W = kUpWaves;
-  __shared__ __attribute__((aligned(16))) float part[W * 4 * 256];
+__global__ __launch_bounds__(64 * kUpWaves, 2) void k_moe_up(MoeArgs a) {
+  constexpr int W = kUpWaves, kRows = kFew ? 4 : 16;
+  constexpr int kStage = Acts<kFew ? 1 : 4>::kLds + 4 * Tile<TY>::kLds;
+  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
   __shared__ uint16_t sids[kMoeMaxTokens * kMoeMaxTopK];
   __shared__ uint32_t bits[kMoeMaxExperts / 32];
   __shared__ uint32_t nans[kMoeMaxTokens / 32];
   __shared__ int list[kMoeMaxTokens];
   __shared__ int count;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int k = a.top_k, E = a.E, assigned = a.T * k;
   if (a.fold) {
-    double* const l = reinterpret_cast<double*>(part);
+    double* const l = reinterpret_cast<double*>(lds);
     if (tid < kMoeMaxTokens / 32) nans[tid] = 0;
     __syncthreads();
     for (int i = tid; i < a.T * E; i += 64 * W) {
@@ -500,37 +662,18 @@ __global__ __launch_bounds__(64 * kUpWaves, kFew || TY != MM_TYPE_Q4_0R ? 2 : 4)
   }
   e = __builtin_amdgcn_readfirstlane(e);
   n = __builtin_amdgcn_readfirstlane(n);
-  const int nfb = a.F / 32, nfp = (nfb + 3) & ~3;
-
-  const int rg = blockIdx.x;
+  uint8_t* const stage = lds + wave * kStage;
+  float* const part = reinterpret_cast<float*>(lds + W * kStage);
+  __syncthreads();                                   // the logits, where they were here, are read
   for (int m0 = 0; m0 < n; m0 += 16) {
-    const int rows = min(n - m0, 16);
+    const int rows = min(n - m0, 16), rg = blockIdx.x, step = a.up_groups;
     if constexpr (kFew) {
-      up_pass<TY, 1, TY != MM_TYPE_F16>(a, e, 32 * rg, list + m0, rows, part, lane, wave);
+      up_pass<TY, 1, kRows>(a, e, rg, step, list + m0, rows, stage, part, lane, wave);
     } else {
-      if (rows <= 4) up_pass<TY, 1, false>(a, e, 32 * rg, list + m0, rows, part, lane, wave);
-      else if (rows <= 8) up_pass<TY, 2, false>(a, e, 32 * rg, list + m0, rows, part, lane, wave);
-      else up_pass<TY, 4, false>(a, e, 32 * rg, list + m0, rows, part, lane, wave);
+      if (rows <= 4) up_pass<TY, 1, kRows>(a, e, rg, step, list + m0, rows, stage, part, lane, wave);
+      else if (rows <= 8) up_pass<TY, 2, kRows>(a, e, rg, step, list + m0, rows, stage, part, lane, wave);
+      else up_pass<TY, 4, kRows>(a, e, rg, step, list + m0, rows, stage, part, lane, wave);
     }
-    __syncthreads();
-    const int m = tid >> 5, c = tid & 31;          // 16 tokens x 32 rows
-    if (m < rows) {
-      const float* const p = part + (c >> 4) * 256 + m * 16 + (c & 15);
-      float gs = p[0], us = p[512];
-#pragma unroll
-      for (int v = 1; v < W; ++v) {
-        gs += p[v * 1024];
-        us += p[v * 1024 + 512];
-      }
-      const float h = gs / (1.0f + expf(-gs)) * us;
-      const float amax = half_wave_max(fabsf(h));
-      const int64_t at = list[m0 + m];
-      const float s = split_store<TY>(a.hp + (at * nfb + rg) * 128, c, h, amax);
-      if (c == 0) a.hs[at * nfp + rg] = s;
-      // the last block's workgroup also writes the row's padding scales
-      if (rg == nfb - 1 && c > 0 && rg + c < nfp) a.hs[at * nfp + rg + c] = 0.0f;
-    }
-    __syncthreads();
   }
 }
 
@@ -538,11 +681,12 @@ __global__ __launch_bounds__(64 * kUpWaves, kFew || TY != MM_TYPE_Q4_0R ? 2 : 4)
 
 // A job is one expert with up to 16 of the tokens that use it.
 struct Jobs {
-  int e[kMoeMaxExperts + kMoeMaxTokens * kMoeMaxTopK / 16];
+  uint16_t e[kMoeMaxExperts + kMoeMaxTokens * kMoeMaxTopK / 16];
   uint16_t first[kMoeMaxExperts + kMoeMaxTokens * kMoeMaxTopK / 16];   // in order[]
   uint16_t rows[kMoeMaxExperts + kMoeMaxTokens * kMoeMaxTopK / 16];
   uint16_t order[kMoeMaxTokens * kMoeMaxTopK];       // assignments, grouped by expert
-  int cnt[kMoeMaxExperts], at[kMoeMaxExperts], job0[kMoeMaxExperts];
+  int cnt[kMoeMaxExperts], at[kMoeMaxExperts];
+  uint16_t job0[kMoeMaxExperts];
   int count;
 };
 
@@ -554,7 +698,7 @@ __device__ __forceinline__ void make_jobs(Jobs& js, const int* ids, int T, int a
   const int tid = threadIdx.x, nt = blockDim.x;
   if (T == 1) {                                      // every assignment is a job
     if (tid < assigned) {
-      js.e[tid] = ids[tid];
+      js.e[tid] = (uint16_t)ids[tid];
       js.first[tid] = js.order[tid] = (uint16_t)tid;
       js.rows[tid] = 1;
     }
@@ -578,7 +722,7 @@ __device__ __forceinline__ void make_jobs(Jobs& js, const int* ids, int T, int a
       }
       if (b + lane < E) {
         js.at[b + lane] = base + sc - c;
-        js.job0[b + lane] = jobs + sj - j;
+        js.job0[b + lane] = (uint16_t)(jobs + sj - j);
       }
       base += __shfl(sc, 63, 64);
       jobs += __shfl(sj, 63, 64);
@@ -589,7 +733,7 @@ __device__ __forceinline__ void make_jobs(Jobs& js, const int* ids, int T, int a
   for (int e = tid; e < E; e += nt) {
     const int c = js.cnt[e], first = js.at[e];
     for (int j = 0; 16 * j < c; ++j) {
-      js.e[js.job0[e] + j] = e;
+      js.e[js.job0[e] + j] = (uint16_t)e;
       js.first[js.job0[e] + j] = (uint16_t)(first + 16 * j);
       js.rows[js.job0[e] + j] = (uint16_t)min(c - 16 * j, 16);
     }
@@ -603,46 +747,23 @@ __device__ __forceinline__ void make_jobs(Jobs& js, const int* ids, int T, int a
 // to the wave's sums[token][16 RT].
 template <int TY, int NR, int RT>
 __device__ __forceinline__ void down_job(const MoeArgs& a, int e, int row0, const uint16_t* order,
-                                         int n, int u0, int u1, float* sums, int lane) {
+                                         int n, int u0, int u1, float* sums, uint8_t* lds, int lane) {
+  asm volatile("" : "+v"(lane));                     // keep a job's addresses inside the job
   const int g = lane >> 4, i16 = lane & 15;
-  const int nb = a.F / 32, nbp = (nb + 3) & ~3;
-  const int mine = 4 * (i16 & 3) + (i16 >> 2);
-  const bool live = mine < n;
-  const uint8_t* const row = a.hp + (int64_t)(live ? order[mine] : 0) * nb * 128 + 32 * g;
-  const float* sc[NR];
-  float p[NR];
+  const int nb = a.F / 32;
+  Acts<NR> x;
+  x.bind(a.hp, a.hs, nb, n, lane, [&](int m) { return (int)order[m]; });
+  float acc[RT][NR], p[NR];
 #pragma unroll
-  for (int r = 0; r < NR; ++r) {
-    const int at = order[min(4 * r + g, n - 1)];
-    sc[r] = a.hs + (int64_t)at * nbp;
-    p[r] = a.weights[at];
-  }
-  float acc[RT][NR];
+  for (int r = 0; r < NR; ++r) p[r] = a.weights[order[min(4 * r + g, n - 1)]];
 #pragma unroll
   for (int i = 0; i < RT; ++i)
 #pragma unroll
     for (int r = 0; r < NR; ++r) acc[i][r] = 0.0f;
-  Tile<TY> w0[RT], w1[RT];
-  Acts<NR> x0, x1;
+  Tile<TY> w[RT];
 #pragma unroll
-  for (int i = 0; i < RT; ++i) {
-    w0[i].bind(a.down, a.down_scale, e, a.D, a.F, row0 + 16 * i, lane);
-    w1[i] = w0[i];
-  }
-  const auto load = [&](Tile<TY> (&w)[RT], Acts<NR>& x, int u) {
-#pragma unroll
-    for (int i = 0; i < RT; ++i) w[i].load(u, nb, lane);
-    x.load(row, live, sc, u, nb);
-  };
-  load(w0, x0, u0);
-  for (int u = u0; u < u1; u += 2) {
-    const bool more = u + 1 < u1;
-    if (more) load(w1, x1, u + 1);
-    unit_product<TY, NR, RT>(x0, w0, p, acc);
-    if (!more) break;
-    if (u + 2 < u1) load(w0, x0, u + 2);
-    unit_product<TY, NR, RT>(x1, w1, p, acc);
-  }
+  for (int i = 0; i < RT; ++i) w[i].bind(a.down, a.down_scale, e, a.D, a.F, row0 + 16 * i, lane);
+  run_units<TY, NR, RT>(x, w, u0, u1, 1, n, nb, p, acc, lds, lane);
 #pragma unroll
   for (int r = 0; r < NR; ++r) {
     if (4 * r + g < n) {
@@ -659,7 +780,9 @@ __device__ __forceinline__ void down_job(const MoeArgs& a, int e, int row0, cons
 template <int TY, int RT, int W, bool kFew>
 __global__ __launch_bounds__(64 * W) void k_moe_down(MoeArgs a, float* __restrict__ out) {
   __shared__ Jobs js;
-  extern __shared__ __attribute__((aligned(16))) float sums[];   // [W][T][16 RT]
+  constexpr int kStage = Acts<kFew ? 1 : 4>::kLds + RT * Tile<TY>::kLds;
+  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];   // the waves' staging, then
+  float* const sums = reinterpret_cast<float*>(lds + W * kStage); // [W][T][16 RT]
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int per = a.T * 16 * RT;
   for (int i = tid; i < W * per; i += 64 * W) sums[i] = 0.0f;
@@ -675,9 +798,10 @@ __global__ __launch_bounds__(64 * W) void k_moe_down(MoeArgs a, float* __restric
     const int n = __builtin_amdgcn_readfirstlane((int)js.rows[j]);
     const uint16_t* const order = js.order + js.first[j];
     float* const s = sums + wave * per;
-    if (kFew || n <= 4) down_job<TY, 1, RT>(a, e, row0, order, n, u0, u1, s, lane);
-    else if (n <= 8) down_job<TY, 2, RT>(a, e, row0, order, n, u0, u1, s, lane);
-    else down_job<TY, 4, RT>(a, e, row0, order, n, u0, u1, s, lane);
+    if constexpr (kFew) down_job<TY, 1, RT>(a, e, row0, order, n, u0, u1, s, lds + wave * kStage, lane);
+    else if (n <= 4) down_job<TY, 1, RT>(a, e, row0, order, n, u0, u1, s, lds + wave * kStage, lane);
+    else if (n <= 8) down_job<TY, 2, RT>(a, e, row0, order, n, u0, u1, s, lds + wave * kStage, lane);
+    else down_job<TY, 4, RT>(a, e, row0, order, n, u0, u1, s, lds + wave * kStage, lane);
     at += u1 - u0;
   }
   __syncthreads();
@@ -692,12 +816,26 @@ __global__ __launch_bounds__(64 * W) void k_moe_down(MoeArgs a, float* __restric
 
 template <int TY, int RT, int W, bool kFew>
 hipError_t down(const MoePlan& p, const MoeArgs& a, float* out, hipStream_t s) {
-  const int lds = W * a.T * 16 * RT * 4;
+  const int lds = W * (Acts<kFew ? 1 : 4>::kLds + RT * Tile<TY>::kLds + a.T * 16 * RT * 4);
+  if (lds > kMoeMaxLds) return hipErrorInvalidValue;  // the plan keeps T RT small enough
   auto* const kern = k_moe_down<TY, RT, W, kFew>;
   static std::atomic<uint64_t> raised{0};            // devices whose limit is set already
-  const hipError_t e = raise_lds(reinterpret_cast<const void*>(kern), kMoeMaxSums, raised);
+  const hipError_t e = raise_lds(reinterpret_cast<const void*>(kern), kMoeMaxLds, raised);
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL(kern, dim3(a.D / (16 * RT), p.slices), dim3(64 * W), lds, s, a, out);
+  return hipGetLastError();
+}
+
+template <int TY, bool kFew>
+hipError_t up(dim3 grid, const MoeArgs& a, hipStream_t s) {
+  constexpr int lds = up_lds<TY, kFew>();
+  auto* const kern = k_moe_up<TY, kFew>;
+  if (lds > 65536) {
+    static std::atomic<uint64_t> raised{0};
+    const hipError_t e = raise_lds(reinterpret_cast<const void*>(kern), lds, raised);
+    if (e != hipSuccess) return e;
+  }
+  hipLaunchKernelGGL(kern, grid, dim3(64 * kUpWaves), lds, s, a);
   return hipGetLastError();
 }
 
@@ -716,15 +854,13 @@ hipError_t run(const MoePlan& p, const MoeArgs& a, float* part, hipStream_t s) {
     if (e != hipSuccess) return e;
   }
   const int assigned = a.T * a.top_k;
-  const dim3 grid(a.F / 32 + (a.fold ? 1 : 0), assigned < a.E ? assigned : a.E);
+  const dim3 grid(a.up_groups + (a.fold ? 1 : 0), assigned < a.E ? assigned : a.E);
   const bool few = a.T <= kMoeFewTokens;
-  if (few) hipLaunchKernelGGL((k_moe_up<TY, true>), grid, dim3(64 * kUpWaves), 0, s, a);
-  else hipLaunchKernelGGL((k_moe_up<TY, false>), grid, dim3(64 * kUpWaves), 0, s, a);
-  e = hipGetLastError();
+  e = few ? up<TY, true>(grid, a, s) : up<TY, false>(grid, a, s);
   if (e != hipSuccess) return e;
   float* const out = p.slices > 1 ? part : a.dst;
   if (few) e = down<TY, 1, 16, true>(p, a, out, s);
-  else if (p.rt == 4) e = down<TY, 4, 8, false>(p, a, out, s);
+  else if (TY != MM_TYPE_F8 && p.rt == 4) e = down<TY, TY == MM_TYPE_F8 ? 1 : 4, 8, false>(p, a, out, s);
   else if (p.rt == 2) e = down<TY, 2, 8, false>(p, a, out, s);
   else e = down<TY, 1, 8, false>(p, a, out, s);
   if (e == hipSuccess && p.slices > 1) e = launch_join_slices(part, a.dst, (int64_t)a.T * a.D, p.slices, s);

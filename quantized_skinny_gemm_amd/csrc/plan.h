@@ -37,7 +37,7 @@ constexpr int64_t kF8MaxK = 1 << 23;   // F8 kernels: 32-bit byte offsets over a
 constexpr int kMoeMaxTokens = 128;     // mixture-of-experts layer: tokens per call,
 constexpr int kMoeMaxExperts = 512;    // experts,
 constexpr int kMoeMaxTopK = 16;        // experts per token,
-constexpr int64_t kMoeMaxDim = 1 << 20;  // model and hidden width
+constexpr int64_t kMoeMaxDim = 1 << 18;  // model and hidden width (32-bit offsets into split h)
 constexpr size_t kNoAllocScratchBytes = (size_t)64 << 20;  // mm_mul_mat_q4_0_f32_noalloc's array
 constexpr int kMmaWaves = 8;       // waves per workgroup of the skinny kernel for unaligned
                                    // weights or K % 64 != 0 (32 rows per workgroup)
@@ -155,9 +155,10 @@ int validate_f8_quantize(const void* x, const void* codes, const void* scales, i
 
 // Plan of the mixture-of-experts layer (moe.hip).
 constexpr int kMoeFewTokens = 4;      // up to this many tokens: kernels for passes of 4
-constexpr int kMoeMaxSums = 131072;    // LDS bytes of the down product's per-wave sums
+constexpr int kMoeMaxLds = 150528;     // dynamic LDS of the down kernel (160 KB less its static part)
 struct MoePlan {
   bool fold = false;       // the selection is made by the gate / up launch
+  int up_groups = 1;       // gate / up: workgroups along F per expert
   int rt = 1, slices = 1;  // down: 16-row tiles per workgroup, workgroups sharing a tile's sum
   size_t off_logits = 0, off_ids = 0, off_weights = 0, off_xp = 0, off_xs = 0, off_hp = 0, off_hs = 0;
   size_t off_part = 0;
