@@ -98,7 +98,7 @@ __device__ __forceinline__ float half_wave_max(float v) {
 // Logits in fp64 (the products of two fp32 values are exact there): the
 // order of close logits decides which experts run, so it must not depend on
 // the summation order.  One workgroup per expert and TT tokens; the
-// workgroups past E split x, 32 blocks of 32 values of the TT tokens each.
+// workgroups past E split x, 8 blocks of 32 values of the TT tokens each.
 template <int TY, int TT>
 __global__ __launch_bounds__(256) void k_moe_router(const float* __restrict__ x,
                                                     const float* __restrict__ router,
@@ -110,20 +110,19 @@ __global__ __launch_bounds__(256) void k_moe_router(const float* __restrict__ x,
   const int t0 = blockIdx.y * TT;
   if ((int)blockIdx.x >= E) {
     const int nb = D / 32, nbp = (nb + 3) & ~3, c = tid & 31;
+    const int b = ((int)blockIdx.x - E) * 8 + (tid >> 5);              // per half wave
+    if (b >= nbp) return;
+    float v[TT];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int b = ((int)blockIdx.x - E) * 32 + (tid >> 5) + 8 * i;   // per half wave
+    for (int j = 0; j < TT; ++j)
+      v[j] = b < nb ? x[(int64_t)min(t0 + j, T - 1) * D + 32 * b + c] : 0.0f;
 #pragma unroll
-      for (int j = 0; j < TT; ++j) {
-        const int t = t0 + j;
-        if (t >= T || b >= nbp) continue;
-        float s = 0.0f;
-        if (b < nb) {
-          const float v = x[(int64_t)t * D + 32 * b + c];
-          s = split_store<TY>(xp + ((int64_t)t * nb + b) * 128, c, v, half_wave_max(fabsf(v)));
-        }
-        if (c == 0) xs[(int64_t)t * nbp + b] = s;
-      }
+    for (int j = 0; j < TT; ++j) {
+      const int t = t0 + j;
+      if (t >= T) break;
+      float s = 0.0f;
+      if (b < nb) s = split_store<TY>(xp + ((int64_t)t * nb + b) * 128, c, v[j], half_wave_max(fabsf(v[j])));
+      if (c == 0) xs[(int64_t)t * nbp + b] = s;
     }
     return;
   }
@@ -690,9 +689,9 @@ struct Jobs {
   int count;
 };
 
-// Groups the assignments by expert.  Within an expert the order is that of
-// the atomics, which no result depends on: a token's contributions are added
-// expert by expert, wherever in a job's rows it sits.
+// Groups the assignments by expert, in ascending order within one (the order
+// decides which job a token of a much used expert falls into, and with it how
+// the waves cut its sum).
 __device__ __forceinline__ void make_jobs(Jobs& js, const int* ids, int T, int assigned, int E,
                                           int lane, int wave) {
   const int tid = threadIdx.x, nt = blockDim.x;
@@ -739,7 +738,24 @@ __device__ __forceinline__ void make_jobs(Jobs& js, const int* ids, int T, int a
     }
   }
   __syncthreads();
-  for (int i = tid; i < assigned; i += nt) js.order[atomicAdd(&js.at[ids[i]], 1)] = (uint16_t)i;
+  if (wave == 0) {
+    // 64 at a time: the lanes of the same expert by one vote per bit of its index
+    for (int b = 0; b < assigned; b += 64) {
+      const bool in = b + lane < assigned;
+      const int e = in ? ids[b + lane] : 0;
+      uint64_t same = __ballot(in);
+#pragma unroll
+      for (int bit = 1; bit < kMoeMaxExperts; bit <<= 1) {
+        const uint64_t v = __ballot((e & bit) != 0);
+        same &= (e & bit) ? v : ~v;
+      }
+      if (in) {
+        const int ahead = __popcll(same & ((1ull << lane) - 1)), at = js.at[e];
+        js.order[at + ahead] = (uint16_t)(b + lane);
+        if (ahead == 0) js.at[e] = at + __popcll(same);
+      }
+    }
+  }
   __syncthreads();
 }
 
@@ -841,7 +857,7 @@ hipError_t up(dim3 grid, const MoeArgs& a, hipStream_t s) {
 
 template <int TY>
 hipError_t run(const MoePlan& p, const MoeArgs& a, float* part, hipStream_t s) {
-  const int splits = (a.D / 32 + 31) / 32;
+  const int splits = (((a.D / 32 + 3) & ~3) + 7) / 8;
   if (a.T == 1)
     hipLaunchKernelGGL((k_moe_router<TY, 1>), dim3(a.E + splits, 1), dim3(256), 0, s, a.x, a.router, a.logits, a.xp, a.xs, a.T, a.D, a.E);
   else

@@ -193,6 +193,20 @@ def test_graph_streams_and_rows_behind_the_batch(kind, t):
     assert all(torch.equal(y, want[0]) for ys in got for y in ys)
 
 
+@pytest.mark.parametrize("kind", KINDS)
+def test_much_used_experts_give_the_same_bits_every_time(kind):
+    """128 tokens on 4 experts, top 2 (about 64 tokens an expert, several jobs each): eight calls, one result."""
+    import torch
+    say("moe determinism", kind)
+    qs = _qs()
+    m = Layer(kind, 128, 256, 288, 4, 2, 3)
+    x = to_dev(m.x)
+    want = qs.moe_f32(m.layer, x)[0].clone()
+    m.check(qs.moe_f32(m.layer, x), what=kind)
+    for _ in range(7):
+        assert torch.equal(qs.moe_f32(m.layer, x)[0], want)
+
+
 def test_decode_step_quantize_project_route_and_project_again():
     """The operators as a decode step uses them: projections with e4m3 weights on an activation quantized once,
     the layer with e4m3 experts, the output projection; against the float64 composition."""
