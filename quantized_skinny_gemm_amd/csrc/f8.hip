@@ -85,11 +85,11 @@ __device__ __forceinline__ v8h widen(uint32_t lo, uint32_t hi) {
 // ---------------------------------------------------------------- quantizer
 
 // 1 x 128 blocks: 16 lanes per block, one 32-byte load and one 8-byte store
-// per lane.  Bound: HBM (5 bytes per value).
+// per lane; rows of codes `pitch` apart (K, or whole blocks).  Bound: HBM (5 bytes per value).
 __global__ __launch_bounds__(256) void k_f8_quantize_rows(const float* __restrict__ x,
                                                           uint8_t* __restrict__ codes,
                                                           float* __restrict__ scales, int K,
-                                                          int nkb, int64_t nblocks) {
+                                                          int pitch, int nkb, int64_t nblocks) {
   const int i = threadIdx.x & 15;
   for (int64_t blk = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4); blk < nblocks;
        blk += (int64_t)gridDim.x * 16) {            // whole groups of 16 lanes
@@ -102,45 +102,21 @@ __global__ __launch_bounds__(256) void k_f8_quantize_rows(const float* __restric
     }
     float d;
     const uint2 c = f8_row_block(a, b, d);
-    if (k < K) *reinterpret_cast<uint2*>(codes + row * K + k) = c;
+    if (k < pitch) *reinterpret_cast<uint2*>(codes + row * pitch + k) = c;   // past K: zeros
     if (i == 0) scales[blk] = d;
   }
 }
 
-// The same codes as binary16 values for the tiled product, rows padded with
-// zeros to whole blocks.
-__global__ __launch_bounds__(256) void k_f8_quantize_rows_f16(const float* __restrict__ x,
-                                                              uint16_t* __restrict__ values,
-                                                              float* __restrict__ scales, int K,
-                                                              int nkb, int64_t nblocks) {
-  const int i = threadIdx.x & 15;
-  for (int64_t blk = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4); blk < nblocks;
-       blk += (int64_t)gridDim.x * 16) {
-    const int64_t row = blk / nkb;
-    const int k = (int)(blk - row * nkb) * kBlk + 8 * i;
-    float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
-    if (k < K) {
-      const float4* p = reinterpret_cast<const float4*>(x + row * K + k);
-      a = p[0]; b = p[1];
-    }
-    float d;
-    const uint2 c = f8_row_block(a, b, d);
-    *reinterpret_cast<v8h*>(values + blk * kBlk + 8 * i) = widen(c.x, c.y);
-    if (i == 0) scales[blk] = d;
-  }
-}
-
-// Codes given by the caller in that form, 16 per thread.
-__global__ __launch_bounds__(256) void k_f8_widen(const uint8_t* __restrict__ codes,
-                                                  uint16_t* __restrict__ values, int K, int nkb,
-                                                  int64_t pieces) {
+// Codes given by the caller as rows of whole blocks, zeros past K, 16 bytes
+// per thread (for the tiled product, where K ends inside a block).
+__global__ __launch_bounds__(256) void k_f8_pad(const uint8_t* __restrict__ codes,
+                                                uint8_t* __restrict__ rows, int K, int nkb,
+                                                int64_t pieces) {
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < pieces; i += 256 * (int64_t)gridDim.x) {
     const int64_t row = i / (8 * nkb);
     const int k = (int)(i - row * 8 * nkb) * 16;
-    const uint4 c = k < K ? *reinterpret_cast<const uint4*>(codes + row * K + k) : make_uint4(0, 0, 0, 0);
-    v8h* const p = reinterpret_cast<v8h*>(values + 16 * i);
-    p[0] = widen(c.x, c.y);
-    p[1] = widen(c.z, c.w);
+    *reinterpret_cast<uint4*>(rows + 16 * i) =
+        k < K ? *reinterpret_cast<const uint4*>(codes + row * K + k) : make_uint4(0, 0, 0, 0);
   }
 }
 
@@ -405,41 +381,51 @@ __global__ __launch_bounds__(512) void k_f8_fused(
 
 // ---------------------------------------------------------------- product, many src1 rows
 
+template <int V>
+struct Int { static constexpr int value = V; };
+
 constexpr int STAGES = 4;      // (8 for the 64-row tiles measured no faster)
 
 // Output tile of BN weight rows x BM src1 rows per workgroup, half a block of
-// 128 k per stage, STAGES stages in LDS, copied there straight from memory: the
-// weights as e4m3 codes, src1 as binary16 (widened once by INIT, so that the
-// vector units only widen the weights).  A wave holds 2 x 2 tiles of 32 x 32.
+// 128 k per stage, STAGES stages in LDS, both operands copied there straight
+// from memory as codes and widened in registers.  (src1 widened once by INIT,
+// binary16 in LDS, spares the widening and costs twice the copies' bytes:
+// 14336 x 4096, M = 256 / 512 57.3 / 82.0 us against 54.7 / 81.1.)
 //
 // A block is eight steps of 16 k (q), four to a stage; each MFMA adds to the
-// block dot c, and the fp32 sums take c * (dw * ds).  Operands are read one q
-// ahead.  The one
-// barrier per stage stands before its last q's MFMAs: there every wave has
-// read the whole stage, so the copy of the stage STAGES further can start, and
-// the next stage has arrived, so its first operands are read behind those
-// MFMAs.
+// block dot c, and the fp32 sums take c * (dw * ds).  Operands are read two
+// steps at a time, ahead of the products.  The one barrier per stage stands
+// before its last q's MFMAs: there every wave has read the whole stage, so the
+// copy of the stage STAGES further can start, and the next stage has arrived,
+// so its first operands are read behind those MFMAs.
 //
-// In LDS a row's 16-byte chunks are permuted so that the 16 rows of an
-// operand read lie in different banks: chunk ^ (row / 4) % 4 of the 4 of a
-// weight row's half block, chunk ^ (row / 2) % 8 of the 8 of a src1 row's.
-// Lane half h of an MFMA holds k 32 p + 16 h + 8 (q % 2) .. + 7, p = q / 2: one
-// chunk of codes serves two q.
+// In LDS a row's four 16-byte chunks (of half a block) are permuted by
+// (row / 4) % 4, so that the 16 rows of an operand read lie in different
+// banks.  Lane half h of an MFMA holds k 32 p + 16 h + 8 (q % 2) .. + 7,
+// p = q / 2: one chunk serves two q.
+//
+// What bounds it, at 512 x 128256 x 4096 (128 x 256 tiles): without the copies,
+// the widening, the scaling and the barriers the same MFMAs take 407 us
+// (1320 TFLOP/s, what the card's power leaves of the matrix cores; a library
+// product of 8192^3 in binary16 reaches 1285), copies back in 490 to 520, all
+// of it 640.  A stage's 24 KB per workgroup come from L2 (81% hits).
 template <int BM, int BN, int WAVES_M, int WAVES_N>
 __global__ __launch_bounds__(64 * WAVES_M * WAVES_N, 1) void k_f8_wide(
-    const uint8_t* __restrict__ w, const float* __restrict__ wsc, const uint16_t* __restrict__ a,
+    const uint8_t* __restrict__ w, const float* __restrict__ wsc, const uint8_t* __restrict__ a,
     const float* __restrict__ asc, int M, int N, int K, float* __restrict__ dst, int tiles_m,
     int tiles, int split, int kchunk) {
   constexpr int NW = WAVES_M * WAVES_N, HB = kBlk / 2;         // k per stage
   constexpr int WTM = BM / WAVES_M, WTN = BN / WAVES_N;
   constexpr int TM = WTM / 32, TN = WTN / 32;
-  constexpr int kA = BN * HB, kS = kA + BM * 2 * HB;           // stage: weights, src1, its scales
+  constexpr int kA = BN * HB, kS = kA + BM * HB;               // stage: weights, src1, its scales
   constexpr int STAGE = kS + BM * 4;
-  constexpr int WL = BN / 16 / NW, AL = BM / 8 / NW;  // 1 KB pieces per wave: 16 weight, 8 src1 rows
+  // pieces of 16 rows, 1 KB, per wave (with fewer src1 pieces than waves, the
+  // first ones copy them)
+  constexpr int WL = BN / 16 / NW, AP = BM / 16, AL = (AP + NW - 1) / NW;
   constexpr int kCopies = WL + AL + 1;
   static_assert((STAGES & (STAGES - 1)) == 0 && (STAGES - 1) * kCopies < 64, "wait counts");
   static_assert(kBlk % WTN == 0, "one weight scale per wave and stage");
-  static_assert(BN % (16 * NW) == 0 && BM % (8 * NW) == 0 && BM % 64 == 0 && NW % 2 == 0, "whole pieces");
+  static_assert(BN % (16 * NW) == 0 && (AP % NW == 0 || AP < NW) && BM % 64 == 0 && NW % 2 == 0, "whole pieces");
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
 
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -455,16 +441,16 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N, 1) void k_f8_wide(
 
   // this lane's part of each piece
   const uint8_t* const wbase = w + (int64_t)n0 * K;
-  const uint16_t* const abase = a + (int64_t)m0 * nkb * kBlk;
-  const int wchunk = (lane & 3) ^ ((lane >> 4) & 3);
-  const int achunk = (lane & 7) ^ ((4 * (wave & 1) + (lane >> 4)) & 7);
+  const bool has_a = AP >= NW || wave < AP;          // uniform
+  const uint8_t* const abase = a + (int64_t)m0 * nkb * kBlk;
+  const int chunk = (lane & 3) ^ ((lane >> 4) & 3);
   uint32_t woff[WL], aoff[AL];
 #pragma unroll
   for (int i = 0; i < WL; ++i)
     woff[i] = (uint32_t)min((i * NW + wave) * 16 + (lane >> 2), N - 1 - n0) * (uint32_t)K;
 #pragma unroll
   for (int i = 0; i < AL; ++i)
-    aoff[i] = (uint32_t)min((i * NW + wave) * 8 + (lane >> 3), M - 1 - m0) * (uint32_t)nkb * (2 * kBlk);
+    aoff[i] = (uint32_t)min((i * NW + wave) * 16 + (lane >> 2), M - 1 - m0) * (uint32_t)nkb * kBlk;
   // every wave issues the same number of copies (the rows' scales are copied
   // by several waves, to the same place)
   const int sm = (wave % (BM / 64)) * 64;
@@ -476,13 +462,12 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N, 1) void k_f8_wide(
     const int k0 = kb0 * kBlk + s * HB;
     // past a weight row: its own first codes, which meet the zeros that src1
     // is padded with (if one is a NaN, so is the whole row's result)
-    uint32_t kw = k0 + wchunk * 16;
-    const uint32_t ka = k0 + achunk * 8;
-    if ((int)kw >= K) kw = 0;
+    const uint32_t ka = k0 + chunk * 16, kw = (int)ka < K ? ka : 0;
 #pragma unroll
     for (int i = 0; i < WL; ++i) copy16(base + (i * NW + wave) * 1024, wbase, woff[i] + kw);
 #pragma unroll
-    for (int i = 0; i < AL; ++i) copy16(base + kA + (i * NW + wave) * 1024, abase, aoff[i] + 2 * ka);
+    for (int i = 0; i < AL; ++i)
+      if (has_a) copy16(base + kA + (i * NW + wave) * 1024, abase, aoff[i] + ka);
     copy4(base + kS + 4 * sm, sbase, 4 * (soff + kb0 + (s >> 1)));
   };
   const int nrow = min(n0 + wn * WTN, N - 1);
@@ -496,27 +481,28 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N, 1) void k_f8_wide(
 #pragma unroll
       for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
 
-  const int wrow = (wn * WTN + l32) * HB, arow = kA + (wm * WTM + l32) * 2 * HB;
-  const int wx = (l32 >> 2) & 3, ax = (l32 >> 1) & 7;
-  uint4 wr[2][TN];
-  v8h av[2][TM];
-  // the operands of step q (0..3) of a stage into register set q % 2 (weights:
-  // of p = q / 2)
-  auto read = [&](const uint8_t* base, int q) {
-    if (q % 2 == 0) {
+  const int wrow = (wn * WTN + l32) * HB, arow = kA + (wm * WTM + l32) * HB;
+  const int x4 = (l32 >> 2) & 3;
+  uint4 wr[2][TN], ar[2][TM];
+  // the operands of steps 2 p and 2 p + 1 (p = 0, 1) of a stage
+  auto read = [&](const uint8_t* base, int p) {
 #pragma unroll
-      for (int i = 0; i < TN; ++i)
-        wr[(q / 2) % 2][i] = *reinterpret_cast<const uint4*>(base + wrow + 32 * i * HB + 16 * ((q + h) ^ wx));
-    }
+    for (int i = 0; i < TN; ++i)
+      wr[p][i] = *reinterpret_cast<const uint4*>(base + wrow + 32 * i * HB + 16 * ((2 * p + h) ^ x4));
 #pragma unroll
     for (int j = 0; j < TM; ++j)
-      av[q % 2][j] = *reinterpret_cast<const v8h*>(base + arow + 64 * j * HB + 16 * ((4 * (q / 2) + 2 * h + q % 2) ^ ax));
+      ar[p][j] = *reinterpret_cast<const uint4*>(base + arow + 32 * j * HB + 16 * ((2 * p + h) ^ x4));
   };
 
 #pragma unroll
   for (int s = 0; s < STAGES; ++s)
     if (s < s1) copy_stage(s);
-  if (s1 >= STAGES) wait_copies<(STAGES - 1) * kCopies>();
+  // wait: all but the youngest S stages' copies of this wave
+  const auto wait_stages = [&](auto S) {
+    if (has_a) wait_copies<decltype(S)::value * kCopies>();
+    else wait_copies<decltype(S)::value * (kCopies - AL)>();
+  };
+  if (s1 >= STAGES) wait_stages(Int<STAGES - 1>{});
   else wait_copies<0>();
   __builtin_amdgcn_s_barrier();
   read(lds, 0);
@@ -529,11 +515,10 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N, 1) void k_f8_wide(
     for (int q = 0; q < 8; ++q) {
       const int st = s + q / 4;                      // stage of this q
       const uint8_t* const base = lds + (st % STAGES) * STAGE;
-      if (q % 4 < 3) {
-        read(base, q % 4 + 1);
-      } else {
+      if (q % 4 == 1) read(base, 1);
+      if (q % 4 == 3) {
         // the next stage is here and this wave's reads of this one are done
-        if (st + STAGES - 1 < s1) wait_copies<(STAGES - 2) * kCopies>();
+        if (st + STAGES - 1 < s1) wait_stages(Int<STAGES - 2>{});
         else wait_copies<0>();
         __builtin_amdgcn_s_barrier();
         if (st + STAGES < s1) copy_stage(st + STAGES);
@@ -546,6 +531,12 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N, 1) void k_f8_wide(
         for (int j = 0; j < TM; ++j) sc[j] = sw * ss[32 * j];
         sw = wscr[min(kb0 + s / 2 + 1, nkb - 1)];
       }
+      v8h av[TM];
+#pragma unroll
+      for (int j = 0; j < TM; ++j) {
+        const uint4 v = ar[(q / 2) % 2][j];
+        av[j] = q % 2 == 0 ? widen(v.x, v.y) : widen(v.z, v.w);
+      }
 #pragma unroll
       for (int i = 0; i < TN; ++i) {
         const uint4 v = wr[(q / 2) % 2][i];
@@ -556,7 +547,7 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N, 1) void k_f8_wide(
 #pragma unroll
             for (int r = 0; r < 16; ++r) c[i][j][r] = 0.0f;
           }
-          c[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(wv, av[q % 2][j], c[i][j], 0, 0, 0);
+          c[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(wv, av[j], c[i][j], 0, 0, 0);
         }
       }
     }
@@ -626,13 +617,14 @@ hipError_t launch_join_slices(const float* part, float* dst, int64_t n, int slic
 }
 
 hipError_t launch_f8_quantize(const float* x, uint8_t* codes, float* scales, int64_t nrows,
-                              int64_t k, int block_rows, hipStream_t s) {
+                              int64_t k, int block_rows, hipStream_t s, int64_t pitch) {
   const int64_t nkb = (k + kBlk - 1) / kBlk;
   if (block_rows == 1) {
     const int64_t nblocks = nrows * nkb;
     const int64_t grid = (nblocks + 15) / 16;
     hipLaunchKernelGGL(k_f8_quantize_rows, dim3((unsigned)(grid < kMaxGridX ? grid : kMaxGridX)),
-                       dim3(256), 0, s, x, codes, scales, (int)k, (int)nkb, nblocks);
+                       dim3(256), 0, s, x, codes, scales, (int)k, (int)(pitch ? pitch : k), (int)nkb,
+                       nblocks);
   } else {
     const int64_t grid = (nrows + kBlk - 1) / kBlk * nkb;
     hipLaunchKernelGGL(k_f8_quantize_tiles, dim3((unsigned)grid), dim3(256), 0, s, x, codes,
@@ -660,9 +652,9 @@ hipError_t fused(const F8Plan& p, const float* x, const uint8_t* w, const float*
 }
 
 template <int BM, int BN, int WAVES_M, int WAVES_N>
-hipError_t wide(const F8Plan& p, const uint8_t* w, const float* wsc, const uint16_t* a,
+hipError_t wide(const F8Plan& p, const uint8_t* w, const float* wsc, const uint8_t* a,
                 const float* asc, float* dst, int M, int N, int K, void* ws, hipStream_t s) {
-  constexpr int kLds = STAGES * (BN * kBlk / 2 + BM * kBlk + BM * 4);
+  constexpr int kLds = STAGES * ((BN + BM) * kBlk / 2 + BM * 4);
   auto* const kern = k_f8_wide<BM, BN, WAVES_M, WAVES_N>;
   if (kLds > 65536) {
     static std::atomic<uint64_t> raised{0};          // devices whose limit is set already
@@ -691,25 +683,26 @@ hipError_t launch_f8_product(const F8Plan& p, const uint8_t* w, const float* wsc
     return hipErrorInvalidValue;
   }
   if (p.kind == F8_WIDE) {
-    uint16_t* const values = reinterpret_cast<uint16_t*>((uint8_t*)ws + p.off_a);
-    const int64_t nkb = (K + kBlk - 1) / kBlk, nblocks = M * nkb;
-    if (x) {
+    uint8_t* const rows = (uint8_t*)ws + p.off_a;
+    const int64_t nkb = (K + kBlk - 1) / kBlk;
+    hipError_t e = hipSuccess;
+    if (x) {                                          // INIT
       float* const scales = reinterpret_cast<float*>((uint8_t*)ws + p.off_as);
-      const int64_t grid = (nblocks + 15) / 16;
-      hipLaunchKernelGGL(k_f8_quantize_rows_f16, dim3((unsigned)(grid < kMaxGridX ? grid : kMaxGridX)),
-                         dim3(256), 0, s, x, values, scales, K, (int)nkb, nblocks);
+      e = launch_f8_quantize(x, rows, scales, M, K, 1, s, nkb * kBlk);
+      a = rows;
       asc = scales;
-    } else {
-      const int64_t pieces = 8 * nblocks, grid = (pieces + 255) / 256;
-      hipLaunchKernelGGL(k_f8_widen, dim3((unsigned)(grid < kMaxGridX ? grid : kMaxGridX)), dim3(256),
-                         0, s, a, values, K, (int)nkb, pieces);
+    } else if (K % kBlk) {
+      const int64_t pieces = 8 * (int64_t)M * nkb, grid = (pieces + 255) / 256;
+      hipLaunchKernelGGL(k_f8_pad, dim3((unsigned)(grid < kMaxGridX ? grid : kMaxGridX)), dim3(256),
+                         0, s, a, rows, K, (int)nkb, pieces);
+      e = hipGetLastError();
+      a = rows;
     }
-    const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    if (p.bm == 128 && p.bn == 256) return wide<128, 256, 2, 4>(p, w, wsc, values, asc, dst, M, N, K, ws, s);
-    if (p.bm == 128 && p.bn == 128) return wide<128, 128, 2, 4>(p, w, wsc, values, asc, dst, M, N, K, ws, s);
-    if (p.bm == 64 && p.bn == 128) return wide<64, 128, 2, 4>(p, w, wsc, values, asc, dst, M, N, K, ws, s);
-    if (p.bm == 64 && p.bn == 64) return wide<64, 64, 2, 2>(p, w, wsc, values, asc, dst, M, N, K, ws, s);
+    if (p.bm == 128 && p.bn == 256) return wide<128, 256, 2, 4>(p, w, wsc, a, asc, dst, M, N, K, ws, s);
+    if (p.bm == 128 && p.bn == 128) return wide<128, 128, 2, 4>(p, w, wsc, a, asc, dst, M, N, K, ws, s);
+    if (p.bm == 64 && p.bn == 128) return wide<64, 128, 2, 4>(p, w, wsc, a, asc, dst, M, N, K, ws, s);
+    if (p.bm == 64 && p.bn == 64) return wide<64, 64, 2, 2>(p, w, wsc, a, asc, dst, M, N, K, ws, s);
     return hipErrorInvalidValue;
   }
   if (x) {                                            // INIT

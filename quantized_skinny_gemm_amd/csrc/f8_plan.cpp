@@ -45,17 +45,24 @@ int make_f8_plan(int64_t M, int64_t N, int64_t K, bool given, F8Plan* p) {
     p->lds = (size_t)(M * (nkb * kF8Block + 16)) + align_up((size_t)blocks * 4, 16) + (size_t)M * 512;
     return MM_OK;
   }
-  // the tiled kernel takes src1 as binary16 values in rows of whole blocks,
-  // whoever quantized it.
   // The tiled kernel from 9 src1 rows on matrices of 32 MiB or more, else from
   // 33 (us per call with INIT, M = 8 / 16 / 32, skinny against 64 x 128 tiles:
   // 14336 x 4096 23.2 / 26.4 / 42.5 against 22.8 / 22.6 / 25.0, 4096 x 4096
   // 10.4 / 11.3 / 14.1 against 13.6 / 13.9 / 15.1).
   const bool wide = M > (N * K >= ((int64_t)1 << 25) ? 8 : 32);
+  // Output tile by M (us per call, 64 x 128, 128 x 128 and 128 x 256 tiles:
+  // 14336 x 4096, M = 128 40.1 / 41.1 / 44.1, M = 256 65.8 / 56.8 / 59.0,
+  // M = 512 117.5 / 107.8 / 81.1; 4096 x 4096, M = 128 22.3 / 27.9 / 33.9,
+  // M = 512 39.5 / 41.7 / 43.9; 64 x 64: 4096 x 4096, M = 64 16.0 against 18.7).
+  p->bm = M <= 128 ? 64 : 128;
+  p->bn = M > 256 && (ceil_div(M, 128) * ceil_div(N, 256) >= kCUs / 2 || nkb >= 64) ? 256 : 128;
+  if (M <= 64 && N * K < ((int64_t)1 << 25)) p->bn = 64;
+  // src1 codes where INIT makes them, or where K ends inside a block and the
+  // tiled kernel needs rows of whole blocks
   size_t off = 0;
-  if (wide || !given) {
+  if (!given || (wide && K % kF8Block)) {
     p->off_a = off;
-    off = align_up(off + (size_t)M * (wide ? (size_t)nkb * kF8Block * 2 : (size_t)K), 256);
+    off = align_up(off + (size_t)M * (wide ? (size_t)nkb * kF8Block : (size_t)K), 256);
   }
   if (!given) {
     p->off_as = off; off = align_up(off + (size_t)M * (size_t)nkb * 4, 256);
@@ -70,13 +77,6 @@ int make_f8_plan(int64_t M, int64_t N, int64_t K, bool given, F8Plan* p) {
     p->lds = (size_t)p->waves * 1024 * p->nt;
   } else {
     p->kind = F8_WIDE;
-    // Output tile by M (us per call, 64 x 128, 128 x 128 and 128 x 256 tiles:
-    // 14336 x 4096, M = 128 40.1 / 41.1 / 44.1, M = 256 65.8 / 56.8 / 59.0,
-    // M = 512 117.5 / 107.8 / 81.1; 4096 x 4096, M = 128 22.3 / 27.9 / 33.9,
-    // M = 512 39.5 / 41.7 / 43.9).
-    p->bm = M <= 128 ? 64 : 128;
-    p->bn = M > 256 && (ceil_div(M, 128) * ceil_div(N, 256) >= kCUs / 2 || nkb >= 64) ? 256 : 128;
-    if (M <= 64 && N * K < ((int64_t)1 << 25)) p->bn = 64;     // 4096 x 4096, M = 64: 16.0 against 18.7
     p->tiles_m = ceil_div(M, p->bm);
     p->tiles_n = ceil_div(N, p->bn);
     const int64_t tiles = p->tiles_m * p->tiles_n;

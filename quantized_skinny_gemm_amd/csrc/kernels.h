@@ -104,9 +104,9 @@ bool f_mma_ok(int type, const void* w, const float* x, int64_t K);
 hipError_t launch_f_mma(const Plan& p, int type, const void* w, const float* x, float* dst, int M,
                         int N, int K, hipStream_t s);
 // e4m3 quantizer: codes [nrows][k], scales [ceil(nrows/block_rows)][ceil(k/128)],
-// block_rows 1 or 128.
+// block_rows 1 or 128; pitch (block_rows 1): bytes between rows of codes, zeros past k (0: k).
 hipError_t launch_f8_quantize(const float* x, uint8_t* codes, float* scales, int64_t nrows,
-                              int64_t k, int block_rows, hipStream_t s);
+                              int64_t k, int block_rows, hipStream_t s, int64_t pitch = 0);
 // Product with e4m3 weights; x != NULL: src1 as f32 (a, asc unused), else as
 // codes a and scales asc.
 hipError_t launch_f8_product(const F8Plan& p, const uint8_t* w, const float* wsc, const float* x,

@@ -754,6 +754,7 @@ __device__ __forceinline__ void make_jobs(Jobs& js, const int* ids, int T, int a
         js.order[at + ahead] = (uint16_t)(b + lane);
         if (ahead == 0) js.at[e] = at + __popcll(same);
       }
+      __builtin_amdgcn_wave_barrier();
     }
   }
   __syncthreads();
