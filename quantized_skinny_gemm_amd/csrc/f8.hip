@@ -381,11 +381,6 @@ __global__ __launch_bounds__(512) void k_f8_fused(
 
 // ---------------------------------------------------------------- product, many src1 rows
 
-template <int V>
-struct Int { static constexpr int value = V; };
-
-constexpr int STAGES = 4;      // (8 for the 64-row tiles measured no faster)
-
 // Output tile of BN weight rows x BM src1 rows per workgroup, half a block of
 // 128 k per stage, STAGES stages in LDS, both operands copied there straight
 // from memory as codes and widened in registers.  (src1 widened once by INIT,
@@ -409,23 +404,21 @@ constexpr int STAGES = 4;      // (8 for the 64-row tiles measured no faster)
 // (1320 TFLOP/s, what the card's power leaves of the matrix cores; a library
 // product of 8192^3 in binary16 reaches 1285), copies back in 490 to 520, all
 // of it 640.  A stage's 24 KB per workgroup come from L2 (81% hits).
-template <int BM, int BN, int WAVES_M, int WAVES_N>
+template <int BM, int BN, int WAVES_M, int WAVES_N, int STAGES>
 __global__ __launch_bounds__(64 * WAVES_M * WAVES_N, 1) void k_f8_wide(
     const uint8_t* __restrict__ w, const float* __restrict__ wsc, const uint8_t* __restrict__ a,
     const float* __restrict__ asc, int M, int N, int K, float* __restrict__ dst, int tiles_m,
     int tiles, int split, int kchunk) {
-  constexpr int NW = WAVES_M * WAVES_N, HB = kBlk / 2;         // k per stage
+  constexpr int NW = WAVES_M * WAVES_N;
   constexpr int WTM = BM / WAVES_M, WTN = BN / WAVES_N;
   constexpr int TM = WTM / 32, TN = WTN / 32;
-  constexpr int kA = BN * HB, kS = kA + BM * HB;               // stage: weights, src1, its scales
+  constexpr int kA = BN * kBlk, kS = kA + BM * kBlk;           // stage: weights, src1, its scales
   constexpr int STAGE = kS + BM * 4;
-  // pieces of 16 rows, 1 KB, per wave (with fewer src1 pieces than waves, the
-  // first ones copy them)
-  constexpr int WL = BN / 16 / NW, AP = BM / 16, AL = (AP + NW - 1) / NW;
+  constexpr int WL = BN / 8 / NW, AL = BM / 8 / NW;            // pieces of 8 rows, 1 KB, per wave
   constexpr int kCopies = WL + AL + 1;
-  static_assert((STAGES & (STAGES - 1)) == 0 && (STAGES - 1) * kCopies < 64, "wait counts");
+  static_assert((STAGES - 1) * kCopies < 64, "wait counts");
   static_assert(kBlk % WTN == 0, "one weight scale per wave and stage");
-  static_assert(BN % (16 * NW) == 0 && (AP % NW == 0 || AP < NW) && BM % 64 == 0 && NW % 2 == 0, "whole pieces");
+  static_assert(BN % (8 * NW) == 0 && BM % (8 * NW) == 0 && BM % 64 == 0 && NW % 2 == 0, "whole pieces");
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
 
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -437,38 +430,35 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N, 1) void k_f8_wide(
   const int tm = tt % tiles_m, tn = tt / tiles_m;    // m fastest: same weight tile adjacent
   const int m0 = tm * BM, n0 = tn * BN;
   const int kb0 = z * kchunk, kb1 = min(kb0 + kchunk, nkb);
-  const int s1 = 2 * (kb1 - kb0);                    // stages
+  const int s1 = kb1 - kb0;                          // stages
 
   // this lane's part of each piece
   const uint8_t* const wbase = w + (int64_t)n0 * K;
-  const bool has_a = AP >= NW || wave < AP;          // uniform
   const uint8_t* const abase = a + (int64_t)m0 * nkb * kBlk;
-  const int chunk = (lane & 3) ^ ((lane >> 4) & 3);
+  const int chunk = (lane & 7) ^ ((4 * (wave & 1) + (lane >> 4)) & 7);
   uint32_t woff[WL], aoff[AL];
 #pragma unroll
   for (int i = 0; i < WL; ++i)
-    woff[i] = (uint32_t)min((i * NW + wave) * 16 + (lane >> 2), N - 1 - n0) * (uint32_t)K;
+    woff[i] = (uint32_t)min((i * NW + wave) * 8 + (lane >> 3), N - 1 - n0) * (uint32_t)K;
 #pragma unroll
   for (int i = 0; i < AL; ++i)
-    aoff[i] = (uint32_t)min((i * NW + wave) * 16 + (lane >> 2), M - 1 - m0) * (uint32_t)nkb * kBlk;
+    aoff[i] = (uint32_t)min((i * NW + wave) * 8 + (lane >> 3), M - 1 - m0) * (uint32_t)nkb * kBlk;
   // every wave issues the same number of copies (the rows' scales are copied
   // by several waves, to the same place)
   const int sm = (wave % (BM / 64)) * 64;
   const float* const sbase = asc + (int64_t)m0 * nkb;
   const uint32_t soff = (uint32_t)min(sm + lane, M - 1 - m0) * (uint32_t)nkb;
   const uint32_t lds0 = lds_offset(lds);
-  auto copy_stage = [&](int s) {
-    const uint32_t base = lds0 + (s % STAGES) * STAGE;
-    const int k0 = kb0 * kBlk + s * HB;
+  auto copy_stage = [&](int s, int buf) {
+    const uint32_t base = lds0 + buf * STAGE;
     // past a weight row: its own first codes, which meet the zeros that src1
     // is padded with (if one is a NaN, so is the whole row's result)
-    const uint32_t ka = k0 + chunk * 16, kw = (int)ka < K ? ka : 0;
+    const uint32_t ka = (kb0 + s) * kBlk + chunk * 16, kw = (int)ka < K ? ka : 0;
 #pragma unroll
     for (int i = 0; i < WL; ++i) copy16(base + (i * NW + wave) * 1024, wbase, woff[i] + kw);
 #pragma unroll
-    for (int i = 0; i < AL; ++i)
-      if (has_a) copy16(base + kA + (i * NW + wave) * 1024, abase, aoff[i] + ka);
-    copy4(base + kS + 4 * sm, sbase, 4 * (soff + kb0 + (s >> 1)));
+    for (int i = 0; i < AL; ++i) copy16(base + kA + (i * NW + wave) * 1024, abase, aoff[i] + ka);
+    copy4(base + kS + 4 * sm, sbase, 4 * (soff + kb0 + s));
   };
   const int nrow = min(n0 + wn * WTN, N - 1);
   const float* const wscr = wsc + (int64_t)(nrow / kBlk) * nkb;
@@ -481,55 +471,51 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N, 1) void k_f8_wide(
 #pragma unroll
       for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
 
-  const int wrow = (wn * WTN + l32) * HB, arow = kA + (wm * WTM + l32) * HB;
-  const int x4 = (l32 >> 2) & 3;
+  const int wrow = (wn * WTN + l32) * kBlk, arow = kA + (wm * WTM + l32) * kBlk;
+  const int x8 = (l32 >> 1) & 7;
   uint4 wr[2][TN], ar[2][TM];
-  // the operands of steps 2 p and 2 p + 1 (p = 0, 1) of a stage
+  // the operands of steps 2 p and 2 p + 1 (p = 0..3) into register set p % 2
   auto read = [&](const uint8_t* base, int p) {
 #pragma unroll
     for (int i = 0; i < TN; ++i)
-      wr[p][i] = *reinterpret_cast<const uint4*>(base + wrow + 32 * i * HB + 16 * ((2 * p + h) ^ x4));
+      wr[p % 2][i] = *reinterpret_cast<const uint4*>(base + wrow + 32 * i * kBlk + 16 * ((2 * p + h) ^ x8));
 #pragma unroll
     for (int j = 0; j < TM; ++j)
-      ar[p][j] = *reinterpret_cast<const uint4*>(base + arow + 32 * j * HB + 16 * ((2 * p + h) ^ x4));
+      ar[p % 2][j] = *reinterpret_cast<const uint4*>(base + arow + 32 * j * kBlk + 16 * ((2 * p + h) ^ x8));
   };
 
 #pragma unroll
   for (int s = 0; s < STAGES; ++s)
-    if (s < s1) copy_stage(s);
-  // wait: all but the youngest S stages' copies of this wave
-  const auto wait_stages = [&](auto S) {
-    if (has_a) wait_copies<decltype(S)::value * kCopies>();
-    else wait_copies<decltype(S)::value * (kCopies - AL)>();
-  };
-  if (s1 >= STAGES) wait_stages(Int<STAGES - 1>{});
+    if (s < s1) copy_stage(s, s);
+  if (s1 >= STAGES) wait_copies<(STAGES - 1) * kCopies>();
   else wait_copies<0>();
   __builtin_amdgcn_s_barrier();
   read(lds, 0);
 
   float sw = wscr[kb0];
-  for (int s = 0; s < s1; s += 2) {
+  int buf = 0;
+  for (int s = 0; s < s1; ++s) {
+    const uint8_t* const base = lds + buf * STAGE;
+    const int next = buf + 1 == STAGES ? 0 : buf + 1;
     v16f c[TN][TM];
     float sc[TM];
 #pragma unroll
     for (int q = 0; q < 8; ++q) {
-      const int st = s + q / 4;                      // stage of this q
-      const uint8_t* const base = lds + (st % STAGES) * STAGE;
-      if (q % 4 == 1) read(base, 1);
-      if (q % 4 == 3) {
+      if (q % 2 == 1 && q < 7) read(base, q / 2 + 1);
+      if (q == 7) {
         // the next stage is here and this wave's reads of this one are done
-        if (st + STAGES - 1 < s1) wait_stages(Int<STAGES - 2>{});
+        if (s + STAGES - 1 < s1) wait_copies<(STAGES - 2) * kCopies>();
         else wait_copies<0>();
         __builtin_amdgcn_s_barrier();
-        if (st + STAGES < s1) copy_stage(st + STAGES);
-        read(lds + ((st + 1) % STAGES) * STAGE, 0);
+        if (s + STAGES < s1) copy_stage(s + STAGES, buf);
+        read(lds + next * STAGE, 0);
       }
       __builtin_amdgcn_sched_barrier(0);             // the reads stay ahead of the products
       if (q == 1) {
         const float* const ss = reinterpret_cast<const float*>(base + kS) + wm * WTM + l32;
 #pragma unroll
         for (int j = 0; j < TM; ++j) sc[j] = sw * ss[32 * j];
-        sw = wscr[min(kb0 + s / 2 + 1, nkb - 1)];
+        sw = wscr[min(kb0 + s + 1, nkb - 1)];
       }
       v8h av[TM];
 #pragma unroll
@@ -557,6 +543,7 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N, 1) void k_f8_wide(
       for (int j = 0; j < TM; ++j)
 #pragma unroll
         for (int r = 0; r < 16; ++r) acc[i][j][r] = fmaf(c[i][j][r], sc[j], acc[i][j][r]);
+    buf = next;
   }
 
   // lane: src1 row of column l32, weight rows 8 q + 4 h + 0..3
@@ -651,11 +638,11 @@ hipError_t fused(const F8Plan& p, const float* x, const uint8_t* w, const float*
   return hipGetLastError();
 }
 
-template <int BM, int BN, int WAVES_M, int WAVES_N>
+template <int BM, int BN, int WAVES_M, int WAVES_N, int STAGES>
 hipError_t wide(const F8Plan& p, const uint8_t* w, const float* wsc, const uint8_t* a,
                 const float* asc, float* dst, int M, int N, int K, void* ws, hipStream_t s) {
-  constexpr int kLds = STAGES * ((BN + BM) * kBlk / 2 + BM * 4);
-  auto* const kern = k_f8_wide<BM, BN, WAVES_M, WAVES_N>;
+  constexpr int kLds = STAGES * ((BN + BM) * kBlk + BM * 4);
+  auto* const kern = k_f8_wide<BM, BN, WAVES_M, WAVES_N, STAGES>;
   if (kLds > 65536) {
     static std::atomic<uint64_t> raised{0};          // devices whose limit is set already
     const hipError_t e = raise_lds(reinterpret_cast<const void*>(kern), kLds, raised);
@@ -699,10 +686,10 @@ hipError_t launch_f8_product(const F8Plan& p, const uint8_t* w, const float* wsc
       a = rows;
     }
     if (e != hipSuccess) return e;
-    if (p.bm == 128 && p.bn == 256) return wide<128, 256, 2, 4>(p, w, wsc, a, asc, dst, M, N, K, ws, s);
-    if (p.bm == 128 && p.bn == 128) return wide<128, 128, 2, 4>(p, w, wsc, a, asc, dst, M, N, K, ws, s);
-    if (p.bm == 64 && p.bn == 128) return wide<64, 128, 2, 4>(p, w, wsc, a, asc, dst, M, N, K, ws, s);
-    if (p.bm == 64 && p.bn == 64) return wide<64, 64, 2, 2>(p, w, wsc, a, asc, dst, M, N, K, ws, s);
+    if (p.bm == 128 && p.bn == 256) return wide<128, 256, 2, 4, 3>(p, w, wsc, a, asc, dst, M, N, K, ws, s);
+    if (p.bm == 128 && p.bn == 128) return wide<128, 128, 2, 4, 4>(p, w, wsc, a, asc, dst, M, N, K, ws, s);
+    if (p.bm == 64 && p.bn == 128) return wide<64, 128, 2, 4, 4>(p, w, wsc, a, asc, dst, M, N, K, ws, s);
+    if (p.bm == 64 && p.bn == 64) return wide<64, 64, 2, 2, 4>(p, w, wsc, a, asc, dst, M, N, K, ws, s);
     return hipErrorInvalidValue;
   }
   if (x) {                                            // INIT
