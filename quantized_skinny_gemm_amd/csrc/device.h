@@ -117,20 +117,24 @@ __device__ __forceinline__ void lds_barrier() {
 }
 
 // Asynchronous copies of 16 (4) bytes per lane from base + off into LDS at
-// dst + 16 (4) * lane, dst uniform.  Written as assembly without outputs, so
-// that the compiler does not drain them ahead of every LDS read: the code
-// below waits for the oldest stage only, by count (copies complete in the
-// order they were issued).
+// dst + 16 (4) * lane, dst uniform.  Written as assembly that returns nothing
+// from memory, so that the compiler does not drain them ahead of every LDS read:
+// the code that copies waits for the oldest by count (they complete in the order
+// they were issued).
 __device__ __forceinline__ uint32_t lds_offset(const void* p) {
   return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void*)p;
 }
 __device__ __forceinline__ void copy16(uint32_t dst, const void* base, uint32_t off) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
-               :: "s"(dst), "v"(off), "s"(base) : "memory", "m0");
+  uint32_t m0;                                       // the register is handed back as it was
+  asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\ts_nop 0\n\t"
+               "global_load_lds_dwordx4 %2, %3\n\ts_mov_b32 m0, %0"
+               : "=&s"(m0) : "s"(dst), "v"(off), "s"(base) : "memory");
 }
 __device__ __forceinline__ void copy4(uint32_t dst, const void* base, uint32_t off) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2"
-               :: "s"(dst), "v"(off), "s"(base) : "memory", "m0");
+  uint32_t m0;
+  asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\ts_nop 0\n\t"
+               "global_load_lds_dword %2, %3\n\ts_mov_b32 m0, %0"
+               : "=&s"(m0) : "s"(dst), "v"(off), "s"(base) : "memory");
 }
 // At most N of this wave's copies still under way; its LDS reads are done.
 template <int N>

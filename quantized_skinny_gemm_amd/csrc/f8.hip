@@ -381,29 +381,31 @@ __global__ __launch_bounds__(512) void k_f8_fused(
 
 // ---------------------------------------------------------------- product, many src1 rows
 
-// Output tile of BN weight rows x BM src1 rows per workgroup, half a block of
-// 128 k per stage, STAGES stages in LDS, both operands copied there straight
-// from memory as codes and widened in registers.  (src1 widened once by INIT,
-// binary16 in LDS, spares the widening and costs twice the copies' bytes:
-// 14336 x 4096, M = 256 / 512 57.3 / 82.0 us against 54.7 / 81.1.)
+// Output tile of BN weight rows x BM src1 rows per workgroup, one block of 128 k
+// per stage, STAGES stages in LDS, both operands copied there straight from
+// memory as codes and widened in registers.  (src1 widened once by INIT,
+// binary16 in LDS, spares the widening and costs twice the copies' bytes: about
+// 3% slower.  Stages of half a block, twice as many: twice the barriers and
+// 64-byte rows in the copies, 14336 x 4096, M = 128 / 512 39.3 / 78.8 us against
+// 31.6 / 75.5.  More stages: no faster.)
 //
-// A block is eight steps of 16 k (q), four to a stage; each MFMA adds to the
-// block dot c, and the fp32 sums take c * (dw * ds).  Operands are read two
-// steps at a time, ahead of the products.  The one barrier per stage stands
-// before its last q's MFMAs: there every wave has read the whole stage, so the
-// copy of the stage STAGES further can start, and the next stage has arrived,
-// so its first operands are read behind those MFMAs.
+// A block is eight steps of 16 k (q); each MFMA adds to the block dot c, and the
+// fp32 sums take c * (dw * ds).  Operands are read two steps at a time, ahead of
+// the products.  The one barrier per stage stands before its last q's MFMAs:
+// there every wave has read the whole stage, so the copy of the stage STAGES
+// further can start, and the next stage has arrived, so its first operands are
+// read behind those MFMAs.
 //
-// In LDS a row's four 16-byte chunks (of half a block) are permuted by
-// (row / 4) % 4, so that the 16 rows of an operand read lie in different
-// banks.  Lane half h of an MFMA holds k 32 p + 16 h + 8 (q % 2) .. + 7,
-// p = q / 2: one chunk serves two q.
+// In LDS a row's eight 16-byte chunks are permuted by (row / 2) % 8, so that the
+// 16 rows of an operand read lie in different banks.  Lane half h of an MFMA
+// holds k 32 p + 16 h + 8 (q % 2) .. + 7, p = q / 2: one chunk serves two q.
 //
-// What bounds it, at 512 x 128256 x 4096 (128 x 256 tiles): without the copies,
-// the widening, the scaling and the barriers the same MFMAs take 407 us
-// (1320 TFLOP/s, what the card's power leaves of the matrix cores; a library
-// product of 8192^3 in binary16 reaches 1285), copies back in 490 to 520, all
-// of it 640.  A stage's 24 KB per workgroup come from L2 (81% hits).
+// What bounds it, at 512 x 128256 x 4096 (128 x 256 tiles): 610 us, 880 TFLOP/s.
+// Without the copies, the widening, the scaling and the barriers the same MFMAs
+// take 407 us (1320 TFLOP/s, what the card's power leaves of the matrix cores; a
+// library product of 8192^3 in binary16 reaches 1285), with LDS reads and
+// barriers 490 to 520.  The copies (48 KB per workgroup and block, 90% L2 hits)
+// keep the address units two thirds busy.
 template <int BM, int BN, int WAVES_M, int WAVES_N, int STAGES>
 __global__ __launch_bounds__(64 * WAVES_M * WAVES_N, 1) void k_f8_wide(
     const uint8_t* __restrict__ w, const float* __restrict__ wsc, const uint8_t* __restrict__ a,

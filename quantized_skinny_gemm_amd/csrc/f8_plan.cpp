@@ -46,17 +46,23 @@ int make_f8_plan(int64_t M, int64_t N, int64_t K, bool given, F8Plan* p) {
     return MM_OK;
   }
   // The tiled kernel from 9 src1 rows on matrices of 32 MiB or more, else from
-  // 33 (us per call with INIT, M = 8 / 16 / 32, skinny against 64 x 128 tiles:
-  // 14336 x 4096 23.2 / 26.4 / 42.5 against 22.8 / 22.6 / 25.0, 4096 x 4096
-  // 10.4 / 11.3 / 14.1 against 13.6 / 13.9 / 15.1).
-  const bool wide = M > (N * K >= ((int64_t)1 << 25) ? 8 : 32);
-  // Output tile by M (us per call, 64 x 128, 128 x 128 and 128 x 256 tiles:
-  // 14336 x 4096, M = 128 40.1 / 41.1 / 44.1, M = 256 65.8 / 56.8 / 59.0,
-  // M = 512 117.5 / 107.8 / 81.1; 4096 x 4096, M = 128 22.3 / 27.9 / 33.9,
-  // M = 512 39.5 / 41.7 / 43.9; 64 x 64: 4096 x 4096, M = 64 16.0 against 18.7).
-  p->bm = M <= 128 ? 64 : 128;
-  p->bn = M > 256 && (ceil_div(M, 128) * ceil_div(N, 256) >= kCUs / 2 || nkb >= 64) ? 256 : 128;
-  if (M <= 64 && N * K < ((int64_t)1 << 25)) p->bn = 64;
+  // 25 (us per call with INIT, M = 16 / 24 / 32: 14336 x 4096, skinny 26.4 / 38.8 /
+  // 42.5 against 64 x 128 tiles 21.3 / 21.6 / 21.8; 4096 x 4096, skinny 11.3 / 12.9 /
+  // 14.0 against 64 x 64 tiles 12.7 / 12.8 / 13.0).
+  const bool large = N * K >= ((int64_t)1 << 25);
+  const bool wide = M > (large ? 8 : 24);
+  // Output tile by M (us per call, 64 x 128, 128 x 128 and 128 x 256 tiles: 14336 x
+  // 4096, M = 128 31.4 / 36.2 / 40.4, M = 256 57.0 / 47.9 / 54.4, M = 512 106.0 /
+  // 90.8 / 77.9; 4096 x 14336, M = 128 32.9 / 36.4 / 41.1, M = 600 158.7 / 125.2 /
+  // 98.1).  Below 32 MiB a small tile also where that gives each CU at most one
+  // (4096 x 4096, M = 256 25.1 / 29.7 / 33.7, M = 512 33.6 / 37.2 / 41.7, M = 1024
+  // 61.3 / 51.9 / 58.2, M = 2048 115.6 / 97.3 / 85.0; 64 x 64 at M = 64 14.6 against
+  // 17.4).
+  const auto fits = [&](int bm, int bn) { return ceil_div(M, bm) * ceil_div(N, bn) <= kCUs; };
+  const bool low = M <= 128 || (!large && fits(64, 128));
+  const bool mid = M <= 256 || (!large && fits(128, 128));
+  p->bm = low ? 64 : 128;
+  p->bn = !low && !mid ? 256 : !large && M <= 64 ? 64 : 128;
   // src1 codes where INIT makes them, or where K ends inside a block and the
   // tiled kernel needs rows of whole blocks
   size_t off = 0;

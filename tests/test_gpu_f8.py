@@ -87,7 +87,8 @@ def test_quantize_edge_values():
     (1, 4096, 4096), (1, 1, 32), (1, 17, 96), (2, 300, 4128), (4, 129, 256), (5, 1000, 4128), (16, 257, 1024),
     (17, 130, 2080), (32, 64, 4096), (33, 48, 160), (64, 333, 1056), (65, 129, 128), (100, 515, 2080),
     (128, 256, 14336), (129, 257, 288), (300, 700, 1184), (512, 1024, 4096), (1, 40, 131072), (4, 40, 131072),
-    (8, 300, 4096), (8, 300, 4128), (16, 65, 2048), (9, 8192, 4096), (70, 8200, 4128), (200, 130, 8224), (260, 16500, 2080),
+    (8, 300, 4096), (8, 300, 4128), (16, 65, 2048), (9, 8192, 4096), (70, 8200, 4128), (200, 130, 8224),
+    (260, 16500, 2080), (24, 1100, 4096), (25, 1100, 4096), (300, 16500, 2080), (600, 4200, 1056), (1100, 4200, 160), (40, 33000, 160),
 ])
 def test_products(m, n, k):
     qs = _qs()
