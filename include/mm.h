@@ -301,9 +301,11 @@ mm_status mm_quantize_f8(const float* x, void* codes, float* scales, int64_t nro
  * dst[m][n] = sum_b scale1[m][b] * scale0[n/128][b] * S_b[m][n], S_b the
  * fp32 sum of the block's code products (each exact); a NaN code or a
  * non-finite scale makes the outputs it enters NaN or infinite and no other.
- * mm_mul_mat_workspace_size(MM_TYPE_F8, ...) is the size for f32 src1 (which
- * is the larger one), mm_row_bytes(MM_TYPE_F8, K) the bytes of a row of
- * codes; mm_dispatch and mm_debug_mul_mat do not take this type.
+ * mm_mul_mat_workspace_size(MM_TYPE_F8, ...) is the size for f32 src1 (a few
+ * rows of f32 may need none where src1 as codes needs some),
+ * mm_row_bytes(MM_TYPE_F8, K) the bytes of a row of codes; mm_dispatch and
+ * mm_debug_mul_mat do not take this type.  M, N < 2^31 - 255; a product
+ * whose output needs 2^32 threads in one launch is MM_ERR_SHAPE too.
  */
 mm_status mm_mul_mat_f8_f32(const void* src0, const float* scale0, const float* src1, float* dst,
                             int64_t M, int64_t N, int64_t K, void* ws, size_t ws_bytes,

@@ -9,8 +9,8 @@ namespace qsg {
 
 namespace {
 
-constexpr int64_t kMaxDim = 0x7fffffff;
-constexpr int64_t kMaxTiles = 1 << 23;       // workgroups x 256 threads stay below 2^32
+constexpr int64_t kMaxDim = 0x7fffff00;      // the ends of tiles stay below 2^31
+constexpr int64_t kMaxTiles = (1 << 23) - 1; // workgroups x 512 threads stay below 2^32
 
 size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -80,6 +80,7 @@ int make_f8_plan(int64_t M, int64_t N, int64_t K, bool given, F8Plan* p) {
     while (p->waves > 1 && p->waves > nkb) p->waves /= 2;
     p->grid_n = ceil_div(N, 16);
     p->grid_m = ceil_div(M, 16 * p->nt);
+    if (p->grid_n * p->grid_m * p->waves > kMaxTiles * 8) return MM_ERR_SHAPE;
     p->lds = (size_t)p->waves * 1024 * p->nt;
   } else {
     p->kind = F8_WIDE;

@@ -49,6 +49,20 @@ def test_product_refusals(call):
     assert call(m=0, w=None, x=None, dst=None, wsb=0) == OK and call(n=0, w=None, dst=None, wsb=0) == OK
 
 
+@pytest.mark.parametrize("call", [_f32, _f8])
+def test_product_refuses_what_no_grid_covers(call):
+    # tile ends past 2^31, launches of 2^32 threads and more
+    for m, n, k in ((1, 2 ** 31 - 1, 32), (2 ** 31 - 1, 1, 32), (8, 2 ** 28, 4128), (2 ** 23, 2 ** 15, 32),
+                    (2 ** 17, 2 ** 22, 32)):
+        assert call(m, n, k, wsb=0) == SHAPE, (m, n, k)
+
+
+def test_workspace_of_few_rows():
+    # f32 rows that the product quantizes within need no workspace; the same rows as codes may
+    assert qs.f8_workspace_size(9, 9400, 3584) == 0 < qs.f8_workspace_size(9, 9400, 3584, True)
+    assert _f8(9, 9400, 3584, ws=None, wsb=0) == WS
+
+
 def test_product_workspace_refusals():
     m, n, k = 100, 256, 4096
     need = qs.f8_workspace_size(m, n, k)
