@@ -56,13 +56,13 @@ int make_f8_plan(int64_t M, int64_t N, int64_t K, bool given, F8Plan* p) {
   // 90.8 / 77.9; 4096 x 14336, M = 128 32.9 / 36.4 / 41.1, M = 600 158.7 / 125.2 /
   // 98.1).  Below 32 MiB a small tile also where that gives each CU at most one
   // (4096 x 4096, M = 256 25.1 / 29.7 / 33.7, M = 512 33.6 / 37.2 / 41.7, M = 1024
-  // 61.3 / 51.9 / 58.2, M = 2048 115.6 / 97.3 / 85.0; 64 x 64 at M = 64 14.6 against
-  // 17.4).
+  // 61.3 / 51.9 / 58.2, M = 2048 115.6 / 97.3 / 85.0), and 64 x 64 up to M = 128
+  // (M = 64 / 128 14.4 / 18.2 against 17.4 / 19.6).
   const auto fits = [&](int bm, int bn) { return ceil_div(M, bm) * ceil_div(N, bn) <= kCUs; };
   const bool low = M <= 128 || (!large && fits(64, 128));
   const bool mid = M <= 256 || (!large && fits(128, 128));
   p->bm = low ? 64 : 128;
-  p->bn = !low && !mid ? 256 : !large && M <= 64 ? 64 : 128;
+  p->bn = !low && !mid ? 256 : !large && M <= 128 ? 64 : 128;
   // src1 codes where INIT makes them, or where K ends inside a block and the
   // tiled kernel needs rows of whole blocks
   size_t off = 0;

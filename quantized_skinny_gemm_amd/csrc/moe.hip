@@ -51,6 +51,8 @@ namespace {
 
 typedef float v4f __attribute__((ext_vector_type(4)));
 typedef _Float16 v2h __attribute__((ext_vector_type(2)));
+typedef uint32_t v2u __attribute__((ext_vector_type(2)));
+typedef uint32_t v4u __attribute__((ext_vector_type(4)));
 
 // ---------------------------------------------------------------- activations
 
@@ -235,10 +237,10 @@ struct Tile;
 
 template <>
 struct Tile<MM_TYPE_Q4_0R> {
-  static constexpr int kLds = 0;
+  static constexpr int kLds = 0, kAhead = 2, kLoads = 2;
   const uint8_t* base;
-  uint4 c;
-  uint2 d;
+  v4u c;                         // whole vectors, so that they stay in the registers that
+  v2u d;                         // the loads fill
   __device__ __forceinline__ void bind(const uint8_t* w, const float*, int64_t e, int N, int K,
                                        int row0, int lane) {
     const int64_t phases = (K + 255) / 256;
@@ -246,12 +248,12 @@ struct Tile<MM_TYPE_Q4_0R> {
   }
   // a unit is half of a repacked chunk of 8 blocks
   __device__ __forceinline__ void fetch(const uint8_t*, int) {
-    asm volatile("" : "+v"(c.x), "+v"(c.y), "+v"(c.z), "+v"(c.w), "+v"(d.x), "+v"(d.y));
+    asm volatile("" : "+v"(c), "+v"(d));
   }
   __device__ __forceinline__ void load(int u, int, int lane, uint32_t) {
     const uint8_t* p = base + (int64_t)(u >> 1) * kQ4RChunk;
-    c = *reinterpret_cast<const uint4*>(p + 1024 * (u & 1));
-    d = *reinterpret_cast<const uint2*>(p - 16 * lane + 2048 + 16 * (lane & 15) + 8 * (u & 1));
+    c = *reinterpret_cast<const v4u*>(p + 1024 * (u & 1));
+    d = *reinterpret_cast<const v2u*>(p - 16 * lane + 2048 + 16 * (lane & 15) + 8 * (u & 1));
   }
   __device__ __forceinline__ v8h operand(int j) const {
     const uint32_t w = j == 0 ? c.x : j == 1 ? c.y : j == 2 ? c.z : c.w;
@@ -276,7 +278,7 @@ struct Tile<MM_TYPE_Q4_0R> {
 // permuted by (row / 2) % 8): a lane's operand is 8 bytes of its row.
 template <>
 struct Tile<MM_TYPE_F8> {
-  static constexpr int kLds = 2048;
+  static constexpr int kLds = 2048, kAhead = 1;
   const uint8_t* base;           // uniform
   const float* sc;
   uint32_t off[2];               // the rows this lane copies
@@ -321,7 +323,7 @@ struct Tile<MM_TYPE_F8> {
 
 template <>
 struct Tile<MM_TYPE_F16> {
-  static constexpr int kLds = 0;
+  static constexpr int kLds = 0, kAhead = 1;
   const uint8_t* base;
   uint4 c[4];
   __device__ __forceinline__ void bind(const uint8_t* w, const float*, int64_t e, int N, int K,
@@ -503,8 +505,7 @@ __device__ __forceinline__ void up_pass(const MoeArgs& a, int e, int rg0, int st
 #pragma unroll
     for (int r = 0; r < NR; ++r) acc[i][r] = 0.0f;
   const uint32_t at = lds_offset(lds), tat = at + Acts<NR>::kLds;
-  const auto issue = [&](Tile<TY> (&w)[4], int rg, int u) {
-    x.load(u, n, lane, at);
+  const auto issue_w = [&](Tile<TY> (&w)[4], int rg, int u) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       w[i].bind(i < 2 ? a.gate : a.up, i < 2 ? a.gate_scale : a.up_scale, e, a.F, a.D,
@@ -512,8 +513,7 @@ __device__ __forceinline__ void up_pass(const MoeArgs& a, int e, int rg0, int st
       w[i].load(u, nb, lane, tat + i * Tile<TY>::kLds);
     }
   };
-  const auto take = [&](Tile<TY> (&w)[4]) {
-    wait_copies<0>();
+  const auto fetch = [&](Tile<TY> (&w)[4]) {
     x.fetch(lds, lane);
 #pragma unroll
     for (int i = 0; i < 4; ++i) w[i].fetch(lds + Acts<NR>::kLds + i * Tile<TY>::kLds, lane);
@@ -561,26 +561,83 @@ __device__ __forceinline__ void up_pass(const MoeArgs& a, int e, int rg0, int st
   }
   // one unit of row group rg; the next one's loads; the join after the last
   int rg = rg0, u = wave;
-  const auto body = [&](Tile<TY> (&w)[4], Tile<TY> (&next)[4]) {
-    take(w);
-    const bool last = u + W >= units;
-    const int nrg = last ? rg + step : rg, nu = last ? wave : u + W;
-    if (nrg < nfb) issue(next, nrg, nu);
-    unit_product<TY, NR, 4>(x, w, one, acc);
-    if (last) join(rg);
-    rg = nrg;
-    u = nu;
-  };
-  Tile<TY> w0[4];
-  issue(w0, rg, u);
-  if constexpr (Tile<TY>::kLds > 0) {
-    while (rg < nfb) body(w0, w0);
-  } else {
-    Tile<TY> w1[4];
-    while (rg < nfb) {
-      body(w0, w1);
-      if (rg >= nfb) break;
+  if constexpr (Tile<TY>::kAhead == 2) {
+    // weights two units ahead, activations one (their LDS is free by then)
+    int rg1, u1, rg2, u2;
+    const auto after = [&](int r, int v, int& rn, int& un) {
+      const bool last = v + W >= units;
+      rn = last ? r + step : r;
+      un = last ? wave : v + W;
+    };
+    after(rg, u, rg1, u1);
+    Tile<TY> w0[4], w1[4], w2[4];
+    issue_w(w0, rg, u);
+    __builtin_amdgcn_sched_barrier(0);
+    x.load(u, n, lane, at);
+    __builtin_amdgcn_sched_barrier(0);
+    issue_w(w1, rg1 < nfb ? rg1 : rg, rg1 < nfb ? u1 : u);
+    const auto finish = [&](Tile<TY> (&w)[4]) {
+      unit_product<TY, NR, 4>(x, w, one, acc);
+      if (u + W >= units) join(rg);
+      rg = rg1; u = u1;
+      rg1 = rg2; u1 = u2;
+    };
+    const auto body = [&](Tile<TY> (&w)[4], Tile<TY> (&next)[4]) {
+      __builtin_amdgcn_sched_barrier(0);
+      wait_copies<4 * Tile<TY>::kLoads>();           // all but the next unit's weights
+      fetch(w);
+      after(rg1, u1, rg2, u2);
+      x.load(rg1 < nfb ? u1 : u, n, lane, at);
+      __builtin_amdgcn_sched_barrier(0);
+      issue_w(next, rg2 < nfb ? rg2 : rg, rg2 < nfb ? u2 : u);   // past the end: read again
+      __builtin_amdgcn_sched_barrier(0);
+      finish(w);
+    };
+    const auto tail = [&](Tile<TY> (&w)[4], bool more) {
+      wait_copies<0>();
+      fetch(w);
+      if (more) x.load(u1, n, lane, at);
+      finish(w);
+    };
+    // whole rounds, then the rest: a loop with exits between the bodies would
+    // make the compiler wait as if each could follow each
+    int left = ((units - wave + W - 1) / W) * ((nfb - rg0 + step - 1) / step);
+    for (; left >= 3; left -= 3) {
+      body(w0, w2);
       body(w1, w0);
+      body(w2, w1);
+    }
+    rg2 = u2 = 0;
+    if (left > 0) tail(w0, left > 1);
+    if (left > 1) tail(w1, false);
+    wait_copies<0>();
+  } else {
+    const auto issue = [&](Tile<TY> (&w)[4], int r, int v) {
+      x.load(v, n, lane, at);
+      issue_w(w, r, v);
+    };
+    const auto body = [&](Tile<TY> (&w)[4], Tile<TY> (&next)[4]) {
+      wait_copies<0>();
+      fetch(w);
+      const bool last = u + W >= units;
+      const int nrg = last ? rg + step : rg, nu = last ? wave : u + W;
+      if (nrg < nfb) issue(next, nrg, nu);
+      unit_product<TY, NR, 4>(x, w, one, acc);
+      if (last) join(rg);
+      rg = nrg;
+      u = nu;
+    };
+    Tile<TY> w0[4];
+    issue(w0, rg, u);
+    if constexpr (Tile<TY>::kLds > 0) {
+      while (rg < nfb) body(w0, w0);
+    } else {
+      Tile<TY> w1[4];
+      while (rg < nfb) {
+        body(w0, w1);
+        if (rg >= nfb) break;
+        body(w1, w0);
+      }
     }
   }
 }
