@@ -37,7 +37,10 @@
 //   computed from registers, the next one's weights are on their way to
 //   registers and its activations (512 consecutive bytes per row; e4m3
 //   weights too) to the wave's own piece of LDS, from which a lane takes its
-//   operand.  Loading operands straight from memory costs one 16-byte access
+//   operand.  A Q4_0R unit is so small that one ahead keeps too few bytes under
+//   way: gate / up has two of them (layer, 4 / 16 / 32 tokens, 8 experts of
+//   4096 x 14336: 113 / 220 / 246 us before, 103 / 206 / 236 with).  In down the
+//   same changed nothing.  Loading operands straight from memory costs one 16-byte access
 //   per lane, since neighbouring lanes belong to different rows: the address
 //   units were 67% busy and the gate / up launch at 2.9 TB/s (32 tokens, 8
 //   experts of 4096 x 14336).
@@ -230,8 +233,9 @@ __global__ __launch_bounds__(512) void k_moe_select(const double* __restrict__ l
 // One 16-row tile of weights, a unit of 4 blocks of 32 k at a time.  bind():
 // expert e's matrix of N rows of K; load(): issues a unit's loads; fetch():
 // takes what load() sent through LDS (kLds bytes at lds), or tells the
-// compiler that its loads have arrived; operand(j): block j as binary16, row lane % 16, in lane group order;
-// scale(j): its dw.
+// compiler that its loads have arrived; operand(j): block j as binary16, row
+// lane % 16, in lane group order; scale(j): its dw.  kAhead: units of weights
+// that gate / up has under way; kLoads: loads of one (kAhead 2).
 template <int TY>
 struct Tile;
 

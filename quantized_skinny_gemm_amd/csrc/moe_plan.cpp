@@ -42,9 +42,9 @@ int make_moe_plan(int type, int64_t T, int64_t D, int64_t F, int64_t E, int64_t 
   // is cut in slices to fill the device.
   const int64_t used = T * top_k < E ? T * top_k : E;
   // Gate / up: groups of 32 rows, several per workgroup where that leaves two
-  // workgroups per CU (gate / up launch, us, with one group each / about 3 / 2 /
-  // 1 workgroups per CU: 32 tokens, 8 experts of 4096 x 14336, Q4_0R 204 / 179 /
-  // 165 / 162; 16 tokens, 8 of 2048 x 5632, F16 87 / 86 / 79 / 98).
+  // workgroups per CU if every expert that can be in use is (whole layer, us,
+  // about 3 / 2 / 1 workgroups per CU, 8 experts of 4096 x 14336, Q4_0R: 32 tokens
+  // 244 / 232 / 226; 4 tokens, on 5 of the experts, 109 / 101 / 142).
   const int64_t groups = F / kQK, per = groups * used / (2 * kCUs);
   p->up_groups = (int)(per > 1 ? (groups + per - 1) / per : groups);
   const bool many = T * top_k > 2 * used;
