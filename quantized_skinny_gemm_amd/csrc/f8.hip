@@ -404,8 +404,8 @@ __global__ __launch_bounds__(512) void k_f8_fused(
 // Without the copies, the widening, the scaling and the barriers the same MFMAs
 // take 407 us (1320 TFLOP/s, what the card's power leaves of the matrix cores; a
 // library product of 8192^3 in binary16 reaches 1285), with LDS reads and
-// barriers 490 to 520.  The copies (48 KB per workgroup and block, 90% L2 hits)
-// keep the address units two thirds busy.
+// barriers 490 to 520.  The copies (48 KB per workgroup and block, 85% L2 hits)
+// keep the address units 58% busy.
 template <int BM, int BN, int WAVES_M, int WAVES_N, int STAGES>
 __global__ __launch_bounds__(64 * WAVES_M * WAVES_N, 1) void k_f8_wide(
     const uint8_t* __restrict__ w, const float* __restrict__ wsc, const uint8_t* __restrict__ a,

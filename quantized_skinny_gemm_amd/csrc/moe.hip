@@ -424,13 +424,13 @@ __device__ __forceinline__ void unit_product(const Acts<NR>& x, const Tile<TY> (
   }
 }
 
-// Units u, u + step, ... < end of RT tiles for one pass: acc += ...  lds: the
+// Units u, u + 1, ... < end of RT tiles for one pass: acc += ...  lds: the
 // wave's staging (activations, then the tiles').  The wait at the top finds
 // exactly the current unit's loads under way; its LDS is free again once the
 // operands are in registers.
 template <int TY, int NR, int RT>
-__device__ __forceinline__ void run_units(Acts<NR>& x, Tile<TY> (&w0)[RT], int u, int end, int step,
-                                          int n, int nb, const float (&p)[NR], float (&acc)[RT][NR],
+__device__ __forceinline__ void run_units(Acts<NR>& x, Tile<TY> (&w0)[RT], int u, int end, int n,
+                                          int nb, const float (&p)[NR], float (&acc)[RT][NR],
                                           uint8_t* lds, int lane) {
   const uint32_t at = lds_offset(lds), tat = at + Acts<NR>::kLds;
   const auto issue = [&](Tile<TY> (&w)[RT], int v) {
@@ -448,22 +448,22 @@ __device__ __forceinline__ void run_units(Acts<NR>& x, Tile<TY> (&w0)[RT], int u
   if (u >= end) return;
   issue(w0, u);
   if constexpr (Tile<TY>::kLds > 0) {
-    for (; u < end; u += step) {
+    for (; u < end; ++u) {
       take(w0);
-      if (u + step < end) issue(w0, u + step);
+      if (u + 1 < end) issue(w0, u + 1);
       unit_product<TY, NR, RT>(x, w0, p, acc);
     }
   } else {
     Tile<TY> w1[RT];
 #pragma unroll
     for (int i = 0; i < RT; ++i) w1[i] = w0[i];
-    for (; u < end; u += 2 * step) {
+    for (; u < end; u += 2) {
       take(w0);
-      if (u + step < end) issue(w1, u + step);
+      if (u + 1 < end) issue(w1, u + 1);
       unit_product<TY, NR, RT>(x, w0, p, acc);
-      if (u + step >= end) break;
+      if (u + 1 >= end) break;
       take(w1);
-      if (u + 2 * step < end) issue(w0, u + 2 * step);
+      if (u + 2 < end) issue(w0, u + 2);
       unit_product<TY, NR, RT>(x, w1, p, acc);
     }
   }
@@ -566,7 +566,10 @@ __device__ __forceinline__ void up_pass(const MoeArgs& a, int e, int rg0, int st
   // one unit of row group rg; the next one's loads; the join after the last
   int rg = rg0, u = wave;
   if constexpr (Tile<TY>::kAhead == 2) {
-    // weights two units ahead, activations one (their LDS is free by then)
+    // weights two units ahead, activations one (their LDS is free by then).  The
+    // count in body's wait holds because a unit's weights are exactly 4 kLoads
+    // loads, all of them used, and nothing else is loaded behind them (the stores
+    // of a join only make it wait for more).
     int rg1, u1, rg2, u2;
     const auto after = [&](int r, int v, int& rn, int& un) {
       const bool last = v + W >= units;
@@ -841,7 +844,7 @@ __device__ __forceinline__ void down_job(const MoeArgs& a, int e, int row0, cons
   Tile<TY> w[RT];
 #pragma unroll
   for (int i = 0; i < RT; ++i) w[i].bind(a.down, a.down_scale, e, a.D, a.F, row0 + 16 * i, lane);
-  run_units<TY, NR, RT>(x, w, u0, u1, 1, n, nb, p, acc, lds, lane);
+  run_units<TY, NR, RT>(x, w, u0, u1, n, nb, p, acc, lds, lane);
 #pragma unroll
   for (int r = 0; r < NR; ++r) {
     if (4 * r + g < n) {

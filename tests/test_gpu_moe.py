@@ -85,6 +85,20 @@ def test_layer(kind, t, d, f, e, top_k):
     m.check(qs.moe_f32(m.layer, to_dev(m.x)), what=f"{kind} T={t} D={d} F={f} E={e} k={top_k}")
 
 
+# many row groups: a workgroup of gate / up walks several of them, with one to three passes over the tokens
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("t,d,f,e,top_k", [
+    (16, 160, 4128, 16, 2), (4, 160, 8256, 8, 2), (1, 1056, 8256, 4, 4), (40, 96, 33024, 2, 2),
+])
+def test_layer_walks_row_groups(kind, t, d, f, e, top_k):
+    say("moe wide", kind, t, d, f, e, top_k)
+    m = Layer(kind, t, d, f, e, top_k, t + d + f + e)
+    qs = _qs()
+    got = qs.moe_f32(m.layer, to_dev(m.x))
+    m.check(got, what=f"{kind} T={t} D={d} F={f} E={e} k={top_k}")
+    assert all(np.array_equal(to_host(a), to_host(b)) for a, b in zip(got, qs.moe_f32(m.layer, to_dev(m.x))))
+
+
 @pytest.mark.parametrize("kind", KINDS)
 def test_probabilities_without_normalisation(kind):
     say("moe no norm", kind)
