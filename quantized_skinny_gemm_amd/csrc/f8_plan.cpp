@@ -32,12 +32,16 @@ int make_f8_plan(int64_t M, int64_t N, int64_t K, bool given, F8Plan* p) {
   const int64_t nkb = ceil_div(K, kF8Block);
 
   // Up to 8 rounds of 32 blocks of 128: every workgroup quantizes src1 itself
-  // (at M = 8 and K = 4096 in about the time of an INIT launch).
-  const int64_t blocks = M * nkb;
-  if (!given && M <= 16 && blocks <= 256) {
+  // (at M = 8 and K = 4096 in about the time of an INIT launch).  Below 32 blocks
+  // of K its waves idle in part, and the join of every 16 rows shows, unless the
+  // rows are few (us per call, fused / tiled, M = 1: 8192 x 1024 7.0 / 9.1, 12000 x
+  // 2048 10.8 / 13.0, 16384 x 1024 13.8 / 9.5, 65536 x 512 39.5 / 15.9; with K = 4096
+  // and 65536 rows 53.7 / 71.8).
+  const int64_t blocks = M * nkb, groups = ceil_div(N, 16);
+  const bool brief = nkb < 32;
+  if (!given && M <= 16 && blocks <= 256 && (!brief || groups <= 3 * kCUs)) {
     p->kind = F8_FUSED;
     p->nt = blocks <= 32 ? 1 : blocks <= 64 ? 2 : blocks <= 128 ? 4 : 8;
-    const int64_t groups = ceil_div(N, 16);
     // workgroups along N, each walking groups of 16 rows (us per call, 14336 x
     // 4096, 512 / 768 workgroups: M = 1 16.5 / 16.0, M = 8 20.3 / 21.7)
     const int64_t most = M <= 2 ? 3 * kCUs : 2 * kCUs;
@@ -48,9 +52,12 @@ int make_f8_plan(int64_t M, int64_t N, int64_t K, bool given, F8Plan* p) {
   // The tiled kernel from 9 src1 rows on matrices of 32 MiB or more, else from
   // 25 (us per call with INIT, M = 16 / 24 / 32: 14336 x 4096, skinny 26.4 / 38.8 /
   // 42.5 against 64 x 128 tiles 21.3 / 21.6 / 21.8; 4096 x 4096, skinny 11.3 / 12.9 /
-  // 14.0 against 64 x 64 tiles 12.7 / 12.8 / 13.0).
+  // 14.0 against 64 x 64 tiles 12.7 / 12.8 / 13.0), and for any number where K is
+  // short and the rows are many (M = 1 / 8: 16384 x 1024, skinny 15.7 / 19.3, tiled
+  // 9.5 / 9.9; 65536 x 2048 51.8 / 61.4, 34.4 / 33.3; with K = 4096 59.1 / 66.5, 71.8 /
+  // 70.4).
   const bool large = N * K >= ((int64_t)1 << 25);
-  const bool wide = M > (large ? 8 : 24);
+  const bool wide = M > (large ? 8 : 24) || (brief && groups >= 2 * kCUs);
   // Output tile by M (us per call, 64 x 128, 128 x 128 and 128 x 256 tiles: 14336 x
   // 4096, M = 128 31.4 / 36.2 / 40.4, M = 256 57.0 / 47.9 / 54.4, M = 512 106.0 /
   // 90.8 / 77.9; 4096 x 14336, M = 128 32.9 / 36.4 / 41.1, M = 600 158.7 / 125.2 /

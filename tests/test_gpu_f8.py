@@ -89,6 +89,7 @@ def test_quantize_edge_values():
     (128, 256, 14336), (129, 257, 288), (300, 700, 1184), (512, 1024, 4096), (1, 40, 131072), (4, 40, 131072),
     (8, 300, 4096), (8, 300, 4128), (16, 65, 2048), (9, 8192, 4096), (70, 8200, 4128), (200, 130, 8224),
     (260, 16500, 2080), (24, 1100, 4096), (25, 1100, 4096), (300, 16500, 2080), (600, 4200, 1056), (1100, 4200, 160), (40, 33000, 160),
+    (1, 16500, 160), (4, 8200, 1056), (16, 12300, 2048), (2, 16500, 2080),
 ])
 def test_products(m, n, k):
     qs = _qs()
