@@ -23,9 +23,12 @@
 //   the sums).  Two MFMAs per block; the matrix cores are idle otherwise.
 //   Rounding them to 8 bits, as the quantized products do, would save
 //   nothing here: the activations' bytes are few.
-// * A block's result C[m][n] enters the fp32 sum as C * (dw * s), dw the
-//   weights' scale and s the activations' block scale (times w in the down
-//   product).  Token m of a pass of up to 16 sits in row 4 (m % 4) + m / 4, so
+// * A block's result C[m][n] enters the fp32 sum as (C * dw) * s, dw the
+//   weights' scale and s the activations' block scale; the down product's w
+//   multiplies the sum over a run of blocks.  In this order no factor falls
+//   below fp32's normal range before the sum itself does: dw * s would (h of
+//   1e-33 and e4m3 weights: s is 2^-126).
+//   Token m of a pass of up to 16 sits in row 4 (m % 4) + m / 4, so
 //   that a lane's four result registers are tokens g, 4 + g, 8 + g, 12 + g and
 //   a pass of n tokens scales and adds ceil(n / 4) of them only: this vector
 //   work per block, not the decode, grows with the rows in use.
@@ -399,17 +402,16 @@ struct Acts {
   }
 };
 
-// acc[i][r] += the unit's contribution of RT weight tiles to token 4 r + g;
-// p: a factor per token.
+// acc[i][r] += the unit's contribution of RT weight tiles to token 4 r + g.
 template <int TY, int NR, int RT>
 __device__ __forceinline__ void unit_product(const Acts<NR>& x, const Tile<TY> (&w)[RT],
-                                             const float (&p)[NR], float (&acc)[RT][NR]) {
+                                             float (&acc)[RT][NR]) {
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const v8h hi = __builtin_bit_cast(v8h, x.hi[j]), lo = __builtin_bit_cast(v8h, x.lo[j]);
     float s[NR];
 #pragma unroll
-    for (int r = 0; r < NR; ++r) s[r] = x.scale(r, j) * p[r];
+    for (int r = 0; r < NR; ++r) s[r] = x.scale(r, j);
 #pragma unroll
     for (int i = 0; i < RT; ++i) {
       const v8h wv = w[i].operand(j);
@@ -418,7 +420,7 @@ __device__ __forceinline__ void unit_product(const Acts<NR>& x, const Tile<TY> (
       v4f c = __builtin_amdgcn_mfma_f32_16x16x32_f16(lo, wv, z, 0, 0, 0);
       c = __builtin_amdgcn_mfma_f32_16x16x32_f16(hi, wv, c, 0, 0, 0);
 #pragma unroll
-      for (int r = 0; r < NR; ++r) acc[i][r] = fmaf(c[r], dw * s[r], acc[i][r]);
+      for (int r = 0; r < NR; ++r) acc[i][r] = fmaf(c[r] * dw, s[r], acc[i][r]);
     }
     __builtin_amdgcn_sched_barrier(0);               // one block's operands in registers at a time
   }
@@ -430,8 +432,7 @@ __device__ __forceinline__ void unit_product(const Acts<NR>& x, const Tile<TY> (
 // operands are in registers.
 template <int TY, int NR, int RT>
 __device__ __forceinline__ void run_units(Acts<NR>& x, Tile<TY> (&w0)[RT], int u, int end, int n,
-                                          int nb, const float (&p)[NR], float (&acc)[RT][NR],
-                                          uint8_t* lds, int lane) {
+                                          int nb, float (&acc)[RT][NR], uint8_t* lds, int lane) {
   const uint32_t at = lds_offset(lds), tat = at + Acts<NR>::kLds;
   const auto issue = [&](Tile<TY> (&w)[RT], int v) {
     x.load(v, n, lane, at);
@@ -451,7 +452,7 @@ __device__ __forceinline__ void run_units(Acts<NR>& x, Tile<TY> (&w0)[RT], int u
     for (; u < end; ++u) {
       take(w0);
       if (u + 1 < end) issue(w0, u + 1);
-      unit_product<TY, NR, RT>(x, w0, p, acc);
+      unit_product<TY, NR, RT>(x, w0, acc);
     }
   } else {
     Tile<TY> w1[RT];
@@ -460,11 +461,11 @@ __device__ __forceinline__ void run_units(Acts<NR>& x, Tile<TY> (&w0)[RT], int u
     for (; u < end; u += 2) {
       take(w0);
       if (u + 1 < end) issue(w1, u + 1);
-      unit_product<TY, NR, RT>(x, w0, p, acc);
+      unit_product<TY, NR, RT>(x, w0, acc);
       if (u + 1 >= end) break;
       take(w1);
       if (u + 2 < end) issue(w0, u + 2);
-      unit_product<TY, NR, RT>(x, w1, p, acc);
+      unit_product<TY, NR, RT>(x, w1, acc);
     }
   }
 }
@@ -501,9 +502,7 @@ __device__ __forceinline__ void up_pass(const MoeArgs& a, int e, int rg0, int st
   const int nfb = a.F / 32, nfp = (nfb + 3) & ~3;
   Acts<NR> x;
   x.bind(a.xp, a.xs, nb, n, lane, [&](int m) { return list[m] / a.top_k; });
-  float acc[4][NR], one[NR];
-#pragma unroll
-  for (int r = 0; r < NR; ++r) one[r] = 1.0f;
+  float acc[4][NR];
 #pragma unroll
   for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -584,7 +583,7 @@ __device__ __forceinline__ void up_pass(const MoeArgs& a, int e, int rg0, int st
     __builtin_amdgcn_sched_barrier(0);
     issue_w(w1, rg1 < nfb ? rg1 : rg, rg1 < nfb ? u1 : u);
     const auto finish = [&](Tile<TY> (&w)[4]) {
-      unit_product<TY, NR, 4>(x, w, one, acc);
+      unit_product<TY, NR, 4>(x, w, acc);
       if (u + W >= units) join(rg);
       rg = rg1; u = u1;
       rg1 = rg2; u1 = u2;
@@ -629,7 +628,7 @@ __device__ __forceinline__ void up_pass(const MoeArgs& a, int e, int rg0, int st
       const bool last = u + W >= units;
       const int nrg = last ? rg + step : rg, nu = last ? wave : u + W;
       if (nrg < nfb) issue(next, nrg, nu);
-      unit_product<TY, NR, 4>(x, w, one, acc);
+      unit_product<TY, NR, 4>(x, w, acc);
       if (last) join(rg);
       rg = nrg;
       u = nu;
@@ -824,8 +823,8 @@ __device__ __forceinline__ void make_jobs(Jobs& js, const int* ids, int T, int a
   __syncthreads();
 }
 
-// Units u0 <= u < u1 of one job: acc of RT tiles over the job's tokens, added
-// to the wave's sums[token][16 RT].
+// Units u0 <= u < u1 of one job: acc of RT tiles over the job's tokens, times
+// their weights, added to the wave's sums[token][16 RT].
 template <int TY, int NR, int RT>
 __device__ __forceinline__ void down_job(const MoeArgs& a, int e, int row0, const uint16_t* order,
                                          int n, int u0, int u1, float* sums, uint8_t* lds, int lane) {
@@ -844,13 +843,13 @@ __device__ __forceinline__ void down_job(const MoeArgs& a, int e, int row0, cons
   Tile<TY> w[RT];
 #pragma unroll
   for (int i = 0; i < RT; ++i) w[i].bind(a.down, a.down_scale, e, a.D, a.F, row0 + 16 * i, lane);
-  run_units<TY, NR, RT>(x, w, u0, u1, n, nb, p, acc, lds, lane);
+  run_units<TY, NR, RT>(x, w, u0, u1, n, nb, acc, lds, lane);
 #pragma unroll
   for (int r = 0; r < NR; ++r) {
     if (4 * r + g < n) {
       float* const s = sums + (order[4 * r + g] / a.top_k) * 16 * RT + i16;
 #pragma unroll
-      for (int i = 0; i < RT; ++i) s[16 * i] += acc[i][r];
+      for (int i = 0; i < RT; ++i) s[16 * i] = fmaf(acc[i][r], p[r], s[16 * i]);
     }
   }
 }

@@ -242,3 +242,24 @@ def test_decode_step_quantize_project_route_and_project_again():
     ra, ras = f8.quantize(m.x, 1)
     ref, mag = f8.mul_mat(wq, wqs, ra, ras)
     assert np.all(np.abs(x1 - ref) <= (128 + 4 + 32) * 2.0 ** -23 * mag)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("exponent", [-30, -54, -58])
+def test_small_activations_keep_their_bits(kind, exponent):
+    """Activations of about 2^exponent (h of about its square, dst down to 1e-38, nearly all in fp32's normal range):
+    as accurate as at unit scale, also where only the expert with a weight near 2^-10 adds to dst."""
+    say("moe small", kind, exponent)
+    qs = _qs()
+    m = Layer(kind, 3, 256, 128, 2, 2, 11)
+    m.x = (m.x * np.float32(2.0 ** exponent)).astype(np.float32)
+    m.check(qs.moe_f32(m.layer, to_dev(m.x)), what=f"{kind} 2^{exponent}")
+    m.x[:, 7] = np.float32(2.0 ** exponent)
+    m.router[0] = m.router[1]
+    m.router[1, 7] += np.float32(2.0 ** -exponent * 7)        # weights 1 / (1 + e^-7) and e^-7 / (1 + e^-7)
+    m.dev[2][1].zero_()                                       # zeros are the value 0 in every type
+    m.values[2][1] = 0
+    m.layer = qs.MoeLayer(m.layer.struct.type, to_dev(m.router), *m.dev, 128, 2, *m.layer.tensors[4:])
+    got = qs.moe_f32(m.layer, to_dev(m.x))
+    assert got[1].tolist() == [[1, 0]] * 3 and bool((got[2][:, 1] < 2.0 ** -9).all())
+    m.check(got, what=f"{kind} 2^{exponent}, small weight")
