@@ -403,8 +403,13 @@ class _MoeStruct(ctypes.Structure):
                 ("gate_scale", _vp), ("up_scale", _vp), ("down_scale", _vp)]
 
 
+_MOE_POINTERS = ("router", "gate", "up", "down", "gate_scale", "up_scale", "down_scale")
+_MOE_DTYPES = {MM_TYPE_Q4_0R: (torch.uint8,), MM_TYPE_F8: _F8_DTYPES, MM_TYPE_F16: (torch.float16,)}
+
+
 class MoeLayer:
-    """The weights of a mixture-of-experts layer, for moe_f32 (holds the tensors and the C struct).
+    """The weights of a mixture-of-experts layer, for moe_f32 (holds the tensors and the C struct, whose
+    addresses are the tensors' own at each call).
 
     router float32 [E, D]; gate, up (F x D per expert) and down (D x F) by mm_type:
     MM_TYPE_Q4_0R uint8 [E, repacked_bytes(rows, K)] (repack_q4_0 of each expert), MM_TYPE_F8
@@ -416,23 +421,35 @@ class MoeLayer:
         _dev(router, "router", torch.float32)
         e, d = router.shape
         f, top_k = int(f), int(top_k)
-        dev = router.get_device()
-        dtypes = {MM_TYPE_Q4_0R: (torch.uint8,), MM_TYPE_F8: _F8_DTYPES, MM_TYPE_F16: (torch.float16,)}
-        if mm_type not in dtypes:
+        if mm_type not in _MOE_DTYPES:
             raise ValueError("mm_type must be MM_TYPE_Q4_0R, MM_TYPE_F8 or MM_TYPE_F16")
-        scales = {"gate": gate_scale, "up": up_scale, "down": down_scale}
-        for name, w, rows, k in (("gate", gate, f, d), ("up", up, f, d), ("down", down, d, f)):
-            _on(w, name, (e, repacked_bytes(rows, k)) if mm_type == MM_TYPE_Q4_0R else (e, rows, k),
-                dtypes[mm_type], dev)
-            if mm_type == MM_TYPE_F8:
-                _on(scales[name], f"{name}_scale", (e, _ceil128(rows), _ceil128(k)), _F32, dev)
-            else:
-                scales[name] = None
-        self.dev, self.device, self.d, self.f, self.e, self.top_k = dev, router.device, d, f, e, top_k
-        self.tensors = (router, gate, up, down, *scales.values())
-        self.struct = _MoeStruct(mm_type, top_k, int(bool(norm)), d, f, e, *(_ptr(t) for t in self.tensors))
+        scales = (gate_scale, up_scale, down_scale) if mm_type == MM_TYPE_F8 else (None,) * 3
+        self.dev, self.device, self.d, self.f, self.e, self.top_k = router.get_device(), router.device, d, f, e, top_k
+        self.tensors = (router, gate, up, down, *scales)
+        self.struct = _MoeStruct(mm_type, top_k, int(bool(norm)), d, f, e)
         self._ref = ctypes.byref(self.struct)
         self._sizes = {}
+        self._live = [(t.data_ptr, t.stride) for t in self.tensors if isinstance(t, torch.Tensor)]
+        self._seen = None
+        self._take()
+
+    def _take(self):
+        """The C struct, with the addresses that the tensors have now: a weight that was given other
+        storage or strides since the last call (t.data = ..., set_, a resize) is checked again."""
+        seen = [f() for get in self._live for f in get]
+        if seen != self._seen:
+            kind, d, f, e, dev = self.struct.type, self.d, self.f, self.e, self.dev
+            router, *rest = self.tensors
+            _on(router, "router", (e, d), _F32, dev)
+            for name, w, scale, rows, k in zip(("gate", "up", "down"), rest[:3], rest[3:], (f, f, d), (d, d, f)):
+                _on(w, name, (e, repacked_bytes(rows, k)) if kind == MM_TYPE_Q4_0R else (e, rows, k),
+                    _MOE_DTYPES[kind], dev)
+                if kind == MM_TYPE_F8:
+                    _on(scale, f"{name}_scale", (e, _ceil128(rows), _ceil128(k)), _F32, dev)
+            for field, t in zip(_MOE_POINTERS, self.tensors):
+                setattr(self.struct, field, _ptr(t))
+            self._seen = seen
+        return self._ref
 
     def workspace_size(self, t: int) -> int:
         """Bytes of workspace for t tokens (0: t is out of range, or the layer's sizes are)."""
@@ -459,7 +476,7 @@ def moe_f32(layer: MoeLayer, x: torch.Tensor, out=None, ids=None, weights=None, 
     else:
         _on(weights, "weights", (t, k), _F32, dev)
     out, ws, nbytes = _buffers(t, layer.d, layer.device, dev, out, layer.workspace_size(t), ws)
-    _launch(lib.mm_moe_f32, "mm_moe_f32", dev, layer._ref, x.data_ptr(), out.data_ptr(), ids.data_ptr(),
+    _launch(lib.mm_moe_f32, "mm_moe_f32", dev, layer._take(), x.data_ptr(), out.data_ptr(), ids.data_ptr(),
             weights.data_ptr(), t, None if ws is None else ws.data_ptr(), nbytes)
     return out, ids, weights
 

@@ -145,3 +145,81 @@ def test_binding_refuses_cpu_tensors_and_wrong_shapes():
               lambda: qs.MoeLayer(qs.MM_TYPE_F16, x, x, x, x, 32, 1)):
         with pytest.raises(TypeError):
             f()
+
+
+def _as_gpu(*shape, dtype):
+    """A tensor in host memory that the binding takes for one on GPU 0 (no call here reaches the GPU)."""
+    import torch
+
+    class Fake(torch.Tensor):
+        is_cuda = True
+
+        def get_device(self):
+            return 0
+
+    return torch.zeros(shape, dtype=dtype).as_subclass(Fake)
+
+
+def _fake_layer(kind, d=64, f=32, e=3):
+    import torch
+    if kind == qs.MM_TYPE_Q4_0R:
+        w = [_as_gpu(e, qs.repacked_bytes(n, k), dtype=torch.uint8) for n, k in ((f, d), (f, d), (d, f))]
+    else:
+        dtype = torch.float16 if kind == qs.MM_TYPE_F16 else torch.uint8
+        w = [_as_gpu(e, n, k, dtype=dtype) for n, k in ((f, d), (f, d), (d, f))]
+    scales = [_as_gpu(e, 1, 1, dtype=torch.float32) for _ in range(3)] if kind == qs.MM_TYPE_F8 else [None] * 3
+    return qs.MoeLayer(kind, _as_gpu(e, d, dtype=torch.float32), *w, f, 2, *scales)
+
+
+@pytest.mark.parametrize("kind", [qs.MM_TYPE_Q4_0R, qs.MM_TYPE_F8, qs.MM_TYPE_F16])
+def test_layer_follows_its_tensors_to_other_storage(kind, monkeypatch):
+    """A weight given other storage after the layer was made: the next call reads that one, or refuses it; the
+    address of the freed storage is never passed on."""
+    import torch
+    layer = _fake_layer(kind)
+    x = _as_gpu(2, 64, dtype=torch.float32)
+    sent = []
+
+    def launch(fn, what, dev, ref, *args):
+        sent.append([getattr(layer.struct, n) for n, _ in qs._MoeStruct._fields_[6:]])
+        assert ref is layer._ref
+
+    monkeypatch.setattr(qs, "_launch", launch)
+    bufs = dict(out=_as_gpu(2, 64, dtype=torch.float32), ids=_as_gpu(2, 2, dtype=torch.int32),
+                weights=_as_gpu(2, 2, dtype=torch.float32), ws=_as_gpu(layer.workspace_size(2), dtype=torch.uint8))
+    now = lambda: [None if t is None else t.data_ptr() for t in layer.tensors]
+    qs.moe_f32(layer, x, **bufs)
+    assert sent[-1] == now()
+    for i, t in enumerate(layer.tensors):
+        if t is None:
+            continue
+        kept = t.data                                     # the first storage lives on, so addresses differ
+        t.data = torch.ones_like(kept)
+        assert t.data_ptr() != kept.data_ptr()
+        qs.moe_f32(layer, x, **bufs)
+        assert sent[-1] == now(), i
+        t.resize_((t.shape[0] + 1, *t.shape[1:]))
+        with pytest.raises(ValueError):
+            qs.moe_f32(layer, x, **bufs)
+        t.data = torch.zeros(kept.shape, dtype=torch.float64)
+        with pytest.raises(TypeError):
+            qs.moe_f32(layer, x, **bufs)
+        t.data = kept
+        qs.moe_f32(layer, x, **bufs)
+        assert sent[-1] == now(), i
+    if kind == qs.MM_TYPE_F16:                            # the same storage, read another way
+        gate = layer.tensors[1]
+        gate.transpose_(1, 2)
+        with pytest.raises(ValueError):
+            qs.moe_f32(layer, x, **bufs)
+        gate.transpose_(1, 2)
+        qs.moe_f32(layer, x, **bufs)
+
+
+def test_layer_refuses_what_is_no_tensor():
+    import torch
+    r = _as_gpu(3, 64, dtype=torch.float32)
+    w = _as_gpu(3, 32, 64, dtype=torch.float16)
+    for bad in (None, [1, 2], 3.0):
+        with pytest.raises(TypeError):
+            qs.MoeLayer(qs.MM_TYPE_F16, r, w, bad, w, 32, 2)

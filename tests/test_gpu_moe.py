@@ -263,3 +263,19 @@ def test_small_activations_keep_their_bits(kind, exponent):
     got = qs.moe_f32(m.layer, to_dev(m.x))
     assert got[1].tolist() == [[1, 0]] * 3 and bool((got[2][:, 1] < 2.0 ** -9).all())
     m.check(got, what=f"{kind} 2^{exponent}, small weight")
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_layer_reads_the_storage_that_its_weights_have_now(kind):
+    import torch
+    say("moe new storage", kind)
+    qs = _qs()
+    m, other = Layer(kind, 5, 128, 96, 4, 2, 61), Layer(kind, 5, 128, 96, 4, 2, 62)
+    x = to_dev(m.x)
+    qs.moe_f32(m.layer, x)
+    torch.cuda.synchronize()
+    for mine, new in zip(m.layer.tensors, other.layer.tensors):
+        if mine is not None:
+            mine.data = new.clone()
+    m.values, m.router = other.values, other.router
+    m.check(qs.moe_f32(m.layer, x), what=kind)
