@@ -284,7 +284,12 @@ def mul_mat_f32(w: torch.Tensor, x: torch.Tensor, out=None, ws=None) -> torch.Te
 # ---- e4m3 products and the mixture-of-experts layer: calls of a few microseconds, so their checks are
 # plain attribute comparisons, and sizes that only depend on the shape are computed once
 
-_raw_stream = torch._C._cuda_getCurrentRawStream
+def _public_stream(dev: int) -> int:
+    return torch.cuda.current_stream(dev).cuda_stream
+
+
+# the same handle without a Stream object (a microsecond less); not in every build of torch
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _public_stream)
 _F8_DTYPES = (torch.float8_e4m3fn, torch.uint8)
 
 

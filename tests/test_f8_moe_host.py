@@ -223,3 +223,18 @@ def test_layer_refuses_what_is_no_tensor():
     for bad in (None, [1, 2], 3.0):
         with pytest.raises(TypeError):
             qs.MoeLayer(qs.MM_TYPE_F16, r, w, bad, w, 32, 2)
+
+
+def test_binding_loads_without_the_private_stream_query():
+    """A build of torch that lacks the private name: everything loads, streams come from the public call."""
+    import subprocess
+    import sys
+    code = ("import torch\n"
+            "if hasattr(torch._C, '_cuda_getCurrentRawStream'): del torch._C._cuda_getCurrentRawStream\n"
+            "import quantized_skinny_gemm_amd as qs\n"
+            "assert qs._raw_stream is qs._public_stream\n"
+            "print(qs.workspace_size(qs.MM_TYPE_Q4_0, 5, 64, 64), qs.f8_workspace_size(100, 256, 4096))\n")
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=120,
+                       cwd=__file__.rsplit("/tests/", 1)[0])
+    assert r.returncode == 0, r.stderr
+    assert r.stdout.split() == [str(qs.workspace_size(qs.MM_TYPE_Q4_0, 5, 64, 64)), str(qs.f8_workspace_size(100, 256, 4096))]

@@ -222,3 +222,13 @@ def test_large_weights_past_4_gib():
         av = f8.dequantize(a, a_s, 1)
         err = np.abs(y - av @ wv.T)
         assert np.all(err <= bound(np.abs(av) @ np.abs(wv).T, k)), m
+
+
+def test_both_stream_queries_name_the_current_stream():
+    import torch
+    qs = _qs()
+    say("f8 streams")
+    st = torch.cuda.Stream()
+    assert qs._raw_stream(0) == qs._public_stream(0)
+    with torch.cuda.stream(st):
+        assert qs._raw_stream(0) == qs._public_stream(0) == st.cuda_stream
