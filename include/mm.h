@@ -343,9 +343,11 @@ size_t mm_mul_mat_f8_workspace_size(int64_t M, int64_t N, int64_t K, int src1_qu
  *   batches amortise the weights in the products above).
  * ids (int32) and weights (f32) [T][top_k]: outputs, either may be NULL.
  * ws: mm_moe_workspace_size(layer, T) bytes, 256-byte aligned.
- * A token whose x holds an infinity or NaN (or whose logits do, or whose h
- * overflows) gets NaN in dst; other tokens are unaffected, as they are by a
- * non-finite weight of an expert that they do not use.
+ * A token gets NaN in dst if its x holds an infinity or NaN, if a logit is NaN
+ * or plus infinity, if all of its logits are minus infinity, or if its h
+ * overflows.  Any other logit of minus infinity is a probability of 0 (an
+ * expert that is masked for the token).  Other tokens are unaffected, as they
+ * are by a non-finite weight of an expert that they do not use.
  */
 typedef struct mm_moe_layer {
     int type, top_k, norm;

@@ -279,3 +279,37 @@ def test_layer_reads_the_storage_that_its_weights_have_now(kind):
             mine.data = new.clone()
     m.values, m.router = other.values, other.router
     m.check(qs.moe_f32(m.layer, x), what=kind)
+
+
+@pytest.mark.parametrize("norm", [True, False])
+@pytest.mark.parametrize("t,e", [(1, 6), (5, 6), (40, 64)])
+def test_infinite_logits(t, e, norm):
+    """Minus infinity masks an expert (probability 0, chosen last), also where fewer than top_k are left; plus infinity,
+    or nothing but minus infinity, makes the token NaN; ids stay valid."""
+    say("moe infinite logits", t, e, norm)
+    qs = _qs()
+    m = Layer("f16", t, 96, 64, e, 2, 17, norm=norm)
+    m.x[:, 0] = 1
+    if t > 1:
+        m.x[1, 0] = -1                                        # plus infinity where the others have minus
+    router = m.router.copy()
+
+    def run(masked):
+        m.router = router.copy()
+        m.router[masked, 0] = -np.inf
+        m.layer = qs.MoeLayer(qs.MM_TYPE_F16, to_dev(m.router), *m.dev, 64, 2, norm=norm)
+        return [to_host(v) for v in qs.moe_f32(m.layer, to_dev(m.x))]
+
+    good = [i for i in range(t) if i != 1]
+    best = np.argmax(m.x.astype(np.float64) @ router.T.astype(np.float64), axis=1)
+    for masked in ([int(best[0])], list(range(e - 1)), [0]):
+        dst, ids, w = run(masked)
+        with np.errstate(invalid="ignore"):                   # token 1
+            rd, ri, rw, err = m.oracle()
+        assert np.array_equal(ids[good], ri[good])
+        assert np.all(np.abs(w - rw)[good] <= 2.0 ** -20 * rw[good]) and np.all(np.abs(dst - rd)[good] <= err[good])
+        assert np.all(w[good][np.isin(ids[good], masked)] == 0)
+        if t > 1:
+            assert np.isnan(dst[1]).all() and np.isnan(w[1]).all() and ids[1, 0] == min(masked)
+    dst, ids, w = run(list(range(e)))
+    assert np.isnan(dst).all() and np.isnan(w).all() and np.array_equal(ids, [[0, 1]] * t)
