@@ -567,8 +567,9 @@ __device__ __forceinline__ void up_pass(const MoeArgs& a, int e, int rg0, int st
   if constexpr (Tile<TY>::kAhead == 2) {
     // weights two units ahead, activations one (their LDS is free by then).  The
     // count in body's wait holds because a unit's weights are exactly 4 kLoads
-    // loads, all of them used, and nothing else is loaded behind them (the stores
-    // of a join only make it wait for more).
+    // loads, all of them used (whatever else comes behind them, as the stores of
+    // a join, only makes it wait for more).  That the compiled code has them is
+    // checked by the build (check_counted_waits in build.py).
     int rg1, u1, rg2, u2;
     const auto after = [&](int r, int v, int& rn, int& un) {
       const bool last = v + W >= units;
