@@ -33,13 +33,15 @@ int make_f8_plan(int64_t M, int64_t N, int64_t K, bool given, F8Plan* p) {
 
   // Up to 8 rounds of 32 blocks of 128: every workgroup quantizes src1 itself
   // (at M = 8 and K = 4096 in about the time of an INIT launch).  Below 32 blocks
-  // of K its waves idle in part, and the join of every 16 rows shows, unless the
-  // rows are few (us per call, fused / tiled, M = 1: 8192 x 1024 7.0 / 9.1, 12000 x
-  // 2048 10.8 / 13.0, 16384 x 1024 13.8 / 9.5, 65536 x 512 39.5 / 15.9; with K = 4096
-  // and 65536 rows 53.7 / 71.8).
+  // of K its waves idle in part, and the join of every 16 rows shows: a workgroup
+  // takes about 7 us per group at any K, the tiled kernel the time of the bytes.
+  // So K bounds the rows (us per call, fused / tiled, M = 1: 12500 x 1024 10.8 / 10.7,
+  // 18944 x 1024 13.3 / 11.1, 65536 x 1024 36 / 20; 12500 x 2048 11.4 / 12.9, 24000 x
+  // 2048 16.4 / 16.6, 30000 x 2048 22.3 / 17.8; 18944 x 2560 14.1 / 18.7, 65536 x 2560
+  // 43.1 / 42.3, 152064 x 2560 96.0 / 94.6; 18944 x 3584 15.1 / 23.8, 65536 x 3584 47.7 /
+  // 55.1, 65536 x 4096 52.1 / 69.1).
   const int64_t blocks = M * nkb, groups = ceil_div(N, 16);
-  const bool brief = nkb < 32;
-  if (!given && M <= 16 && blocks <= 256 && (!brief || groups <= 3 * kCUs)) {
+  if (!given && M <= 16 && blocks <= 256 && (nkb >= 20 || groups <= (nkb >= 16 ? 6 : 3) * kCUs)) {
     p->kind = F8_FUSED;
     p->nt = blocks <= 32 ? 1 : blocks <= 64 ? 2 : blocks <= 128 ? 4 : 8;
     // workgroups along N, each walking groups of 16 rows (us per call, 14336 x
@@ -49,15 +51,19 @@ int make_f8_plan(int64_t M, int64_t N, int64_t K, bool given, F8Plan* p) {
     p->lds = (size_t)(M * (nkb * kF8Block + 16)) + align_up((size_t)blocks * 4, 16) + (size_t)M * 512;
     return MM_OK;
   }
-  // The tiled kernel from 9 src1 rows on matrices of 32 MiB or more, else from
-  // 25 (us per call with INIT, M = 16 / 24 / 32: 14336 x 4096, skinny 26.4 / 38.8 /
-  // 42.5 against 64 x 128 tiles 21.3 / 21.6 / 21.8; 4096 x 4096, skinny 11.3 / 12.9 /
-  // 14.0 against 64 x 64 tiles 12.7 / 12.8 / 13.0), and for any number where K is
-  // short and the rows are many (M = 1 / 8: 16384 x 1024, skinny 15.7 / 19.3, tiled
-  // 9.5 / 9.9; 65536 x 2048 51.8 / 61.4, 34.4 / 33.3; with K = 4096 59.1 / 66.5, 71.8 /
-  // 70.4).
+  // The skinny kernel up to 24 src1 rows, 8 on matrices of 32 MiB or more, else the
+  // tiled one (us per call with INIT, M = 16 / 24 / 32: 14336 x 4096, skinny 26.4 / 38.8 /
+  // 42.5 against 64 x 128 tiles 21.3 / 21.6 / 21.8; 4096 x 4096, skinny 11.3 / 12.9 / 14.0
+  // against 64 x 64 tiles 12.7 / 12.8 / 13.0).  With a third workgroup of it on some CU
+  // (over 8192 weight rows) its time steps up, and fewer rows of src1 make up for
+  // that the shorter K is (us per call without INIT, skinny / tiled, M = 1, 4, 8: 8200 x
+  // 1024 8.7 / 8.0, 9.8 / 8.1, 11.3 / 8.0; 12500 x 2560 12.7 / 12.6, 14.4 / 12.5, 15.7 / 12.6;
+  // 18944 x 2816 15.9 / 17.6, 17.4 / 17.8, 18.9 / 17.7; 18944 x 3584 16.6 / 21.2, 17.7 / 21.4,
+  // 19.2 / 21.4; 65536 x 3584, M = 1, 8 53.4 / 53.8, 61.2 / 53.9; 65536 x 4096 58.2 / 67.0,
+  // 66.0 / 68.0; of 8192 rows M = 1 at K = 1024 / 3968 8.0 / 11.7, 8.3 / 13.4).
   const bool large = N * K >= ((int64_t)1 << 25);
-  const bool wide = M > (large ? 8 : 24) || (brief && groups >= 2 * kCUs);
+  const int64_t skinny_rows = groups > 2 * kCUs ? (nkb < 22 ? 0 : nkb < 32 ? 4 : 8) : large ? 8 : 24;
+  const bool wide = M > skinny_rows;
   // Output tile by M (us per call, 64 x 128, 128 x 128 and 128 x 256 tiles: 14336 x
   // 4096, M = 128 31.4 / 36.2 / 40.4, M = 256 57.0 / 47.9 / 54.4, M = 512 106.0 /
   // 90.8 / 77.9; 4096 x 14336, M = 128 32.9 / 36.4 / 41.1, M = 600 158.7 / 125.2 /

@@ -7,6 +7,7 @@ import ctypes
 import pytest
 
 import quantized_skinny_gemm_amd as qs
+from tests import plans
 
 OK, NULL, SHAPE, ALIGN, WS, ALIAS, ARG = 0, -1, -2, -3, -4, -5, -8
 W, WSC, X, XSC, DST, WSP = (0x7f0000000000 + (i << 36) for i in range(6))
@@ -238,3 +239,16 @@ def test_binding_loads_without_the_private_stream_query():
                        cwd=__file__.rsplit("/tests/", 1)[0])
     assert r.returncode == 0, r.stderr
     assert r.stdout.split() == [str(qs.workspace_size(qs.MM_TYPE_Q4_0, 5, 64, 64)), str(qs.f8_workspace_size(100, 256, 4096))]
+
+
+@pytest.mark.parametrize("m,n,k,given,kind", [
+    # one row, K below 4096: the kernel that measures faster at each size
+    (1, 18944, 3584, False, "fused"), (8, 18944, 3584, False, "fused"), (1, 65536, 3584, False, "fused"),
+    (1, 152064, 2560, False, "fused"), (1, 24000, 2048, False, "fused"), (1, 30000, 2048, False, "wide"),
+    (1, 12500, 1024, False, "wide"), (1, 65536, 2304, False, "wide"), (1, 12000, 1024, False, "fused"),
+    (1, 8192, 1024, True, "skinny"), (16, 8192, 3200, True, "skinny"), (1, 8200, 1024, True, "wide"),
+    (4, 18944, 3584, True, "skinny"), (8, 24000, 2816, True, "wide"), (1, 18944, 2560, True, "wide"),
+    (8, 65536, 4096, True, "skinny"), (9, 65536, 4096, True, "wide"),
+])
+def test_kernel_of_a_few_rows(m, n, k, given, kind):
+    assert plans.f8(m, n, k, given).kind == kind
