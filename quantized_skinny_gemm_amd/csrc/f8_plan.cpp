@@ -51,18 +51,31 @@ int make_f8_plan(int64_t M, int64_t N, int64_t K, bool given, F8Plan* p) {
     p->lds = (size_t)(M * (nkb * kF8Block + 16)) + align_up((size_t)blocks * 4, 16) + (size_t)M * 512;
     return MM_OK;
   }
-  // The skinny kernel up to 24 src1 rows, 8 on matrices of 32 MiB or more, else the
-  // tiled one (us per call with INIT, M = 16 / 24 / 32: 14336 x 4096, skinny 26.4 / 38.8 /
-  // 42.5 against 64 x 128 tiles 21.3 / 21.6 / 21.8; 4096 x 4096, skinny 11.3 / 12.9 / 14.0
-  // against 64 x 64 tiles 12.7 / 12.8 / 13.0).  With a third workgroup of it on some CU
-  // (over 8192 weight rows) its time steps up, and fewer rows of src1 make up for
-  // that the shorter K is (us per call without INIT, skinny / tiled, M = 1, 4, 8: 8200 x
-  // 1024 8.7 / 8.0, 9.8 / 8.1, 11.3 / 8.0; 12500 x 2560 12.7 / 12.6, 14.4 / 12.5, 15.7 / 12.6;
-  // 18944 x 2816 15.9 / 17.6, 17.4 / 17.8, 18.9 / 17.7; 18944 x 3584 16.6 / 21.2, 17.7 / 21.4,
-  // 19.2 / 21.4; 65536 x 3584, M = 1, 8 53.4 / 53.8, 61.2 / 53.9; 65536 x 4096 58.2 / 67.0,
-  // 66.0 / 68.0; of 8192 rows M = 1 at K = 1024 / 3968 8.0 / 11.7, 8.3 / 13.4).
+  // Few src1 rows: the skinny kernel, which has 16 weight rows per workgroup and
+  // no split of K across them; else the tiled one.  The most rows for it (us per
+  // call without INIT, skinny / tiled):
+  // - Over 8192 weight rows a third workgroup of it shares a CU and its time steps
+  //   up; the shorter K is, the sooner the tiled kernel is ahead (M = 1, 4, 8: 8200 x
+  //   1024 8.7 / 8.0, 9.8 / 8.1, 11.3 / 8.0; 12500 x 2560 12.7 / 12.6, 14.4 / 12.5, 15.7 /
+  //   12.6; 18944 x 2816 15.9 / 17.6, 17.4 / 17.8, 18.9 / 17.7; 18944 x 3584 16.6 / 21.2,
+  //   17.7 / 21.4, 19.2 / 21.4; 65536 x 3584, M = 1, 8 53.4 / 53.8, 61.2 / 53.9; 65536 x
+  //   4096 58.2 / 67.0, 66.0 / 68.0; of 8192 rows M = 1 at K = 1024 / 3968 8.0 / 11.7,
+  //   8.3 / 13.4).
+  // - Up to 2048 weight rows most CUs have none, and the longer K is, the more the
+  //   tiled kernel's K split gains (M = 1, 8, 16, 24: 1024 x 4096 7 / 10, 7 / 10, 7 / 10,
+  //   9 / 10; 1024 x 8192 7 / 10, 9 / 10, 11 / 10, 15 / 10; 1024 x 14336 12 / 10, 16 / 10,
+  //   20 / 10, 26 / 10; 1024 x 28672 20 / 13, 26 / 14, 33 / 14, 44 / 14; 2048 x 14336 12 / 12,
+  //   16 / 13, 20 / 13, 26 / 13).
+  // - Between: 8 on matrices of 32 MiB or more (4096 x 14336, M = 4, 8, 16 14 / 16, 16 /
+  //   17, 20 / 17; 14336 x 4096, M = 16 with INIT 26.4 / 21.3), else 24, where the two
+  //   tiles of 16 src1 rows past 16 are worth it (M = 16, 24: 4096 x 4096 8 / 12, 10 / 12;
+  //   3200 x 8192 12 / 12, 15 / 13; 7000 x 3200 10.8 / 12.2, 15.2 / 12.2; 8192 x 1024 11.3 /
+  //   11.7, 15.6 / 11.8).
   const bool large = N * K >= ((int64_t)1 << 25);
-  const int64_t skinny_rows = groups > 2 * kCUs ? (nkb < 22 ? 0 : nkb < 32 ? 4 : 8) : large ? 8 : 24;
+  const int64_t skinny_rows = groups > 2 * kCUs    ? (nkb < 22 ? 0 : nkb < 32 ? 4 : 8)
+                              : groups <= kCUs / 2 ? (nkb >= 96 ? 0 : nkb >= 64 ? 8 : 24)
+                              : large              ? 8
+                                                   : (groups <= kCUs && nkb < 64 ? 24 : 16);
   const bool wide = M > skinny_rows;
   // Output tile by M (us per call, 64 x 128, 128 x 128 and 128 x 256 tiles: 14336 x
   // 4096, M = 128 31.4 / 36.2 / 40.4, M = 256 57.0 / 47.9 / 54.4, M = 512 106.0 /

@@ -252,3 +252,16 @@ def test_binding_loads_without_the_private_stream_query():
 ])
 def test_kernel_of_a_few_rows(m, n, k, given, kind):
     assert plans.f8(m, n, k, given).kind == kind
+
+
+@pytest.mark.parametrize("m,n,k,given,kind", [
+    # few weight rows, long K: the kernel that splits K over the CUs
+    (16, 1024, 14336, True, "wide"), (4, 1024, 14336, True, "wide"), (16, 1024, 14336, False, "wide"),
+    (1, 1024, 28672, True, "wide"), (4, 40, 131072, False, "wide"), (16, 2048, 8192, True, "wide"),
+    (8, 2048, 8192, True, "skinny"), (24, 1024, 4096, True, "skinny"), (8, 4096, 14336, True, "skinny"),
+    # a second tile of 16 src1 rows, over and up to 4096 weight rows
+    (24, 8192, 1024, True, "wide"), (24, 7000, 3200, True, "wide"), (16, 7000, 3200, True, "skinny"),
+    (24, 4096, 4096, True, "skinny"), (24, 3200, 8192, True, "wide"), (16, 3200, 8192, True, "skinny"),
+])
+def test_kernel_of_a_few_rows_on_few_weight_rows(m, n, k, given, kind):
+    assert plans.f8(m, n, k, given).kind == kind
