@@ -194,13 +194,12 @@ __device__ __forceinline__ void block_fma(const v8h (&w)[4], const v8h (&a)[4], 
   for (int e = 0; e < 4; ++e) acc[e] = fmaf(c[e], s, acc[e]);
 }
 
-// Each workgroup takes 16 weight rows and NT tiles of 16 src1 rows (codes and
-// scales as INIT or the caller left them), its waves the K blocks wave,
-// wave + W, ... (together they read W * 128 consecutive bytes of each weight
-// row); the waves' partial tiles are added in LDS in wave order.  32 rows
-// per workgroup, sharing each src1 operand, measured slower wherever this
-// kernel is used (4096 x 4096, M = 5 / 16 / 32: 11.9 / 13.2 / 17.9 us against
-// 10.0 / 11.3 / 14.1).
+// Each workgroup takes 16 weight rows and all src1 rows, at most NT tiles of 16
+// (codes and scales as INIT or the caller left them), its waves the K blocks
+// wave, wave + W, ... (together they read W * 128 consecutive bytes of each
+// weight row); the waves' partial tiles are added in LDS in wave order.  32
+// weight rows per workgroup, sharing each src1 operand, measured slower (4096 x
+// 4096, M = 5 / 16: 11.9 / 13.2 us against 10.0 / 11.3).
 template <int NT>
 __global__ __launch_bounds__(512) void k_f8_skinny(
     const uint8_t* __restrict__ w, const float* __restrict__ wsc, const uint8_t* __restrict__ a,
@@ -211,7 +210,7 @@ __global__ __launch_bounds__(512) void k_f8_skinny(
   const int W = blockDim.x >> 6;
   const int g = lane >> 4, i16 = lane & 15;
   const int nkb = (K + kBlk - 1) / kBlk;
-  const int n0 = blockIdx.x * 16, m0 = blockIdx.y * 16 * NT;
+  const int n0 = blockIdx.x * 16;
 
   const uint8_t* const wrow = w + (int64_t)min(n0 + i16, N - 1) * K;
   const float* const wscr = wsc + (int64_t)(n0 / kBlk) * nkb;
@@ -220,7 +219,7 @@ __global__ __launch_bounds__(512) void k_f8_skinny(
   bool live[NT];
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
-    const int m = m0 + 16 * t + i16;
+    const int m = 16 * t + i16;
     live[t] = m < M;
     arow[t] = a + (int64_t)(live[t] ? m : 0) * K;
     ascr[t] = asc + (int64_t)(live[t] ? m : 0) * nkb;
@@ -272,7 +271,7 @@ __global__ __launch_bounds__(512) void k_f8_skinny(
   for (int e = tid; e < TILE; e += blockDim.x) {
     float s = part[e];
     for (int v = 1; v < W; ++v) s += part[v * TILE + e];
-    const int m = m0 + e / 16, n = n0 + e % 16;
+    const int m = e / 16, n = n0 + e % 16;
     if (m < M && n < N) dst[(int64_t)m * N + n] = s;
   }
 }
@@ -627,7 +626,8 @@ namespace {
 template <int NT>
 hipError_t skinny(const F8Plan& p, const uint8_t* w, const float* wsc, const uint8_t* a,
                   const float* asc, float* dst, int M, int N, int K, hipStream_t s) {
-  hipLaunchKernelGGL((k_f8_skinny<NT>), dim3((unsigned)p.grid_n, (unsigned)p.grid_m),
+  if (M > 16 * NT) return hipErrorInvalidValue;       // the plan gives it no more rows
+  hipLaunchKernelGGL((k_f8_skinny<NT>), dim3((unsigned)p.grid_n),
                      dim3(64 * p.waves), p.lds, s, w, wsc, a, asc, M, N, K, dst);
   return hipGetLastError();
 }

@@ -105,8 +105,7 @@ int make_f8_plan(int64_t M, int64_t N, int64_t K, bool given, F8Plan* p) {
     p->waves = 8;
     while (p->waves > 1 && p->waves > nkb) p->waves /= 2;
     p->grid_n = ceil_div(N, 16);
-    p->grid_m = ceil_div(M, 16 * p->nt);
-    if (p->grid_n * p->grid_m * p->waves > kMaxTiles * 8) return MM_ERR_SHAPE;
+    if (p->grid_n * p->waves > kMaxTiles * 8) return MM_ERR_SHAPE;
     p->lds = (size_t)p->waves * 1024 * p->nt;
   } else {
     p->kind = F8_WIDE;

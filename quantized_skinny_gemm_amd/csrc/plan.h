@@ -131,10 +131,10 @@ enum F8Kind { F8_NONE = 0, F8_ZERO = 1, F8_FUSED = 2, F8_SKINNY = 3, F8_WIDE = 4
 
 struct F8Plan {
   int kind = F8_NONE;
-  int nt = 1;                  // skinny: tiles of 16 src1 rows per pass; fused: rounds of the
+  int nt = 1;                  // skinny: tiles of 16 src1 rows; fused: rounds of the
                                // quantization (32 blocks of 128 each)
   int waves = 8;               // skinny: waves per workgroup (they split K)
-  int64_t grid_n = 1, grid_m = 1;
+  int64_t grid_n = 1;          // skinny, fused: workgroups
   size_t lds = 0;              // skinny, fused: LDS bytes
   int bm = 0, bn = 0;          // wide: output tile (src1 rows, weight rows)
   int64_t tiles_m = 1, tiles_n = 1, kchunk = 0;   // wide: K blocks per split

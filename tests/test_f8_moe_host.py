@@ -265,3 +265,14 @@ def test_kernel_of_a_few_rows(m, n, k, given, kind):
 ])
 def test_kernel_of_a_few_rows_on_few_weight_rows(m, n, k, given, kind):
     assert plans.f8(m, n, k, given).kind == kind
+
+
+def test_few_row_kernels_hold_all_rows_of_src1():
+    """The skinny kernel has no second pass over src1 rows, the fused one 16 rows and the LDS of a workgroup."""
+    for m in range(1, 40):
+        for n in (16, 1000, 2049, 4096, 4097, 8192, 8193, 60000):
+            for k in (32, 1056, 2048, 2720, 4096, 8192, 14336, 65536):
+                for given in (False, True):
+                    p = plans.f8(m, n, k, given)
+                    assert p.kind != "skinny" or m <= 16 * p.nt, (m, n, k, given)
+                    assert p.kind != "fused" or m <= 16 and m * -(-k // 128) <= 32 * p.nt, (m, n, k, given)
