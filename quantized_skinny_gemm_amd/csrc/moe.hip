@@ -350,6 +350,9 @@ struct Tile<MM_TYPE_F16> {
   __device__ __forceinline__ float scale(int) const { return 1.0f; }
 };
 
+static_assert((uint64_t)kMoeMaxTokens * kMoeMaxTopK * 4 * kMoeMaxDim < 1ull << 32,
+              "offsets into split h (4 bytes a value, a row per token and expert) fit 32 bits");
+
 // The activations of a pass of up to 4 NR tokens, a unit at a time through
 // the wave's LDS: [row][512 bytes], the 16-byte chunks of a row permuted by
 // row % 16, then the rows' scales [row][4].  Rows past the pass repeat the

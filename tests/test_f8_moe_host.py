@@ -276,3 +276,13 @@ def test_few_row_kernels_hold_all_rows_of_src1():
                     p = plans.f8(m, n, k, given)
                     assert p.kind != "skinny" or m <= 16 * p.nt, (m, n, k, given)
                     assert p.kind != "fused" or m <= 16 and m * -(-k // 128) <= 32 * p.nt, (m, n, k, given)
+
+
+@pytest.mark.parametrize("kind", [qs.MM_TYPE_Q4_0R, qs.MM_TYPE_F8, qs.MM_TYPE_F16])
+@pytest.mark.parametrize("dim", ["D", "F"])
+def test_moe_width_limit(kind, dim):
+    """2^18 is the last width: split h of 128 tokens on 16 experts is 2^31 bytes there, offsets are 32 bits."""
+    size = lambda width: qs.lib.mm_moe_workspace_size(ctypes.byref(_layer(type=kind, E=16, top_k=16, **{dim: width})), 128)
+    assert size(2 ** 18) > 2048 * (4 * 2 ** 18 if dim == "F" else 4 * 128)
+    for width in (2 ** 18 + 32, 2 ** 19, 2 ** 20):
+        assert size(width) == 0 and _moe(_layer(type=kind, **{dim: width}), wsb=0) == SHAPE
