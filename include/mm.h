@@ -326,8 +326,9 @@ size_t mm_mul_mat_f8_workspace_size(int64_t M, int64_t N, int64_t K, int src1_qu
  *     silu(v) = v / (1 + exp(-v))
  *   dst[t] = sum_j weights[t][j] * down_e h[t][j]
  * The activations are not rounded to 8 bits (unlike the quantized products'
- * src1): x and h enter the products with 22 significant bits relative to
- * their block of 32 values, every product is exact and sums are fp32.
+ * src1): x and h enter the products with an error of at most 2^-22 of the
+ * value, or of 2^-39 of the largest of its block of 32 values where that is
+ * more; every product is exact and sums are fp32.
  *
  * The layer (a host struct; the library keeps no reference to it):
  *   type    of the expert matrices:

@@ -17,9 +17,22 @@ def select(x, router, top_k, norm):
     return ids.astype(np.int32), (w / w.sum(axis=1, keepdims=True) if norm else w)
 
 
+def act_error(v):
+    """Bound of |error| per element of v [..., K] where activations are held in blocks of 32 as two binary16 numbers,
+    scaled by a power of two that puts the block's largest magnitude in [2^14, 2^15).
+
+    Of a scaled value in [2^e, 2^(e+1)) the first keeps 11 bits, off by at most 2^(e-11); the second keeps 11 bits of that,
+    off by at most 2^(e-23), or half of binary16's smallest step, 2^-25, where that is more (e < -2).  So the error is at
+    most 2^-23 of the value, or 2^-39 of the block's largest (2^-25 of at least 2^14)."""
+    a = np.abs(v)
+    k = a.shape[-1]
+    top = np.maximum.reduceat(a, np.arange(0, k, 32), axis=-1).repeat(32, axis=-1)[..., :k]
+    return np.maximum(2.0 ** -23 * a, 2.0 ** -39 * top)
+
+
 def layer(x, router, gate, up, down, top_k, norm, act_eps, sum_eps):
-    """dst, ids, weights and a bound of |dst - exact| where activations enter products with relative error
-    act_eps and a product's sum is off by at most sum_eps times the sum of its terms' magnitudes.
+    """dst, ids, weights and a bound of |dst - exact| where activations enter products with an error of act_eps relative
+    and act_error, and a product's sum is off by at most sum_eps times the sum of its terms' magnitudes.
     gate, up [E, F, D] and down [E, D, F] as float64 values."""
     x = x.astype(np.float64)
     ids, w = select(x, router, top_k, norm)
@@ -29,7 +42,8 @@ def layer(x, router, gate, up, down, top_k, norm, act_eps, sum_eps):
         for j in range(top_k):
             e = ids[t, j]
             g, u = gate[e] @ x[t], up[e] @ x[t]
-            eg, eu = c * (np.abs(gate[e]) @ np.abs(x[t])), c * (np.abs(up[e]) @ np.abs(x[t]))
+            ex = c * np.abs(x[t]) + act_error(x[t])
+            eg, eu = np.abs(gate[e]) @ ex, np.abs(up[e]) @ ex
             s = g / (1 + np.exp(-g))
             h = s * u
             # |silu'| <= 1.1; the elementwise part itself within 8 fp32 roundings
@@ -37,5 +51,6 @@ def layer(x, router, gate, up, down, top_k, norm, act_eps, sum_eps):
             y = down[e] @ h
             dst[t] += w[t, j] * y
             # weights within 16 fp32 roundings
-            err[t] += w[t, j] * (np.abs(down[e]) @ eh + c * (np.abs(down[e]) @ (np.abs(h) + eh)) + 2.0 ** -20 * np.abs(y))
+            held = c * (np.abs(h) + eh) + act_error(np.abs(h) + eh)
+            err[t] += w[t, j] * (np.abs(down[e]) @ (eh + held) + 2.0 ** -20 * np.abs(y))
     return dst, ids, w, err

@@ -18,9 +18,11 @@
 //   block of 32 k.
 // * Activations stay fp32 in effect: each row's block of 32 values is scaled
 //   by a power of two that puts its largest magnitude in [2^14, 2^15) and
-//   split as hi + lo, two binary16 numbers (22 significant bits; below 2^-28
-//   of the block's largest value bits are lost, far under fp32 rounding of
-//   the sums).  Two MFMAs per block; the matrix cores are idle otherwise.
+//   split as hi + lo, two binary16 numbers: off by at most 2^-22 of the value
+//   down to 2^-17 of the block's largest, by 2^-39 of the largest below that
+//   (half of binary16's smallest step; far under the fp32 rounding of a sum
+//   that the largest enters).  Two MFMAs per block; the matrix cores are idle
+//   otherwise.
 //   Rounding them to 8 bits, as the quantized products do, would save
 //   nothing here: the activations' bytes are few.
 // * A block's result C[m][n] enters the fp32 sum as (C * dw) * s, dw the

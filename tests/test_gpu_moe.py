@@ -313,3 +313,25 @@ def test_infinite_logits(t, e, norm):
             assert np.isnan(dst[1]).all() and np.isnan(w[1]).all() and ids[1, 0] == min(masked)
     dst, ids, w = run(list(range(e)))
     assert np.isnan(dst).all() and np.isnan(w).all() and np.array_equal(ids, [[0, 1]] * t)
+
+
+@pytest.mark.parametrize("t", [1, 7, 20])
+def test_values_far_below_their_blocks_largest(t):
+    """Activations of 2^-27 of the one large value of their block, which meets zero weights: what is kept of them
+    decides the result.  2^-27 + 0.98 * 2^-39 is held as 2^-27 (the bound's worst case), and all weights are positive,
+    so that these errors add up: past a bound that is relative to each value, within the one that holds."""
+    say("moe far below", t)
+    qs = _qs()
+    m = Layer("f16", t, 64, 32, 2, 1, 41)
+    m.x[:] = np.float32(2.0 ** -27 + 0.98 * 2.0 ** -39)
+    m.x[:, ::32] = 1
+    for w, v in zip(m.dev, m.values):
+        w.abs_()
+        np.abs(v, out=v)
+    for i in (0, 1):
+        m.dev[i][:, :, ::32] = 0
+        m.values[i][:, :, ::32] = 0
+    dst, ids, _ = (to_host(v) for v in qs.moe_f32(m.layer, to_dev(m.x)))
+    rd, ri, _, err = m.oracle()
+    assert np.array_equal(ids, ri) and np.all(np.abs(dst - rd) <= err)
+    assert np.all(np.abs(dst - rd) > 2.0 ** -13 * rd)

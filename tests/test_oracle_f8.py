@@ -81,3 +81,24 @@ def test_moe_layer_is_the_single_expert_mlp():
     a = x @ g[0].T
     want = (a / (1 + np.exp(-a)) * (x @ u[0].T)) @ d[0].T
     assert np.allclose(y, want, rtol=1e-13) and np.all(ids == 0) and np.all(w == 1)
+
+
+def test_error_of_split_activations():
+    """The two-part form in NumPy's binary16 keeps to the bound at every distance from the block's largest value,
+    reaches it, and does not keep 22 bits far below it."""
+    rng = np.random.default_rng(4)
+    v = (rng.uniform(-1, 1, (4000, 32)) * 2.0 ** -rng.integers(0, 34, (4000, 32))).astype(np.float32)
+    v[:, 0] = rng.uniform(0.5, 1, 4000).astype(np.float32)
+    v[0, :2] = 1, 2.0 ** -27 + 2.0 ** -39 * 0.99              # the part below the first is lost whole
+    v *= (2.0 ** rng.integers(-60, 60, (4000, 1))).astype(np.float32)
+    top = np.abs(v).max(axis=1, keepdims=True)
+    shift = 15 - np.frexp(top)[1]                             # largest magnitude in [2^14, 2^15)
+    xs = np.ldexp(v, shift)
+    hi = xs.astype(np.float16)
+    lo = (xs - hi.astype(np.float32)).astype(np.float16)
+    err = np.abs(np.ldexp(hi.astype(np.float64) + lo.astype(np.float64), -shift) - v)
+    bound = moe.act_error(v)
+    assert np.all(err <= bound) and err[0, 1] > 0.98 * bound[0, 1]
+    assert np.any(err > 2.0 ** -13 * np.abs(v))
+    near = np.abs(v) >= 2.0 ** -17 * top
+    assert np.all(err[near] <= 2.0 ** -22 * np.abs(v)[near])
