@@ -286,3 +286,38 @@ def test_moe_width_limit(kind, dim):
     assert size(2 ** 18) > 2048 * (4 * 2 ** 18 if dim == "F" else 4 * 128)
     for width in (2 ** 18 + 32, 2 ** 19, 2 ** 20):
         assert size(width) == 0 and _moe(_layer(type=kind, **{dim: width}), wsb=0) == SHAPE
+
+
+def _gpu_shapes():
+    from tests import test_gpu_f8 as t
+    listed = next(m.args[1] for m in t.test_products.pytestmark if m.name == "parametrize")
+    return listed, t.PLANNED
+
+
+def _kind_of_plan(m, n, k, given):
+    p, tail = plans.f8(m, n, k, given), k % 128 != 0
+    if p.kind != "wide":
+        return p.kind, p.nt, tail
+    uneven = p.split > 1 and -(-k // 128) % p.kchunk != 0
+    return p.bm, p.bn, p.split > 1, uneven, tail
+
+
+def test_gpu_shapes_have_the_plans_that_they_are_listed_for():
+    for shape, want in _gpu_shapes()[1]:
+        p = plans.f8(*shape)
+        if want[0] in ("fused", "skinny"):
+            assert (p.kind, p.nt) == want, shape
+        else:
+            assert (p.bm, p.bn, p.split, p.kchunk) == want and p == plans.f8(*shape, True), shape
+
+
+def test_gpu_shapes_meet_every_kind_of_plan():
+    """Kernel, rounds or tile, K slices even, uneven or one, K ending inside a block or not: whatever the plan gives on a
+    wide grid of calls, a tested shape has it."""
+    listed, planned = _gpu_shapes()
+    tested = {_kind_of_plan(*s, g) for s in [*listed, *(s for s, _ in planned)] for g in (False, True)}
+    for m in (1, 2, 3, 5, 8, 9, 16, 17, 24, 25, 64, 65, 128, 129, 256, 257, 300, 512, 1100, 2048):
+        for n in (16, 300, 1000, 2049, 4096, 5000, 8192, 8200, 12500, 33000, 130000):
+            for k in (32, 128, 160, 1024, 1056, 2080, 2560, 3584, 4096, 4128, 8192, 8224, 11008, 14336, 28672, 32992):
+                for given in (False, True):
+                    assert _kind_of_plan(m, n, k, given) in tested, (m, n, k, given, plans.f8(m, n, k, given))

@@ -232,3 +232,73 @@ def test_both_stream_queries_name_the_current_stream():
     assert qs._raw_stream(0) == qs._public_stream(0)
     with torch.cuda.stream(st):
         assert qs._raw_stream(0) == qs._public_stream(0) == st.cuda_stream
+
+
+# What the shapes of test_products leave out, with the plan that each is here for (tests/test_f8_moe_host.py holds the
+# plans to these, and the shapes of both lists to every kind of plan): (kernel, quantization rounds) or (tiled kernel's src1
+# and weight rows, K slices, blocks of 128 per slice).
+PLANNED = [
+    ((1, 300, 7168), ("fused", 2)), ((2, 12400, 2592), ("fused", 2)), ((8, 12400, 2560), ("fused", 8)),
+    ((24, 1030, 2080), ("skinny", 2)),
+    ((25, 40, 8224), (64, 64, 13, 5)), ((3, 1100, 16384), (64, 64, 13, 10)),
+    ((40, 33000, 1024), (64, 128, 1, 8)), ((9, 2049, 16384), (64, 128, 15, 9)), ((30, 4100, 8224), (64, 128, 7, 10)),
+    ((129, 8200, 4096), (128, 128, 1, 32)), ((257, 16500, 2048), (128, 256, 1, 16)),
+    ((129, 2049, 16384), (128, 128, 7, 19)), ((200, 4100, 8224), (128, 128, 3, 22)), ((200, 4100, 8416), (128, 128, 3, 22)),
+    ((160, 4096, 8192), (128, 128, 4, 16)),
+    ((257, 2049, 16384), (128, 256, 9, 15)), ((300, 4100, 8224), (128, 256, 5, 13)), ((270, 4160, 8096), (128, 256, 5, 13)),
+    ((390, 4100, 8416), (128, 256, 3, 22)), ((512, 4096, 8192), (128, 256, 4, 16)),
+]
+
+
+def _codes(rng, n, k):
+    """Weight codes of every magnitude and both signs, no NaN, with scales."""
+    w = rng.integers(0, 0x7f, (n, k), dtype=np.uint8) | (rng.integers(0, 2, (n, k), dtype=np.uint8) << 7)
+    return w, (1e-4 * rng.uniform(0.75, 1.25, (-(-n // 128), -(-k // 128)))).astype(np.float32)
+
+
+@pytest.mark.parametrize("m,n,k", [shape for shape, _ in PLANNED])
+def test_products_of_every_plan(m, n, k):
+    """Several K slices on each tile (the last one shorter, K ending inside a block), calls on either side of the rules."""
+    import torch
+    qs = _qs()
+    say("f8 planned", m, n, k)
+    rng = np.random.default_rng(m * 1_000_003 + n * 17 + k)
+    w, ws = _codes(rng, n, k)
+    x = _act(rng, m, k)
+    a, a_s = f8.quantize(x, 1)
+    wd, wsd = to_dev(w), to_dev(ws)
+    y = qs.mul_mat_f8_f32(wd, wsd, to_dev(x))
+    check(to_host(y), w, ws, a, a_s, f"f8_f32 {m}x{n}x{k}")
+    y8 = qs.mul_mat_f8_f8(wd, wsd, to_dev(a), to_dev(a_s))
+    check(to_host(y8), w, ws, a, a_s, f"f8_f8 {m}x{n}x{k}")
+    assert torch.equal(y8, qs.mul_mat_f8_f8(wd, wsd, to_dev(a), to_dev(a_s)))
+
+
+@pytest.mark.parametrize("n,k", [(300, 4128), (1100, 2048), (4200, 8224), (8300, 1184)])
+def test_rows_agree_between_batches(n, k):
+    """A src1 row by itself and in larger batches: the same bits wherever the same kernel sums K in the same slices (each
+    kernel's order of blocks depends on K alone), otherwise within the two sums' bounds; and by f32 or by codes."""
+    import torch
+
+    from tests import plans
+    qs = _qs()
+    say("f8 batches", n, k)
+    rng = np.random.default_rng(n + k)
+    w, ws = _codes(rng, n, k)
+    x = _act(rng, 300, k)
+    a, a_s = f8.quantize(x, 1)
+    wd, wsd, xd, ad, asd = (to_dev(v) for v in (w, ws, x, a, a_s))
+    first, seen = None, {}
+    for m in (1, 2, 5, 8, 16, 17, 24, 33, 64, 65, 129, 300):
+        for given in (False, True):
+            y = qs.mul_mat_f8_f8(wd, wsd, ad[:m], asd[:m]) if given else qs.mul_mat_f8_f32(wd, wsd, xd[:m])
+            p = plans.f8(m, n, k, given)
+            other = seen.setdefault((p.kind, p.kchunk), y)
+            rows = min(m, other.shape[0])
+            assert torch.equal(y[:rows], other[:rows]), (m, given, p)
+            if m > other.shape[0]:
+                seen[p.kind, p.kchunk] = y
+            first = y if first is None else first
+            _, mag = f8.mul_mat(w, ws, a[:1], a_s[:1])
+            assert np.all(np.abs(to_host(y[:1]).astype(np.float64) - to_host(first)) <= 2 * bound(mag, k)), (m, given)
+    assert len(seen) > 1
