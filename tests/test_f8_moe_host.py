@@ -321,3 +321,19 @@ def test_gpu_shapes_meet_every_kind_of_plan():
             for k in (32, 128, 160, 1024, 1056, 2080, 2560, 3584, 4096, 4128, 8192, 8224, 11008, 14336, 28672, 32992):
                 for given in (False, True):
                     assert _kind_of_plan(m, n, k, given) in tested, (m, n, k, given, plans.f8(m, n, k, given))
+
+
+def test_gpu_layers_have_the_plans_that_they_are_listed_for():
+    from tests import test_gpu_moe as t
+    kinds = {"q4_0r": qs.MM_TYPE_Q4_0R, "f8": qs.MM_TYPE_F8, "f16": qs.MM_TYPE_F16}
+    d, f, e, k = (t.LONG[n] for n in ("d", "f", "e", "top_k"))
+    for tokens, by_kind in t.LONG_PLANS.items():
+        for kind, want in by_kind.items():
+            p = plans.moe(kinds[kind], tokens, d, f, e, k)
+            assert (p.rt, p.slices) == want, (tokens, kind, p)
+            # units of 128 k for 8 waves: not the same number each; several groups of 32 rows per workgroup
+            assert -(-d // 128) > 16 and -(-d // 128) % 8 and p.up_groups < f // 32, (tokens, kind, p)
+            assert p.fold
+    assert all(plans.moe(v, 70, 96, 16416, 2, 2)[2:] == (1, 4) for v in kinds.values())
+    for e in (300, 200, 512):
+        assert not plans.moe(qs.MM_TYPE_F8, {300: 1, 200: 2, 512: 4}[e], 96, 64, e, 1).fold

@@ -335,3 +335,106 @@ def test_values_far_below_their_blocks_largest(t):
     rd, ri, _, err = m.oracle()
     assert np.array_equal(ids, ri) and np.all(np.abs(dst - rd) <= err)
     assert np.all(np.abs(dst - rd) > 2.0 ** -13 * rd)
+
+
+# A layer whose waves take several units of K in a row group and several row groups, and whose down is cut in slices;
+# (T, plan of each kind as rt, slices), held to the plans by tests/test_f8_moe_host.py.
+LONG = dict(d=2112, f=16416, e=2, top_k=2)
+LONG_PLANS = {3: {"q4_0r": (1, 1), "f8": (1, 1), "f16": (1, 1)}, 7: {"q4_0r": (4, 4), "f8": (2, 4), "f16": (4, 4)},
+              16: {"q4_0r": (4, 4), "f8": (2, 4), "f16": (4, 4)}, 24: {"q4_0r": (4, 4), "f8": (2, 4), "f16": (4, 4)},
+              40: {"q4_0r": (2, 4), "f8": (1, 1), "f16": (2, 4)}, 100: {"q4_0r": (1, 1), "f8": (1, 1), "f16": (1, 1)}}
+
+
+class LongLayer:
+    """Random codes and scales; the float64 values are on the GPU, where the reference is computed."""
+
+    def __init__(self, kind):
+        import torch
+        qs = _qs()
+        d, f, e, k = (LONG[n] for n in ("d", "f", "e", "top_k"))
+        rng = np.random.default_rng(97)
+        self.values, dev, scales = [], [], []
+        for n, width in ((f, d), (f, d), (d, f)):
+            if kind == "q4_0r":
+                q = rng.integers(0, 256, (e * n * width // 32, 18), dtype=np.uint8)
+                q[:, :2] = (0.01 * rng.uniform(0.75, 1.25, len(q))).astype(np.float16).view(np.uint8).reshape(-1, 2)
+                q = q.reshape(e, n, -1)
+                values = np.stack([codec.dequantize_q4_0(v, width) for v in q])
+                dev.append(torch.stack([qs.repack_q4_0(to_dev(v), width) for v in q]))
+                scales.append(None)
+            elif kind == "f8":
+                c = rng.integers(0, 0x7f, (e, n, width), dtype=np.uint8) | (rng.integers(0, 2, (e, n, width), dtype=np.uint8) << 7)
+                s = (4e-4 * rng.uniform(0.75, 1.25, (e, -(-n // 128), -(-width // 128)))).astype(np.float32)
+                values = np.stack([f8.dequantize(c[i], s[i], 128) for i in range(e)])
+                dev.append(to_dev(c))
+                scales.append(to_dev(s))
+            else:
+                values = (rng.standard_normal((e, n, width), dtype=np.float32) * 0.05).astype(np.float16)
+                dev.append(to_dev(values))
+                scales.append(None)
+            self.values.append(to_dev(values).double())
+        self.x = rng.standard_normal((100, d)).astype(np.float32)
+        self.router = (rng.standard_normal((e, d)) / np.sqrt(d)).astype(np.float32)
+        code = {"q4_0r": qs.MM_TYPE_Q4_0R, "f8": qs.MM_TYPE_F8, "f16": qs.MM_TYPE_F16}[kind]
+        self.layer = qs.MoeLayer(code, to_dev(self.router), *dev, f, k, *scales)
+
+    def reference(self, t):
+        """moe.layer's dst and bound, every expert on every token (top_k = E)."""
+        import torch
+        x = self.x[:t].astype(np.float64)
+        ids, w = moe.select(x, self.router, 2, True)
+        c = ACT_EPS + sum_eps(max(LONG["d"], LONG["f"]))
+        xd, ex = to_dev(x), to_dev(c * np.abs(x) + moe.act_error(x))
+        dst, err = torch.zeros_like(xd), torch.zeros_like(xd)
+        for e in range(LONG["e"]):
+            gate, up, down = (v[e] for v in self.values)
+            p = to_dev(np.sum(np.where(ids == e, w, 0), axis=1))[:, None]
+            g, u = xd @ gate.t(), xd @ up.t()
+            eg, eu = ex @ gate.abs().t(), ex @ up.abs().t()
+            s = g / (1 + torch.exp(-g))
+            h = s * u
+            eh = 1.1 * eg * (u.abs() + eu) + s.abs() * eu + 8 * 2.0 ** -24 * h.abs()
+            y = h @ down.t()
+            held = to_dev(moe.act_error(to_host(h.abs() + eh))) + c * (h.abs() + eh)
+            dst += p * y
+            err += p * ((eh + held) @ down.abs().t() + 2.0 ** -20 * y.abs())
+        return to_host(dst), ids, w, to_host(err)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_waves_take_several_units_of_several_row_groups(kind):
+    """3 to 100 tokens on both experts: passes of up to 4, 8 and 16, down in several slices of 64- and 32-row workgroups and
+    in one of 16-row ones; repeated calls give the same bits."""
+    import torch
+    say("moe long", kind)
+    qs = _qs()
+    m = LongLayer(kind)
+    for t in LONG_PLANS:
+        say("moe long", kind, t)
+        x = to_dev(m.x[:t])
+        got = qs.moe_f32(m.layer, x)
+        dst, ids, w = (to_host(v) for v in got)
+        rd, ri, rw, err = m.reference(t)
+        assert np.array_equal(ids, ri) and np.all(np.abs(w - rw) <= 2.0 ** -20 * rw), t
+        assert np.all(np.abs(dst - rd) <= err), f"{t}: {np.max(np.abs(dst - rd) / err):.3g} of the bound"
+        assert np.linalg.norm(dst - rd) <= 3e-6 * np.linalg.norm(rd), t
+        for _ in range(3):
+            assert all(torch.equal(a, b) for a, b in zip(got, qs.moe_f32(m.layer, x))), t
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("t,e,top_k", [(1, 300, 4), (2, 200, 16), (4, 512, 1)])
+def test_few_tokens_with_the_selection_launched_by_itself(kind, t, e, top_k):
+    say("moe select", kind, t, e, top_k)
+    m = Layer(kind, t, 96, 64, e, top_k, t + e)
+    m.check(_qs().moe_f32(m.layer, to_dev(m.x)), what=f"{kind} T={t} E={e} k={top_k}")
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_many_tokens_with_down_in_slices_of_16_rows(kind):
+    say("moe slices", kind)
+    qs = _qs()
+    m = Layer(kind, 70, 96, 16416, 2, 2, 29)
+    got = qs.moe_f32(m.layer, to_dev(m.x))
+    m.check(got, what=kind)
+    assert all(np.array_equal(to_host(a), to_host(b)) for a, b in zip(got, qs.moe_f32(m.layer, to_dev(m.x))))
