@@ -298,9 +298,12 @@ mm_status mm_quantize_f8(const float* x, void* codes, float* scales, int64_t nro
  *   (one mm_quantize_f8, block_rows 1, ahead of several products): src1 codes
  *   [M][K], scale1 [M][ceil(K/128)].  ws: mm_mul_mat_f8_workspace_size(M, N,
  *   K, 1) bytes.
- * dst[m][n] = sum_b scale1[m][b] * scale0[n/128][b] * S_b[m][n], S_b the
- * fp32 sum of the block's code products (each exact); a NaN code or a
- * non-finite scale makes the outputs it enters NaN or infinite and no other.
+ * dst[m][n] = sum_b (scale1[m][b] * scale0[n/128][b]) * S_b[m][n], S_b the
+ * fp32 sum of the block's code products (each exact), the scales' product
+ * rounded to fp32 first: below 2^-126 (src1 of less than about 1e-31 with weights of
+ * ordinary size) it keeps fewer bits, past fp32's range it is infinite.  A NaN
+ * code or a non-finite scale, or product of scales, makes the outputs it enters
+ * NaN or infinite and no other.
  * mm_mul_mat_workspace_size(MM_TYPE_F8, ...) is the size for f32 src1 (a few
  * rows of f32 may need none where src1 as codes needs some),
  * mm_row_bytes(MM_TYPE_F8, K) the bytes of a row of codes; mm_dispatch and

@@ -302,3 +302,24 @@ def test_rows_agree_between_batches(n, k):
             _, mag = f8.mul_mat(w, ws, a[:1], a_s[:1])
             assert np.all(np.abs(to_host(y[:1]).astype(np.float64) - to_host(first)) <= 2 * bound(mag, k)), (m, given)
     assert len(seen) > 1
+
+
+@pytest.mark.parametrize("m", [1, 24, 70])
+@pytest.mark.parametrize("exponent", [-110, -100, 100, 118])
+def test_smallest_and_largest_scales(m, exponent):
+    """Activations near both ends of fp32's range on each kernel.  The scales' product is rounded once, to 2^-24 of itself
+    (in bound()) or to 2^-150 below the normal range, which each block's sum then multiplies."""
+    qs = _qs()
+    say("f8 scales", m, exponent)
+    rng = np.random.default_rng(m)
+    n, k = 300, 1056
+    w, ws = _codes(rng, n, k)
+    x = np.ldexp(rng.uniform(-1, 1, (m, k)), exponent).astype(np.float32)
+    a, a_s = f8.quantize(x, 1)
+    ref, mag = f8.mul_mat(w, ws, a, a_s)
+    assert np.all(mag < 2.0 ** 127)
+    sums = np.abs(f8.VALUES[a]) @ np.abs(f8.VALUES[w]).T
+    tol = bound(mag, k) + 2.0 ** -150 * sums + (k // 128 + 40) * 2.0 ** -149
+    for y in (qs.mul_mat_f8_f32(to_dev(w), to_dev(ws), to_dev(x)),
+              qs.mul_mat_f8_f8(to_dev(w), to_dev(ws), to_dev(a), to_dev(a_s))):
+        assert np.all(np.abs(to_host(y) - ref) <= tol)
