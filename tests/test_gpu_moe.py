@@ -438,3 +438,23 @@ def test_many_tokens_with_down_in_slices_of_16_rows(kind):
     got = qs.moe_f32(m.layer, to_dev(m.x))
     m.check(got, what=kind)
     assert all(np.array_equal(to_host(a), to_host(b)) for a, b in zip(got, qs.moe_f32(m.layer, to_dev(m.x))))
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("t,e", [(1, 8), (20, 8), (40, 64)])
+def test_ids_and_weights_may_be_null(kind, t, e):
+    """The C entry point without the two outputs, whoever makes the selection: the same dst."""
+    import torch
+    say("moe null outputs", kind, t, e)
+    qs = _qs()
+    m = Layer(kind, t, 96, 64, e, 3, 53)
+    x = to_dev(m.x)
+    want = qs.moe_f32(m.layer, x)[0]
+    ws = torch.full((m.layer.workspace_size(t),), 0xff, dtype=torch.uint8, device="cuda")
+    for ids, w in ((None, None), (torch.empty((t, 3), dtype=torch.int32, device="cuda"), None),
+                   (None, torch.empty((t, 3), device="cuda"))):
+        out = torch.full((t, 96), 7.0, device="cuda")
+        st = qs.lib.mm_moe_f32(m.layer._ref, x.data_ptr(), out.data_ptr(), None if ids is None else ids.data_ptr(),
+                               None if w is None else w.data_ptr(), t, ws.data_ptr(), ws.numel(),
+                               torch.cuda.current_stream().cuda_stream)
+        assert st == 0 and torch.equal(out, want)
