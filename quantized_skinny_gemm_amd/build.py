@@ -11,11 +11,9 @@ the objects are linked into ``quantized_skinny_gemm_amd/libqsgemm.so``.
 from __future__ import annotations
 
 import os
-import re
 import shutil
 import subprocess
 import sys
-import tempfile
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -62,65 +60,6 @@ def _run(cmd):
     return r
 
 
-def _disassemble(obj: str) -> str:
-    """The gfx950 code of an object, as llvm-objdump lists it."""
-    root = os.path.dirname(os.path.dirname(os.path.realpath(_hipcc())))
-    tools = [os.path.join(root, d, "bin", "llvm-objdump") for d in ("llvm", "lib/llvm", ".")]
-    tool = next((t for t in tools if os.path.exists(t)), None) or shutil.which("llvm-objdump")
-    if tool is None:
-        raise RuntimeError("llvm-objdump not found (ROCm's LLVM has it)")
-    with tempfile.TemporaryDirectory() as tmp:
-        local = os.path.join(tmp, "x.o")
-        shutil.copy(obj, local)
-        subprocess.run([tool, "--offloading", local], check=True, capture_output=True, cwd=tmp)
-        code = [f for f in os.listdir(tmp) if ARCH in f]
-        return _run([tool, "-d", os.path.join(tmp, code[0])]).stdout
-
-
-# Kernels whose waits count on loads that the compiler issues, with the count: see up_pass in moe.hip.
-COUNTED_WAITS = {"moe.hip": ("k_moe_upILi4E", 8)}
-
-
-def check_counted_waits(listing: str, kernel: str, count: int) -> int:
-    """Checks in a disassembly that a wait for all but `count` memory operations leaves only register loads under
-    way: behind the last copy to LDS ahead of it, and behind every other one that loads follow, there are
-    `count` of them at least, with no branch between.  (One that was merged with another or left out would make
-    the wait end before the copies have arrived.)  Returns the number of such waits; raises RuntimeError."""
-    waits = 0
-    for name, body in re.findall(r"^[0-9a-f]+ <(\S+)>:\n(.*?)(?=^[0-9a-f]+ <|\Z)", listing, re.M | re.S):
-        if kernel not in name:
-            continue
-        here = filled = 0
-        loads, open_ = None, False          # register loads since the last copy; None: none yet
-        for line in body.splitlines():
-            op = line.split("//")[0].strip()
-            wait = re.match(r"s_waitcnt .*?vmcnt\((\d+)\)", op)
-            if op.startswith("global_load_lds"):
-                if loads and loads < count:
-                    raise RuntimeError(f"{name}: {loads} loads behind a copy to LDS, not {count}")
-                loads, open_ = 0, True
-            elif op.startswith(("global_load", "buffer_load", "flat_load")) and open_:
-                loads += 1
-                filled += loads == count
-            elif op.startswith(("s_branch", "s_cbranch")) and loads:
-                open_ = False
-            elif re.match(rf"s_waitcnt vmcnt\({count}\) lgkmcnt\(0\)", op):
-                here += 1
-                if loads is None or loads < count:
-                    raise RuntimeError(f"{name}: {loads} loads ahead of a wait for all but {count}")
-            elif wait and int(wait.group(1)) == 0:
-                if loads and loads < count:
-                    raise RuntimeError(f"{name}: {loads} loads behind a copy to LDS, not {count}")
-                loads, open_ = None, False
-        # one wait per unit in a round of three, and the loads ahead of the round besides
-        if here == 0 or 3 * filled != 4 * here:
-            raise RuntimeError(f"{name}: {here} counted waits, {filled} sets of {count} loads")
-        waits += here
-    if waits == 0:
-        raise RuntimeError(f"no kernel {kernel} with a counted wait")
-    return waits
-
-
 def build(verbose: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
     hipcc = _hipcc()
@@ -139,8 +78,6 @@ def build(verbose: bool = False) -> str:
         for r in ex.map(_run, jobs):
             if verbose and (r.stdout or r.stderr):
                 print(r.stdout + r.stderr)
-    for src, (kernel, count) in COUNTED_WAITS.items():
-        check_counted_waits(_disassemble(os.path.join(BUILD, src + ".o")), kernel, count)
     tmp = LIB + ".tmp"
     _run([hipcc, f"--offload-arch={ARCH}", "-shared", "-fPIC", *objs, "-ldl", "-o", tmp])
     os.replace(tmp, LIB)

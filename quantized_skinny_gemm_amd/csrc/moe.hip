@@ -42,13 +42,13 @@
 //   computed from registers, the next one's weights are on their way to
 //   registers and its activations (512 consecutive bytes per row; e4m3
 //   weights too) to the wave's own piece of LDS, from which a lane takes its
-//   operand.  A Q4_0R unit is so small that one ahead keeps too few bytes under
-//   way: gate / up has two of them (layer, 4 / 16 / 32 tokens, 8 experts of
-//   4096 x 14336: 113 / 220 / 246 us before, 103 / 206 / 236 with).  In down the
-//   same changed nothing.  Loading operands straight from memory costs one 16-byte access
-//   per lane, since neighbouring lanes belong to different rows: the address
-//   units were 67% busy and the gate / up launch at 2.9 TB/s (32 tokens, 8
-//   experts of 4096 x 14336).
+//   operand.  (Weights two units ahead in gate / up, Q4_0R, measured no faster:
+//   layer, 1 / 16 / 64 tokens, 8 experts of 4096 x 14336, 65 / 204 / 371 us against
+//   61 / 200 / 364, and its wait had to count loads that the compiler issues; in
+//   down nothing changed.)  Loading operands straight from memory costs one
+//   16-byte access per lane, since neighbouring lanes belong to different rows:
+//   the address units were 67% busy and the gate / up launch at 2.9 TB/s (32
+//   tokens, 8 experts of 4096 x 14336).
 #include "device.h"
 #include "kernels.h"
 #include "../../include/mm.h"
@@ -239,14 +239,13 @@ __global__ __launch_bounds__(512) void k_moe_select(const double* __restrict__ l
 // expert e's matrix of N rows of K; load(): issues a unit's loads; fetch():
 // takes what load() sent through LDS (kLds bytes at lds), or tells the
 // compiler that its loads have arrived; operand(j): block j as binary16, row
-// lane % 16, in lane group order; scale(j): its dw.  kAhead: units of weights
-// that gate / up has under way; kLoads: loads of one (kAhead 2).
+// lane % 16, in lane group order; scale(j): its dw.
 template <int TY>
 struct Tile;
 
 template <>
 struct Tile<MM_TYPE_Q4_0R> {
-  static constexpr int kLds = 0, kAhead = 2, kLoads = 2;
+  static constexpr int kLds = 0;
   const uint8_t* base;
   v4u c;                         // whole vectors, so that they stay in the registers that
   v2u d;                         // the loads fill
@@ -287,7 +286,7 @@ struct Tile<MM_TYPE_Q4_0R> {
 // permuted by (row / 2) % 8): a lane's operand is 8 bytes of its row.
 template <>
 struct Tile<MM_TYPE_F8> {
-  static constexpr int kLds = 2048, kAhead = 1;
+  static constexpr int kLds = 2048;
   const uint8_t* base;           // uniform
   const float* sc;
   uint32_t off[2];               // the rows this lane copies
@@ -332,7 +331,7 @@ struct Tile<MM_TYPE_F8> {
 
 template <>
 struct Tile<MM_TYPE_F16> {
-  static constexpr int kLds = 0, kAhead = 1;
+  static constexpr int kLds = 0;
   const uint8_t* base;
   uint4 c[4];
   __device__ __forceinline__ void bind(const uint8_t* w, const float*, int64_t e, int N, int K,
@@ -569,87 +568,31 @@ __device__ __forceinline__ void up_pass(const MoeArgs& a, int e, int rg0, int st
   }
   // one unit of row group rg; the next one's loads; the join after the last
   int rg = rg0, u = wave;
-  if constexpr (Tile<TY>::kAhead == 2) {
-    // weights two units ahead, activations one (their LDS is free by then).  The
-    // count in body's wait holds because a unit's weights are exactly 4 kLoads
-    // loads, all of them used (whatever else comes behind them, as the stores of
-    // a join, only makes it wait for more).  That the compiled code has them is
-    // checked by the build (check_counted_waits in build.py).
-    int rg1, u1, rg2, u2;
-    const auto after = [&](int r, int v, int& rn, int& un) {
-      const bool last = v + W >= units;
-      rn = last ? r + step : r;
-      un = last ? wave : v + W;
-    };
-    after(rg, u, rg1, u1);
-    Tile<TY> w0[4], w1[4], w2[4];
-    issue_w(w0, rg, u);
-    __builtin_amdgcn_sched_barrier(0);
-    x.load(u, n, lane, at);
-    __builtin_amdgcn_sched_barrier(0);
-    issue_w(w1, rg1 < nfb ? rg1 : rg, rg1 < nfb ? u1 : u);
-    const auto finish = [&](Tile<TY> (&w)[4]) {
-      unit_product<TY, NR, 4>(x, w, acc);
-      if (u + W >= units) join(rg);
-      rg = rg1; u = u1;
-      rg1 = rg2; u1 = u2;
-    };
-    const auto body = [&](Tile<TY> (&w)[4], Tile<TY> (&next)[4]) {
-      __builtin_amdgcn_sched_barrier(0);
-      wait_copies<4 * Tile<TY>::kLoads>();           // all but the next unit's weights
-      fetch(w);
-      after(rg1, u1, rg2, u2);
-      x.load(rg1 < nfb ? u1 : u, n, lane, at);
-      __builtin_amdgcn_sched_barrier(0);
-      issue_w(next, rg2 < nfb ? rg2 : rg, rg2 < nfb ? u2 : u);   // past the end: read again
-      __builtin_amdgcn_sched_barrier(0);
-      finish(w);
-    };
-    const auto tail = [&](Tile<TY> (&w)[4], bool more) {
-      wait_copies<0>();
-      fetch(w);
-      if (more) x.load(u1, n, lane, at);
-      finish(w);
-    };
-    // whole rounds, then the rest: a loop with exits between the bodies would
-    // make the compiler wait as if each could follow each
-    int left = ((units - wave + W - 1) / W) * ((nfb - rg0 + step - 1) / step);
-    for (; left >= 3; left -= 3) {
-      body(w0, w2);
-      body(w1, w0);
-      body(w2, w1);
-    }
-    rg2 = u2 = 0;
-    if (left > 0) tail(w0, left > 1);
-    if (left > 1) tail(w1, false);
+  const auto issue = [&](Tile<TY> (&w)[4], int r, int v) {
+    x.load(v, n, lane, at);
+    issue_w(w, r, v);
+  };
+  const auto body = [&](Tile<TY> (&w)[4], Tile<TY> (&next)[4]) {
     wait_copies<0>();
+    fetch(w);
+    const bool last = u + W >= units;
+    const int nrg = last ? rg + step : rg, nu = last ? wave : u + W;
+    if (nrg < nfb) issue(next, nrg, nu);
+    unit_product<TY, NR, 4>(x, w, acc);
+    if (last) join(rg);
+    rg = nrg;
+    u = nu;
+  };
+  Tile<TY> w0[4];
+  issue(w0, rg, u);
+  if constexpr (Tile<TY>::kLds > 0) {
+    while (rg < nfb) body(w0, w0);
   } else {
-    const auto issue = [&](Tile<TY> (&w)[4], int r, int v) {
-      x.load(v, n, lane, at);
-      issue_w(w, r, v);
-    };
-    const auto body = [&](Tile<TY> (&w)[4], Tile<TY> (&next)[4]) {
-      wait_copies<0>();
-      fetch(w);
-      const bool last = u + W >= units;
-      const int nrg = last ? rg + step : rg, nu = last ? wave : u + W;
-      if (nrg < nfb) issue(next, nrg, nu);
-      unit_product<TY, NR, 4>(x, w, acc);
-      if (last) join(rg);
-      rg = nrg;
-      u = nu;
-    };
-    Tile<TY> w0[4];
-    issue(w0, rg, u);
-    if constexpr (Tile<TY>::kLds > 0) {
-      while (rg < nfb) body(w0, w0);
-    } else {
-      Tile<TY> w1[4];
-      while (rg < nfb) {
-        body(w0, w1);
-        if (rg >= nfb) break;
-        body(w1, w0);
-      }
+    Tile<TY> w1[4];
+    while (rg < nfb) {
+      body(w0, w1);
+      if (rg >= nfb) break;
+      body(w1, w0);
     }
   }
 }
