@@ -399,7 +399,7 @@ __global__ __launch_bounds__(512) void k_f8_fused(
 // 16 rows of an operand read lie in different banks.  Lane half h of an MFMA
 // holds k 32 p + 16 h + 8 (q % 2) .. + 7, p = q / 2: one chunk serves two q.
 //
-// What bounds it, at 512 x 128256 x 4096 (128 x 256 tiles): 610 us, 880 TFLOP/s.
+// What bounds it, at 512 x 128256 x 4096 (128 x 256 tiles): 613 us, 880 TFLOP/s.
 // Without the copies, the widening, the scaling and the barriers the same MFMAs
 // take 407 us (1320 TFLOP/s, what the card's power leaves of the matrix cores; a
 // library product of 8192^3 in binary16 reaches 1285), with LDS reads and

@@ -45,7 +45,7 @@ int make_f8_plan(int64_t M, int64_t N, int64_t K, bool given, F8Plan* p) {
     p->kind = F8_FUSED;
     p->nt = blocks <= 32 ? 1 : blocks <= 64 ? 2 : blocks <= 128 ? 4 : 8;
     // workgroups along N, each walking groups of 16 rows (us per call, 14336 x
-    // 4096, 512 / 768 workgroups: M = 1 16.5 / 16.0, M = 8 20.3 / 21.7)
+    // 4096, 512 / 768 workgroups: M = 1 15.1 / 14.3, M = 8 18.5 / 20.1)
     const int64_t most = M <= 2 ? 3 * kCUs : 2 * kCUs;
     p->grid_n = groups < most ? groups : most;
     p->lds = (size_t)(M * (nkb * kF8Block + 16)) + align_up((size_t)blocks * 4, 16) + (size_t)M * 512;
@@ -67,7 +67,7 @@ int make_f8_plan(int64_t M, int64_t N, int64_t K, bool given, F8Plan* p) {
   //   20 / 10, 26 / 10; 1024 x 28672 20 / 13, 26 / 14, 33 / 14, 44 / 14; 2048 x 14336 12 / 12,
   //   16 / 13, 20 / 13, 26 / 13).
   // - Between: 8 on matrices of 32 MiB or more (4096 x 14336, M = 4, 8, 16 14 / 16, 16 /
-  //   17, 20 / 17; 14336 x 4096, M = 16 with INIT 26.4 / 21.3), else 24, where the two
+  //   17, 20 / 17; 14336 x 4096, M = 16 with INIT 24.7 / 19.8), else 24, where the two
   //   tiles of 16 src1 rows past 16 are worth it (M = 16, 24: 4096 x 4096 8 / 12, 10 / 12;
   //   3200 x 8192 12 / 12, 15 / 13; 7000 x 3200 10.8 / 12.2, 15.2 / 12.2; 8192 x 1024 11.3 /
   //   11.7, 15.6 / 11.8).
@@ -77,13 +77,13 @@ int make_f8_plan(int64_t M, int64_t N, int64_t K, bool given, F8Plan* p) {
                               : large              ? 8
                                                    : (groups <= kCUs && nkb < 64 ? 24 : 16);
   const bool wide = M > skinny_rows;
-  // Output tile by M (us per call, 64 x 128, 128 x 128 and 128 x 256 tiles: 14336 x
-  // 4096, M = 128 31.4 / 36.2 / 40.4, M = 256 57.0 / 47.9 / 54.4, M = 512 106.0 /
-  // 90.8 / 77.9; 4096 x 14336, M = 128 32.9 / 36.4 / 41.1, M = 600 158.7 / 125.2 /
-  // 98.1).  Below 32 MiB a small tile also where that gives each CU at most one
-  // (4096 x 4096, M = 256 25.1 / 29.7 / 33.7, M = 512 33.6 / 37.2 / 41.7, M = 1024
-  // 61.3 / 51.9 / 58.2, M = 2048 115.6 / 97.3 / 85.0), and 64 x 64 up to M = 128
-  // (M = 64 / 128 14.4 / 18.2 against 17.4 / 19.6).
+  // Output tile by M (us per call with INIT, 64 x 128, 128 x 128 and 128 x 256 tiles:
+  // 14336 x 4096, M = 128 29.0 / 32.9 / 37.1, M = 256 53.8 / 44.3 / 51.4, M = 512 102.5 /
+  // 84.8 / 72.1; 4096 x 14336, M = 128 30.6 / 33.1 / 38.2, M = 256 52.1 / 49.0 / 51.5,
+  // M = 600 157.3 / 120.7 / 94.5).  Below 32 MiB a small tile also where that gives
+  // each CU at most one (4096 x 4096, M = 256 23.0 / 27.8 / 31.5, M = 512 31.4 / 35.3 /
+  // 39.7, M = 1024 57.6 / 49.8 / 56.0, M = 2048 113.2 / 97.9 / 81.7), and 64 x 64 up to
+  // M = 128 (M = 64 / 128 14.9 / 17.4 against 17.1 / 18.9).
   const auto fits = [&](int bm, int bn) { return ceil_div(M, bm) * ceil_div(N, bn) <= kCUs; };
   const bool low = M <= 128 || (!large && fits(64, 128));
   const bool mid = M <= 256 || (!large && fits(128, 128));

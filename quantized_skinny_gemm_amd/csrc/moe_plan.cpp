@@ -41,10 +41,12 @@ int make_moe_plan(int type, int64_t T, int64_t D, int64_t F, int64_t E, int64_t 
   // weights as few as half a byte) and the sequence of (expert, unit) pairs
   // is cut in slices to fill the device.
   const int64_t used = T * top_k < E ? T * top_k : E;
-  // Gate / up: groups of 32 rows, several per workgroup where that leaves two
-  // workgroups per CU if every expert that can be in use is (whole layer, us,
-  // about 3 / 2 / 1 workgroups per CU, 8 experts of 4096 x 14336, Q4_0R: 32 tokens
-  // 244 / 232 / 226; 4 tokens, on 5 of the experts, 109 / 101 / 142).
+  // Gate / up: groups of 32 rows, several per workgroup where that leaves a grid of
+  // two workgroups per CU if every expert that can be in use is.  Registers or LDS
+  // let one run on a CU at a time; the second is there for calls that use fewer
+  // experts than they could (whole layer, us, grids of about 3 / 2 / 1 per CU, 8
+  // experts of 4096 x 14336, Q4_0R: 32 tokens 246 / 232 / 229, 16 tokens 221 / 203 /
+  // 199; 4 tokens on 7 of the experts 179 / 166 / 163, on 3 or 4 of them 98 / 94 / 134).
   const int64_t groups = F / kQK, per = groups * used / (2 * kCUs);
   p->up_groups = (int)(per > 1 ? (groups + per - 1) / per : groups);
   const bool many = T * top_k > 2 * used;
