@@ -65,8 +65,10 @@ typedef enum mm_type {
     MM_TYPE_Q4_0 = 2,
     MM_TYPE_Q8_0 = 3,
     MM_TYPE_Q4_0R = 4,     /* Q4_0 weights in the repacked layout (mm_repack_q4_0) */
-    MM_TYPE_F8 = 5         /* OCP e4m3 codes with one f32 scale per block of 128
+    MM_TYPE_F8 = 5,        /* OCP e4m3 codes with one f32 scale per block of 128
                               (mm_quantize_f8); products: mm_mul_mat_f8_*, mm_moe_f32 */
+    MM_TYPE_MXFP4 = 6      /* OCP MX: e2m1 codes with one power of two per block of 32
+                              (mm_quantize_mxfp4); products: mm_mul_mat_mxfp4_*, mm_moe_* */
 } mm_type;
 
 /*
@@ -319,6 +321,116 @@ mm_status mm_mul_mat_f8_f8(const void* src0, const float* scale0, const void* sr
 size_t mm_mul_mat_f8_workspace_size(int64_t M, int64_t N, int64_t K, int src1_quantized);
 
 /*
+ * The MXFP4 type: OCP microscaling format, 4-bit e2m1 codes (sign, 2 exponent bits
+ * with bias 1, 1 fraction bit: 0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives) with
+ * one scale 2^(byte - 127) per 32 values along K (byte 255: NaN), for weights and
+ * activations alike.  Codes and scales are two arrays:
+ *   codes:  [rows][K/2] bytes, element 2 i of a row in the low half of its byte i,
+ *           16-byte aligned; K % 32 == 0, K <= 2^23;
+ *   scales: [rows][4 * ceil(K / 128)] bytes, 4-byte aligned: a row's K / 32 scale
+ *           bytes, padded to whole 4 bytes (where K % 128 == 0 there is no padding).
+ *           The quantizer writes 127 into the padding, the products ignore it.
+ *
+ * mm_quantize_mxfp4 -- x[nrows][k] (f32, 16-byte aligned) -> codes and scales:
+ *     byte = max(floor(log2(amax)) - 2 + 127, 0), amax over the block;
+ *     code = e2m1(x / 2^(byte - 127)), round to nearest, ties to the even code,
+ *     magnitudes over 6 (at most 8) become 6; a code's sign is its value's.
+ *   A block of zeros has byte 0.  A block that holds an infinity or NaN gets byte 255
+ *   and codes 0: its values, and the products that it enters, are NaN.
+ * mm_dequantize_mxfp4 -- codes and scales -> the values they stand for, y[nrows][k]
+ *   (f32, 16-byte aligned), each exact.
+ *   No overlap between the three arrays.
+ */
+mm_status mm_quantize_mxfp4(const float* x, void* codes, void* scales, int64_t nrows, int64_t k,
+                            void* stream);
+mm_status mm_dequantize_mxfp4(const void* codes, const void* scales, float* y, int64_t nrows, int64_t k,
+                              void* stream);
+
+/*
+ * mm_mul_mat_mxfp4_f32 -- dst[M][N] (f32) = MXFP4(src1)[M][K] . MXFP4 src0[N][K]^T.
+ *   src0, scale0: weight codes [N][K/2] and scales [N][4 ceil(K/128)].
+ *   src1: f32 [M][K], 16-byte aligned; quantized within the call as
+ *         mm_quantize_mxfp4 does (same codes and scales).
+ *   dst: f32 [M][N], 4-byte aligned.
+ *   ws:  mm_mul_mat_mxfp4_workspace_size(M, N, K, 0) bytes, 256-byte aligned (the
+ *        quantized src1 and any split-K partial sums).
+ * mm_mul_mat_mxfp4_mxfp4 -- the same product of a src1 that is quantized already
+ *   (mm_quantize_mxfp4, or mm_rms_norm_f32 with that output): src1 codes [M][K/2],
+ *   scale1 [M][4 ceil(K/128)].  ws: mm_mul_mat_mxfp4_workspace_size(M, N, K, 1) bytes.
+ * dst[m][n] = sum_b 2^(e1[m][b] + e0[n][b]) * S_b[m][n], S_b the (exact) sum of the
+ * block's 32 code products, accumulated in fp32.  A scale byte of 255 makes the
+ * outputs that its row enters NaN and no other.
+ * mm_mul_mat_workspace_size(MM_TYPE_MXFP4, ...) is the size for f32 src1 (a few rows
+ * of f32 may need none where src1 as codes needs some), mm_row_bytes(MM_TYPE_MXFP4, K)
+ * the bytes of a row of codes; mm_dispatch and mm_debug_mul_mat do not take this type.
+ * M, N < 2^31 - 255; a product whose output needs 2^32 threads in one launch is
+ * MM_ERR_SHAPE too.
+ */
+mm_status mm_mul_mat_mxfp4_f32(const void* src0, const void* scale0, const float* src1, float* dst,
+                               int64_t M, int64_t N, int64_t K, void* ws, size_t ws_bytes,
+                               void* stream);
+mm_status mm_mul_mat_mxfp4_mxfp4(const void* src0, const void* scale0, const void* src1,
+                                 const void* scale1, float* dst, int64_t M, int64_t N, int64_t K,
+                                 void* ws, size_t ws_bytes, void* stream);
+size_t mm_mul_mat_mxfp4_workspace_size(int64_t M, int64_t N, int64_t K, int src1_quantized);
+
+/*
+ * mm_rms_norm_f32 -- root-mean-square norm with the residual's addition, y as the
+ * products take it:
+ *     v = x + residual                 (residual NULL: v = x)
+ *     rstd = 1 / sqrt(mean over D of v^2 + eps)     (fp64, rounded once to fp32)
+ *     y = (v * rstd) * weight          (weight NULL: y = v * rstd), fp32
+ *   x, residual: f32 [T][D]; weight: f32 [D]; eps >= 0 (else MM_ERR_ARG).
+ *   sum: v, f32 [T][D], may be NULL; may be x or residual itself (in place).
+ *   y by out_type: MM_TYPE_F32 f32 [T][D] (scales unused); MM_TYPE_F8 codes [T][D] and
+ *     scales f32 [T][ceil(D/128)], as mm_quantize_f8 with block_rows 1 makes them of y
+ *     (src1 of mm_mul_mat_f8_f8); MM_TYPE_MXFP4 codes [T][D/2] and scales
+ *     [T][4 ceil(D/128)], as mm_quantize_mxfp4 does (src1 of mm_mul_mat_mxfp4_mxfp4).
+ *     Another type is MM_ERR_ARG.
+ *   D <= 2^23, a multiple of 32 for the 8- and 4-bit outputs.  f32 arrays and scales
+ *   4-byte aligned, codes 16-byte.  No other overlap than sum's.
+ * A row with an infinity or NaN yields NaN in that row only (an infinity: zeros in the
+ * row's finite places), a row of zeros with eps = 0 too.
+ */
+mm_status mm_rms_norm_f32(const float* x, const float* residual, const float* weight, float eps,
+                          float* sum, int out_type, void* y, void* scales, int64_t T, int64_t D,
+                          void* stream);
+
+/*
+ * mm_route_f32 -- routing of T tokens to experts by their logits [T][E] (f32):
+ *   s[e] = softmax over e of the logits, or sigmoid(logit)
+ *   c[e] = s[e] + bias[e]                         (bias NULL: c = s)
+ *   groups > 1: the E experts are groups of E / groups neighbours, each worth the sum
+ *     of its group_top (1 or 2) largest c; only the group_k groups worth most are
+ *     chosen from (ties: the lower group).
+ *   ids[t][j], j < top_k: the experts of the largest c, in descending order, ties to
+ *     the lower index.
+ *   weights[t][j] = s[ids[t][j]], norm: divided by their sum over j (0 where that is
+ *     0), times scale.
+ * Scores and sums are fp64, weights rounded once to fp32.
+ * An expert whose logit or bias is minus infinity is masked: it is never chosen.
+ * Where fewer than top_k experts are left to choose from, the last slots get id -1
+ * and weight 0 (mm_moe_routed_f32 skips them).  A NaN among a token's logits, or
+ * under a softmax plus infinity, makes all of that token's weights NaN; its ids are
+ * experts (or -1) all the same.
+ *   router: host struct (the library keeps no reference).  1 <= E <= 512, 1 <= top_k
+ *   <= 64, E; groups <= 64 divides E; 1 <= group_k <= groups.  T <= 2^25.
+ *   All arrays 4-byte aligned; ids and weights must not overlap anything.
+ */
+#define MM_SCORE_SOFTMAX 0
+#define MM_SCORE_SIGMOID 1
+typedef struct mm_router {
+    int score, top_k, norm;
+    int groups, group_k, group_top;   /* 1, 1, 1: no groups */
+    int64_t E;
+    float scale;
+    const float* bias;                /* device [E], may be NULL */
+} mm_router;
+
+mm_status mm_route_f32(const mm_router* router, const float* logits, int32_t* ids, float* weights,
+                       int64_t T, void* stream);
+
+/*
  * mm_moe_f32 -- a mixture-of-experts layer for a few tokens (decode), whole:
  *   l[t][e] = sum_d x[t][d] router[e][d]       (summed in fp64)
  *   p[t] = softmax over e of l[t]
@@ -339,8 +451,9 @@ size_t mm_mul_mat_f8_workspace_size(int64_t M, int64_t N, int64_t K, int src1_qu
  *                    (mm_repacked_q4_0_bytes(rows, K) bytes), experts in a row
  *     MM_TYPE_F8     codes [E][rows][K], scales [E][ceil(rows/128)][ceil(K/128)]
  *     MM_TYPE_F16    binary16 [E][rows][K]
+ *     MM_TYPE_MXFP4  codes [E][rows][K/2], scales [E][rows][4 ceil(K/128)] bytes
  *   gate, up: rows = F, K = D; down: rows = D, K = F; 16-byte aligned
- *   gate_scale, up_scale, down_scale: F8 only (4-byte aligned), else unused
+ *   gate_scale, up_scale, down_scale: F8 and MXFP4 only (4-byte aligned), else unused
  *   router: f32 [E][D], 16-byte aligned
  *   D, F: multiples of 32, at most 2^18; 1 <= E <= 512; 1 <= top_k <= 16, E
  * x: f32 [T][D], 16-byte aligned; dst: f32 [T][D]; 0 <= T <= 128 (larger
@@ -358,15 +471,31 @@ typedef struct mm_moe_layer {
     int64_t D, F, E;
     const float* router;
     const void *gate, *up, *down;
-    const float *gate_scale, *up_scale, *down_scale;
+    const void *gate_scale, *up_scale, *down_scale;
 } mm_moe_layer;
 
 mm_status mm_moe_f32(const mm_moe_layer* layer, const float* x, float* dst, int32_t* ids,
                      float* weights, int64_t T, void* ws, size_t ws_bytes, void* stream);
 size_t mm_moe_workspace_size(const mm_moe_layer* layer, int64_t T);
 
-/* Bytes of workspace the product of `type` (F32, F16, Q4_0, Q8_0, Q4_0R or F8)
- * needs at this shape (F8: with f32 src1); 0 for an invalid shape or type.  Pure host function. */
+/*
+ * mm_moe_routed_f32 -- the layer's experts for a choice that is given (mm_route_f32's,
+ * or the caller's own): dst[t] = sum_j weights[t][j] * down_e h[t][j], e = ids[t][j].
+ *   ids (int32) and weights (f32) [T][top_k], device, 4-byte aligned: inputs, not
+ *   changed.  layer->router and layer->norm are not used (router may be NULL).
+ *   An id outside 0 .. E-1 is a slot without an expert: it adds nothing, whatever its
+ *   weight.  An expert that a token names several times counts with the sum of its
+ *   weights.  A token without experts gets zeros.  A NaN weight of an expert makes
+ *   that token NaN.  Otherwise as mm_moe_f32.
+ * ws: mm_moe_routed_workspace_size(layer, T) bytes, 256-byte aligned.
+ */
+mm_status mm_moe_routed_f32(const mm_moe_layer* layer, const float* x, const int32_t* ids,
+                            const float* weights, float* dst, int64_t T, void* ws, size_t ws_bytes,
+                            void* stream);
+size_t mm_moe_routed_workspace_size(const mm_moe_layer* layer, int64_t T);
+
+/* Bytes of workspace the product of `type` (F32, F16, Q4_0, Q8_0, Q4_0R, F8 or MXFP4)
+ * needs at this shape (F8, MXFP4: with f32 src1); 0 for an invalid shape or type.  Pure host function. */
 size_t mm_mul_mat_workspace_size(int type, int64_t M, int64_t N, int64_t K);
 
 /* Bytes of one row of K values of `type`; -1 if K is invalid for it. */

@@ -15,6 +15,7 @@ What it computes (plain NumPy, float64 unless a step is fixed to fp32):
 * ``mul_mat`` -- ``dst[M, N] = src1[M, K] . src0[N, K]^T`` for Q4_0, Q8_0, F16
   and F32 ``src0``, in float64.
 
+* ``mx4``, ``norm``, ``route`` -- MXFP4 (quantizer, products in float64), the RMS norm and the routing to experts.
 * ``f8``, ``moe`` -- e4m3 with one fp32 scale per block of 128 (quantizer as fp32
   operations, products in float64) and the mixture-of-experts layer in float64.
 
@@ -56,4 +57,4 @@ R10 Q8_0 weights (src0): the Q8_0 block of R1, quantized from f32 weights
     both fp16 scales.
 """
 
-from . import codec, f8, moe, mul_mat  # noqa: F401
+from . import codec, f8, moe, mul_mat, mx4, norm, route  # noqa: F401

@@ -15,6 +15,12 @@ there is no CPU fallback.
     dst = mul_mat_f8_f32(w_f8, w_scale, x)        # x quantized per row and 128 values within
     layer = MoeLayer(MM_TYPE_F16, router, gate, up, down, F, top_k)
     dst, ids, weights = moe_f32(layer, x)         # mixture-of-experts layer, a few tokens
+    w_mx, w_scale = quantize_mxfp4(w_f32)         # 4-bit codes, a power of two per 32 values
+    dst = mul_mat_mxfp4_f32(w_mx, w_scale, x)     # x quantized to MXFP4 within
+    (a, a_scale), h = rms_norm_f32(x, g, residual=h, out_type=MM_TYPE_MXFP4)
+    dst = mul_mat_mxfp4_mxfp4(w_mx, w_scale, a, a_scale)
+    ids, weights = route_f32(Router(E, top_k, score="sigmoid", bias=b, groups=8, group_k=4), logits)
+    dst = moe_routed_f32(layer, x, ids, weights)  # the layer's experts for that choice
 """
 from __future__ import annotations
 
@@ -32,13 +38,16 @@ __all__ = [
     "mul_mat_f32", "workspace_size", "debug_workspace_size", "row_bytes", "dispatch",
     "debug_mul_mat", "status_string", "q4_0_init", "q4_0_compute", "mul_mat_q4_0_f32_group",
     "group_workspace_size", "MM_TYPE_F8", "quantize_f8", "mul_mat_f8_f32", "mul_mat_f8_f8",
-    "f8_workspace_size", "MoeLayer", "moe_f32",
+    "f8_workspace_size", "MoeLayer", "moe_f32", "MM_TYPE_MXFP4", "quantize_mxfp4", "dequantize_mxfp4",
+    "mul_mat_mxfp4_f32", "mul_mat_mxfp4_mxfp4", "mxfp4_workspace_size", "rms_norm_f32", "Router",
+    "route_f32", "moe_routed_f32",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libqsgemm.so")
 
 MM_TYPE_F32, MM_TYPE_F16, MM_TYPE_Q4_0, MM_TYPE_Q8_0, MM_TYPE_Q4_0R = 0, 1, 2, 3, 4
 MM_TYPE_F8 = 5
+MM_TYPE_MXFP4 = 6
 
 if not os.path.exists(LIB_PATH):
     raise ImportError(
@@ -66,6 +75,15 @@ for _name, _args, _res in [
     ("mm_mul_mat_f8_workspace_size", [_i64, _i64, _i64, _int], _sz),
     ("mm_moe_f32", [_vp, _vp, _vp, _vp, _vp, _i64, _vp, _sz, _vp], _int),
     ("mm_moe_workspace_size", [_vp, _i64], _sz),
+    ("mm_quantize_mxfp4", [_vp, _vp, _vp, _i64, _i64, _vp], _int),
+    ("mm_dequantize_mxfp4", [_vp, _vp, _vp, _i64, _i64, _vp], _int),
+    ("mm_mul_mat_mxfp4_f32", [_vp, _vp, _vp, _vp, _i64, _i64, _i64, _vp, _sz, _vp], _int),
+    ("mm_mul_mat_mxfp4_mxfp4", [_vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _vp, _sz, _vp], _int),
+    ("mm_mul_mat_mxfp4_workspace_size", [_i64, _i64, _i64, _int], _sz),
+    ("mm_rms_norm_f32", [_vp, _vp, _vp, ctypes.c_float, _vp, _int, _vp, _vp, _i64, _i64, _vp], _int),
+    ("mm_route_f32", [_vp, _vp, _vp, _vp, _i64, _vp], _int),
+    ("mm_moe_routed_f32", [_vp, _vp, _vp, _vp, _vp, _i64, _vp, _sz, _vp], _int),
+    ("mm_moe_routed_workspace_size", [_vp, _i64], _sz),
     ("mm_q4_0_init", [_vp, _vp, _i64, _i64, _i64, _sz, _vp], _int),
     ("mm_q4_0_compute", [_vp, _vp, _i64, _i64, _i64, _vp, _sz, _vp], _int),
     ("mm_mul_mat_q4_0_f32_group", [_int, ctypes.POINTER(_vp), ctypes.POINTER(_vp),
@@ -402,6 +420,179 @@ def mul_mat_f8_f8(w: torch.Tensor, w_scale: torch.Tensor, a: torch.Tensor, a_sca
     return out
 
 
+# MXFP4 codes are pairs in bytes, its scales exponent bytes: uint8, or torch's types for them
+_MX_CODES = (torch.uint8,) + ((torch.float4_e2m1fn_x2,) if hasattr(torch, "float4_e2m1fn_x2") else ())
+_MX_SCALES = (torch.uint8,) + ((torch.float8_e8m0fnu,) if hasattr(torch, "float8_e8m0fnu") else ())
+
+
+def quantize_mxfp4(x: torch.Tensor, out=None):
+    """float32 [rows, K] -> (codes uint8 [rows, K/2], scales uint8 [rows, 4 ceil(K/128)])."""
+    x = _dev(x, "x", torch.float32)
+    rows, k = x.shape
+    dev = x.get_device()
+    if out is None:
+        codes = torch.empty((rows, k // 2), dtype=torch.uint8, device=x.device)
+        scales = torch.empty((rows, 4 * _ceil128(k)), dtype=torch.uint8, device=x.device)
+    else:
+        codes, scales = out
+        _on(codes, "out codes", (rows, k // 2), _MX_CODES, dev)
+        _on(scales, "out scales", (rows, 4 * _ceil128(k)), _MX_SCALES, dev)
+    _launch(lib.mm_quantize_mxfp4, "mm_quantize_mxfp4", dev, x.data_ptr(), codes.data_ptr(), scales.data_ptr(),
+            rows, k)
+    return codes, scales
+
+
+def _mx_pair(codes, scales, name: str, dev: int):
+    """(rows, K) of MXFP4 codes [rows, K/2] with their scales, both on device dev."""
+    if not isinstance(codes, torch.Tensor) or codes.dim() != 2:
+        raise TypeError(f"{name} must be a 2-d GPU (HIP) tensor")
+    rows, half = codes.shape
+    _on(codes, name, (rows, half), _MX_CODES, dev)
+    _on(scales, f"{name}_scale", (rows, 4 * _ceil128(2 * half)), _MX_SCALES, dev)
+    return rows, 2 * half
+
+
+def dequantize_mxfp4(codes: torch.Tensor, scales: torch.Tensor, out: torch.Tensor | None = None) -> torch.Tensor:
+    """MXFP4 codes [rows, K/2] and scales [rows, 4 ceil(K/128)] -> float32 [rows, K], exact."""
+    _dev(codes, "codes")
+    dev = codes.get_device()
+    rows, k = _mx_pair(codes, scales, "codes", dev)
+    if out is None:
+        out = torch.empty((rows, k), dtype=torch.float32, device=codes.device)
+    else:
+        _on(out, "out", (rows, k), _F32, dev)
+    _launch(lib.mm_dequantize_mxfp4, "mm_dequantize_mxfp4", dev, codes.data_ptr(), scales.data_ptr(), out.data_ptr(),
+            rows, k)
+    return out
+
+
+@functools.lru_cache(maxsize=4096)
+def mxfp4_workspace_size(m: int, n: int, k: int, src1_quantized: bool = False) -> int:
+    return int(lib.mm_mul_mat_mxfp4_workspace_size(int(m), int(n), int(k), int(src1_quantized)))
+
+
+def mul_mat_mxfp4_f32(w: torch.Tensor, w_scale: torch.Tensor, x: torch.Tensor, out=None, ws=None) -> torch.Tensor:
+    """dst[M, N] = MXFP4(x)[M, K] . MXFP4(w)[N, K]^T; w codes [N, K/2] with scales [N, 4 ceil(K/128)]
+    (quantize_mxfp4), x float32 [M, K], quantized within."""
+    x = _dev(x, "x", torch.float32)
+    m, k = x.shape
+    dev = x.get_device()
+    n, wk = _mx_pair(w, w_scale, "w", dev)
+    if wk != k:
+        raise ValueError(f"w has rows of {wk} values, x of {k}")
+    out, ws, nbytes = _buffers(m, n, x.device, dev, out, mxfp4_workspace_size(m, n, k, False), ws)
+    _launch(lib.mm_mul_mat_mxfp4_f32, "mm_mul_mat_mxfp4_f32", dev, w.data_ptr(), w_scale.data_ptr(), x.data_ptr(),
+            out.data_ptr(), m, n, k, None if ws is None else ws.data_ptr(), nbytes)
+    return out
+
+
+def mul_mat_mxfp4_mxfp4(w: torch.Tensor, w_scale: torch.Tensor, a: torch.Tensor, a_scale: torch.Tensor,
+                        out=None, ws=None) -> torch.Tensor:
+    """mul_mat_mxfp4_f32 with src1 quantized already: a codes [M, K/2], a_scale [M, 4 ceil(K/128)]."""
+    a = _dev(a, "a")
+    dev = a.get_device()
+    m, k = _mx_pair(a, a_scale, "a", dev)
+    n, wk = _mx_pair(w, w_scale, "w", dev)
+    if wk != k:
+        raise ValueError(f"w has rows of {wk} values, a of {k}")
+    out, ws, nbytes = _buffers(m, n, a.device, dev, out, mxfp4_workspace_size(m, n, k, True), ws)
+    _launch(lib.mm_mul_mat_mxfp4_mxfp4, "mm_mul_mat_mxfp4_mxfp4", dev, w.data_ptr(), w_scale.data_ptr(), a.data_ptr(),
+            a_scale.data_ptr(), out.data_ptr(), m, n, k, None if ws is None else ws.data_ptr(), nbytes)
+    return out
+
+
+def rms_norm_f32(x: torch.Tensor, weight=None, eps: float = 1e-5, residual=None, out_type: int = MM_TYPE_F32,
+                 out=None, sum_out=None):
+    """(y, v) with v = x + residual and y = v / sqrt(mean(v^2) + eps) * weight, float32 [T, D].
+
+    y is float32, or (codes, scales) as quantize_f8(y) (out_type MM_TYPE_F8) or quantize_mxfp4(y)
+    (MM_TYPE_MXFP4) gives them.  v is sum_out where given (x or residual itself: in place), else a new
+    tensor; None without a residual and sum_out (v is x then)."""
+    x = _dev(x, "x", torch.float32)
+    t, d = x.shape
+    dev = x.get_device()
+    for name, v, shape in (("weight", weight, (d,)), ("residual", residual, (t, d)), ("sum_out", sum_out, (t, d))):
+        if v is not None:
+            _on(v, name, shape, _F32, dev)
+    if sum_out is None and residual is not None:
+        sum_out = torch.empty((t, d), dtype=torch.float32, device=x.device)
+    scales = None
+    if out_type == MM_TYPE_F32:
+        if out is None:
+            out = torch.empty((t, d), dtype=torch.float32, device=x.device)
+        else:
+            _on(out, "out", (t, d), _F32, dev)
+        y, got = out, out
+    else:
+        f8 = out_type == MM_TYPE_F8
+        if not f8 and out_type != MM_TYPE_MXFP4:
+            raise ValueError("out_type must be MM_TYPE_F32, MM_TYPE_F8 or MM_TYPE_MXFP4")
+        shape, sshape = ((t, d), (t, _ceil128(d))) if f8 else ((t, d // 2), (t, 4 * _ceil128(d)))
+        if out is None:
+            y = torch.empty(shape, dtype=torch.float8_e4m3fn if f8 else torch.uint8, device=x.device)
+            scales = torch.empty(sshape, dtype=torch.float32 if f8 else torch.uint8, device=x.device)
+        else:
+            y, scales = out
+            _on(y, "out codes", shape, _F8_DTYPES if f8 else _MX_CODES, dev)
+            _on(scales, "out scales", sshape, _F32 if f8 else _MX_SCALES, dev)
+        got = (y, scales)
+    _launch(lib.mm_rms_norm_f32, "mm_rms_norm_f32", dev, x.data_ptr(), _ptr(residual), _ptr(weight), eps, _ptr(sum_out),
+            out_type, y.data_ptr(), _ptr(scales), t, d)
+    return got, sum_out
+
+
+class _RouterStruct(ctypes.Structure):
+    _fields_ = [("score", _int), ("top_k", _int), ("norm", _int), ("groups", _int), ("group_k", _int),
+                ("group_top", _int), ("E", _i64), ("scale", ctypes.c_float), ("bias", _vp)]
+
+
+_SCORES = {"softmax": 0, "sigmoid": 1}
+
+
+class Router:
+    """How tokens choose among e experts, for route_f32 (holds the bias tensor and the C struct).
+
+    score: "softmax" or "sigmoid" of the logits; bias float32 [e] is added to the scores for the choice
+    only.  groups > 1: experts in groups of e / groups neighbours, chosen from the group_k groups whose
+    group_top (1 or 2) best sum highest.  norm: the chosen scores are divided by their sum; scale: then
+    multiplied."""
+
+    def __init__(self, e, top_k, score="softmax", bias=None, groups=1, group_k=1, group_top=1, norm=True, scale=1.0):
+        if score not in _SCORES:
+            raise ValueError("score must be 'softmax' or 'sigmoid'")
+        self.e, self.top_k, self.bias = int(e), int(top_k), bias
+        if bias is not None:
+            _on(bias, "bias", (self.e,), _F32, bias.get_device() if isinstance(bias, torch.Tensor) else 0)
+        self.struct = _RouterStruct(_SCORES[score], self.top_k, int(bool(norm)), int(groups), int(group_k),
+                                    int(group_top), self.e, float(scale), None)
+        self._ref = ctypes.byref(self.struct)
+
+    def _take(self, dev: int):
+        if self.bias is not None:                      # where the tensor is now
+            _on(self.bias, "bias", (self.e,), _F32, dev)
+            self.struct.bias = self.bias.data_ptr()
+        return self._ref
+
+
+def route_f32(router: Router, logits: torch.Tensor, ids=None, weights=None):
+    """(ids int32 [T, top_k], weights [T, top_k]) of logits float32 [T, e]; a slot without an expert
+    (fewer than top_k to choose from) has id -1 and weight 0."""
+    logits = _dev(logits, "logits", torch.float32)
+    t, dev, k = logits.shape[0], logits.get_device(), router.top_k
+    _on(logits, "logits", (t, router.e), _F32, dev)
+    if ids is None:
+        ids = torch.empty((t, k), dtype=torch.int32, device=logits.device)
+    else:
+        _on(ids, "ids", (t, k), _I32, dev)
+    if weights is None:
+        weights = torch.empty((t, k), dtype=torch.float32, device=logits.device)
+    else:
+        _on(weights, "weights", (t, k), _F32, dev)
+    _launch(lib.mm_route_f32, "mm_route_f32", dev, router._take(dev), logits.data_ptr(), ids.data_ptr(),
+            weights.data_ptr(), t)
+    return ids, weights
+
+
 class _MoeStruct(ctypes.Structure):
     _fields_ = [("type", _int), ("top_k", _int), ("norm", _int), ("D", _i64), ("F", _i64), ("E", _i64),
                 ("router", _vp), ("gate", _vp), ("up", _vp), ("down", _vp),
@@ -409,7 +600,8 @@ class _MoeStruct(ctypes.Structure):
 
 
 _MOE_POINTERS = ("router", "gate", "up", "down", "gate_scale", "up_scale", "down_scale")
-_MOE_DTYPES = {MM_TYPE_Q4_0R: (torch.uint8,), MM_TYPE_F8: _F8_DTYPES, MM_TYPE_F16: (torch.float16,)}
+_MOE_DTYPES = {MM_TYPE_Q4_0R: (torch.uint8,), MM_TYPE_F8: _F8_DTYPES, MM_TYPE_F16: (torch.float16,),
+               MM_TYPE_MXFP4: _MX_CODES}
 
 
 class MoeLayer:
@@ -419,21 +611,41 @@ class MoeLayer:
     router float32 [E, D]; gate, up (F x D per expert) and down (D x F) by mm_type:
     MM_TYPE_Q4_0R uint8 [E, repacked_bytes(rows, K)] (repack_q4_0 of each expert), MM_TYPE_F8
     e4m3 [E, rows, K] with float32 scales [E, ceil(rows/128), ceil(K/128)], MM_TYPE_F16 float16
-    [E, rows, K].  norm: the top_k probabilities are divided by their sum."""
+    [E, rows, K], MM_TYPE_MXFP4 codes [E, rows, K/2] with scales [E, rows, 4 ceil(K/128)].  norm: the
+    top_k probabilities are divided by their sum.
+
+    router None: a layer for moe_routed_f32 only (router and norm play no part there); D then comes from
+    gate, or for MM_TYPE_Q4_0R from d."""
 
     def __init__(self, mm_type, router, gate, up, down, f, top_k, gate_scale=None, up_scale=None,
-                 down_scale=None, norm=True):
-        _dev(router, "router", torch.float32)
-        e, d = router.shape
-        f, top_k = int(f), int(top_k)
+                 down_scale=None, norm=True, d=None):
         if mm_type not in _MOE_DTYPES:
-            raise ValueError("mm_type must be MM_TYPE_Q4_0R, MM_TYPE_F8 or MM_TYPE_F16")
-        scales = (gate_scale, up_scale, down_scale) if mm_type == MM_TYPE_F8 else (None,) * 3
-        self.dev, self.device, self.d, self.f, self.e, self.top_k = router.get_device(), router.device, d, f, e, top_k
+            raise ValueError("mm_type must be MM_TYPE_Q4_0R, MM_TYPE_F8, MM_TYPE_F16 or MM_TYPE_MXFP4")
+        f, top_k = int(f), int(top_k)
+        if router is not None:
+            _dev(router, "router", torch.float32)
+            e, width = router.shape
+            at = router
+        else:
+            at = _dev(gate, "gate")
+            if gate.dim() != (2 if mm_type == MM_TYPE_Q4_0R else 3):
+                raise ValueError("gate must have its experts in the first of three dimensions (Q4_0R: of two)")
+            e = gate.shape[0]
+            if mm_type == MM_TYPE_Q4_0R:
+                if d is None:
+                    raise ValueError("d is needed for repacked experts without a router")
+                width = int(d)
+            else:
+                width = gate.shape[2] * (2 if mm_type == MM_TYPE_MXFP4 else 1)
+        if d is not None and int(d) != width:
+            raise ValueError(f"d is {d}, the layer's tensors have {width}")
+        d = width
+        scales = (gate_scale, up_scale, down_scale) if mm_type in (MM_TYPE_F8, MM_TYPE_MXFP4) else (None,) * 3
+        self.dev, self.device, self.d, self.f, self.e, self.top_k = at.get_device(), at.device, d, f, e, top_k
         self.tensors = (router, gate, up, down, *scales)
         self.struct = _MoeStruct(mm_type, top_k, int(bool(norm)), d, f, e)
         self._ref = ctypes.byref(self.struct)
-        self._sizes = {}
+        self._sizes, self._routed_sizes = {}, {}
         self._live = [(t.data_ptr, t.stride) for t in self.tensors if isinstance(t, torch.Tensor)]
         self._seen = None
         self._take()
@@ -445,12 +657,15 @@ class MoeLayer:
         if seen != self._seen:
             kind, d, f, e, dev = self.struct.type, self.d, self.f, self.e, self.dev
             router, *rest = self.tensors
-            _on(router, "router", (e, d), _F32, dev)
+            if router is not None:
+                _on(router, "router", (e, d), _F32, dev)
             for name, w, scale, rows, k in zip(("gate", "up", "down"), rest[:3], rest[3:], (f, f, d), (d, d, f)):
-                _on(w, name, (e, repacked_bytes(rows, k)) if kind == MM_TYPE_Q4_0R else (e, rows, k),
-                    _MOE_DTYPES[kind], dev)
+                _on(w, name, (e, repacked_bytes(rows, k)) if kind == MM_TYPE_Q4_0R else
+                    (e, rows, k // 2 if kind == MM_TYPE_MXFP4 else k), _MOE_DTYPES[kind], dev)
                 if kind == MM_TYPE_F8:
                     _on(scale, f"{name}_scale", (e, _ceil128(rows), _ceil128(k)), _F32, dev)
+                elif kind == MM_TYPE_MXFP4:
+                    _on(scale, f"{name}_scale", (e, rows, 4 * _ceil128(k)), _MX_SCALES, dev)
             for field, t in zip(_MOE_POINTERS, self.tensors):
                 setattr(self.struct, field, _ptr(t))
             self._seen = seen
@@ -462,6 +677,12 @@ class MoeLayer:
             self._sizes[t] = int(lib.mm_moe_workspace_size(self._ref, int(t)))
         return self._sizes[t]
 
+    def routed_workspace_size(self, t: int) -> int:
+        """workspace_size for moe_routed_f32."""
+        if t not in self._routed_sizes:
+            self._routed_sizes[t] = int(lib.mm_moe_routed_workspace_size(self._ref, int(t)))
+        return self._routed_sizes[t]
+
 
 _I32 = (torch.int32,)
 
@@ -469,6 +690,8 @@ _I32 = (torch.int32,)
 def moe_f32(layer: MoeLayer, x: torch.Tensor, out=None, ids=None, weights=None, ws=None):
     """(dst [T, D], ids int32 [T, top_k], weights [T, top_k]) of the layer on x float32 [T, D]."""
     x = _dev(x, "x", torch.float32)
+    if layer.tensors[0] is None:
+        raise ValueError("the layer has no router: moe_routed_f32 takes it")
     t = x.shape[0]
     dev, k = layer.dev, layer.top_k
     _on(x, "x", (t, layer.d), _F32, dev)
@@ -484,6 +707,21 @@ def moe_f32(layer: MoeLayer, x: torch.Tensor, out=None, ids=None, weights=None, 
     _launch(lib.mm_moe_f32, "mm_moe_f32", dev, layer._take(), x.data_ptr(), out.data_ptr(), ids.data_ptr(),
             weights.data_ptr(), t, None if ws is None else ws.data_ptr(), nbytes)
     return out, ids, weights
+
+
+def moe_routed_f32(layer: MoeLayer, x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, out=None, ws=None):
+    """dst [T, D] of the layer's experts on x float32 [T, D] for a choice that is given: ids int32 and weights
+    float32 [T, top_k] (route_f32); an id outside 0 .. E-1 is a slot without an expert."""
+    x = _dev(x, "x", torch.float32)
+    t = x.shape[0]
+    dev, k = layer.dev, layer.top_k
+    _on(x, "x", (t, layer.d), _F32, dev)
+    _on(ids, "ids", (t, k), _I32, dev)
+    _on(weights, "weights", (t, k), _F32, dev)
+    out, ws, nbytes = _buffers(t, layer.d, layer.device, dev, out, layer.routed_workspace_size(t), ws)
+    _launch(lib.mm_moe_routed_f32, "mm_moe_routed_f32", dev, layer._take(), x.data_ptr(), ids.data_ptr(),
+            weights.data_ptr(), out.data_ptr(), t, None if ws is None else ws.data_ptr(), nbytes)
+    return out
 
 
 def q4_0_init(x: torch.Tensor, n: int, ws: torch.Tensor | None = None) -> torch.Tensor:

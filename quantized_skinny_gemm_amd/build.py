@@ -26,8 +26,9 @@ BENCH_SRC = os.path.join(ROOT, "bench_read.hip")
 BENCH_LIB = os.path.join(ROOT, "bench_read.so")
 
 HIP_SOURCES = ["api.hip", "quantize.hip", "q4_narrow.hip", "q4_mma.hip", "q4_skinny.hip",
-               "q4_wide_i8.hip", "f_kernels.hip", "repack.hip", "f8.hip", "moe.hip"]
-CXX_SOURCES = ["plan.cpp", "f8_plan.cpp", "moe_plan.cpp", "dispatch_table.cpp"]
+               "q4_wide_i8.hip", "f_kernels.hip", "repack.hip", "f8.hip", "moe.hip", "mx4.hip",
+               "norm.hip", "route.hip"]
+CXX_SOURCES = ["plan.cpp", "f8_plan.cpp", "moe_plan.cpp", "mx4_plan.cpp", "dispatch_table.cpp"]
 
 ARCH = "gfx950"
 HIPCC_FLAGS = [

@@ -224,6 +224,25 @@ int f8_product(const void* src0, const float* scale0, const float* x, const void
                                       dst, (int)M, (int)N, (int)K, ws, s));
 }
 
+// Product with MXFP4 weights: src1 as f32 (x) or as codes and scales (a, asc).
+int mx4_product(const void* src0, const void* scale0, const float* x, const void* a, const void* asc,
+                float* dst, int64_t M, int64_t N, int64_t K, void* ws, size_t ws_bytes, void* stream,
+                bool given) {
+  Mx4Plan p;
+  int st = make_mx4_plan(M, N, K, given, &p);
+  if (st != MM_OK) return st;
+  st = validate_mx4(src0, scale0, given ? a : (const void*)x, asc, dst, M, N, K, given, ws, ws_bytes, p);
+  if (st != MM_OK) return st;
+  if (p.kind == MX4_NONE) return MM_OK;
+  st = check_device();
+  if (st != MM_OK) return st;
+  hipStream_t s = (hipStream_t)stream;
+  if (p.kind == MX4_ZERO) return hip_status(launch_zero(dst, M * N, s));
+  return hip_status(launch_mx4_product(p, (const uint8_t*)src0, (const uint8_t*)scale0, x,
+                                       (const uint8_t*)a, (const uint8_t*)asc, dst, (int)M, (int)N,
+                                       (int)K, ws, s));
+}
+
 }  // namespace
 
 // Status codes travel as int inside the library; the C entry points return
@@ -327,6 +346,46 @@ size_t mm_mul_mat_f8_workspace_size(int64_t M, int64_t N, int64_t K, int src1_qu
   return p.ws_bytes;
 }
 
+mm_status mm_quantize_mxfp4(const float* x, void* codes, void* scales, int64_t nrows, int64_t k,
+                            void* stream) {
+  int st = validate_mx4_quantize(x, codes, scales, nrows, k);
+  if (st != MM_OK || nrows == 0 || k == 0) return as_status(st);
+  st = check_device();
+  if (st != MM_OK) return as_status(st);
+  return as_status(hip_status(launch_mx4_quantize(x, (uint8_t*)codes, (uint8_t*)scales, nrows, k,
+                                                  (hipStream_t)stream)));
+}
+
+mm_status mm_dequantize_mxfp4(const void* codes, const void* scales, float* y, int64_t nrows, int64_t k,
+                              void* stream) {
+  int st = validate_mx4_quantize(y, codes, scales, nrows, k);
+  if (st != MM_OK || nrows == 0 || k == 0) return as_status(st);
+  st = check_device();
+  if (st != MM_OK) return as_status(st);
+  return as_status(hip_status(launch_mx4_dequantize((const uint8_t*)codes, (const uint8_t*)scales, y,
+                                                    nrows, k, (hipStream_t)stream)));
+}
+
+mm_status mm_mul_mat_mxfp4_f32(const void* src0, const void* scale0, const float* src1, float* dst,
+                               int64_t M, int64_t N, int64_t K, void* ws, size_t ws_bytes,
+                               void* stream) {
+  return as_status(mx4_product(src0, scale0, src1, nullptr, nullptr, dst, M, N, K, ws, ws_bytes,
+                               stream, false));
+}
+
+mm_status mm_mul_mat_mxfp4_mxfp4(const void* src0, const void* scale0, const void* src1,
+                                 const void* scale1, float* dst, int64_t M, int64_t N, int64_t K,
+                                 void* ws, size_t ws_bytes, void* stream) {
+  return as_status(mx4_product(src0, scale0, nullptr, src1, scale1, dst, M, N, K, ws, ws_bytes,
+                               stream, true));
+}
+
+size_t mm_mul_mat_mxfp4_workspace_size(int64_t M, int64_t N, int64_t K, int src1_quantized) {
+  Mx4Plan p;
+  if (make_mx4_plan(M, N, K, src1_quantized != 0, &p) != MM_OK) return 0;
+  return p.ws_bytes;
+}
+
 mm_status mm_mul_mat_f32(const float* src0, const float* src1, float* dst,
                          int64_t M, int64_t N, int64_t K, void* ws, size_t ws_bytes,
                          void* stream) {
@@ -408,9 +467,77 @@ size_t moe_matrix_bytes(const mm_moe_layer& l, int64_t rows, int64_t K) {
                                                         : rows * row_bytes(l.type, K));
 }
 size_t moe_scale_bytes(const mm_moe_layer& l, int64_t rows, int64_t K) {
+  if (l.type == MM_TYPE_MXFP4)
+    return (size_t)l.E * (size_t)rows * 4 * (size_t)((K + kMx4Group - 1) / kMx4Group);
   if (l.type != MM_TYPE_F8) return 0;
   return (size_t)l.E * (size_t)((rows + kF8Block - 1) / kF8Block) *
          (size_t)((K + kF8Block - 1) / kF8Block) * 4;
+}
+
+}  // namespace
+
+namespace {
+
+// The layer, with its own router (ids and weights are outputs, may be NULL) or,
+// `routed`, for a choice that is given (ids and weights are inputs).
+int moe(const mm_moe_layer* layer, const float* x, float* dst, int32_t* ids, float* weights,
+        bool routed, int64_t T, void* ws, size_t ws_bytes, void* stream) {
+  if (!layer) return MM_ERR_NULL;
+  const mm_moe_layer& l = *layer;
+  MoePlan p;
+  int st = make_moe_plan(l.type, T, l.D, l.F, l.E, l.top_k, &p, routed);
+  if (st != MM_OK) return st;
+  if (T == 0) return MM_OK;
+  const bool scaled = l.type == MM_TYPE_F8 || l.type == MM_TYPE_MXFP4;
+  if (!x || !dst || !l.gate || !l.up || !l.down) return MM_ERR_NULL;
+  if (routed ? !ids || !weights : !l.router) return MM_ERR_NULL;
+  if (scaled && (!l.gate_scale || !l.up_scale || !l.down_scale)) return MM_ERR_NULL;
+  const void* const router = routed ? nullptr : l.router;
+  const auto off = [](const void* v, uintptr_t a) { return (uintptr_t)v % a != 0; };
+  if (off(x, 16) || off(router, 16) || off(l.gate, 16) || off(l.up, 16) || off(l.down, 16) ||
+      off(dst, 4) || off(ids, 4) || off(weights, 4))
+    return MM_ERR_ALIGN;
+  if (scaled && (off(l.gate_scale, 4) || off(l.up_scale, 4) || off(l.down_scale, 4))) return MM_ERR_ALIGN;
+  if (!ws || ws_bytes < p.ws_bytes) return MM_ERR_WORKSPACE;
+  if (off(ws, 256)) return MM_ERR_ALIGN;
+  const size_t xb = (size_t)(T * l.D) * 4, kb = (size_t)(T * l.top_k) * 4;
+  const struct { const void* p; size_t n; } in[10] = {
+      {x, xb}, {router, (size_t)(l.E * l.D) * 4},
+      {l.gate, moe_matrix_bytes(l, l.F, l.D)}, {l.up, moe_matrix_bytes(l, l.F, l.D)},
+      {l.down, moe_matrix_bytes(l, l.D, l.F)},
+      {scaled ? l.gate_scale : nullptr, moe_scale_bytes(l, l.F, l.D)},
+      {scaled ? l.up_scale : nullptr, moe_scale_bytes(l, l.F, l.D)},
+      {scaled ? l.down_scale : nullptr, moe_scale_bytes(l, l.D, l.F)},
+      {routed ? ids : nullptr, kb}, {routed ? weights : nullptr, kb}};
+  const struct { const void* p; size_t n; } out[4] = {
+      {dst, xb}, {ws, p.ws_bytes}, {routed ? nullptr : ids, kb}, {routed ? nullptr : weights, kb}};
+  for (int i = 0; i < 4; ++i) {
+    for (const auto& v : in)
+      if (ranges_overlap(out[i].p, out[i].n, v.p, v.n)) return MM_ERR_ALIAS;
+    for (int j = 0; j < i; ++j)
+      if (ranges_overlap(out[i].p, out[i].n, out[j].p, out[j].n)) return MM_ERR_ALIAS;
+  }
+  st = check_device();
+  if (st != MM_OK) return st;
+  uint8_t* const b = (uint8_t*)ws;
+  MoeArgs a;
+  a.x = x;
+  a.router = l.router;
+  a.gate = (const uint8_t*)l.gate; a.up = (const uint8_t*)l.up; a.down = (const uint8_t*)l.down;
+  a.gate_scale = l.gate_scale; a.up_scale = l.up_scale; a.down_scale = l.down_scale;
+  a.dst = dst;
+  a.logits = (double*)(b + p.off_logits);
+  a.ids = ids && !routed ? ids : (int*)(b + p.off_ids);
+  a.weights = weights && !routed ? weights : (float*)(b + p.off_weights);
+  a.given_ids = routed ? ids : nullptr;
+  a.given_weights = routed ? weights : nullptr;
+  a.xp = b + p.off_xp; a.xs = (float*)(b + p.off_xs);
+  a.hp = b + p.off_hp; a.hs = (float*)(b + p.off_hs);
+  a.T = (int)T; a.D = (int)l.D; a.F = (int)l.F; a.E = (int)l.E;
+  a.top_k = l.top_k; a.norm = l.norm != 0;
+  a.fold = p.fold;
+  a.up_groups = p.up_groups;
+  return hip_status(launch_moe(l.type, p, a, (float*)(b + p.off_part), (hipStream_t)stream));
 }
 
 }  // namespace
@@ -424,57 +551,89 @@ size_t mm_moe_workspace_size(const mm_moe_layer* layer, int64_t T) {
 
 mm_status mm_moe_f32(const mm_moe_layer* layer, const float* x, float* dst, int32_t* ids,
                      float* weights, int64_t T, void* ws, size_t ws_bytes, void* stream) {
-  if (!layer) return MM_ERR_NULL;
-  const mm_moe_layer& l = *layer;
+  return as_status(moe(layer, x, dst, ids, weights, false, T, ws, ws_bytes, stream));
+}
+
+size_t mm_moe_routed_workspace_size(const mm_moe_layer* layer, int64_t T) {
   MoePlan p;
-  int st = make_moe_plan(l.type, T, l.D, l.F, l.E, l.top_k, &p);
-  if (st != MM_OK) return as_status(st);
+  if (!layer || make_moe_plan(layer->type, T, layer->D, layer->F, layer->E, layer->top_k, &p, true) != MM_OK)
+    return 0;
+  return p.ws_bytes;
+}
+
+mm_status mm_moe_routed_f32(const mm_moe_layer* layer, const float* x, const int32_t* ids,
+                            const float* weights, float* dst, int64_t T, void* ws, size_t ws_bytes,
+                            void* stream) {
+  return as_status(moe(layer, x, dst, const_cast<int32_t*>(ids), const_cast<float*>(weights), true, T,
+                       ws, ws_bytes, stream));
+}
+
+mm_status mm_route_f32(const mm_router* router, const float* logits, int32_t* ids, float* weights,
+                       int64_t T, void* stream) {
+  if (!router) return MM_ERR_NULL;
+  const mm_router& r = *router;
+  if ((r.score != MM_SCORE_SOFTMAX && r.score != MM_SCORE_SIGMOID) || r.group_top < 1 || r.group_top > 2)
+    return MM_ERR_ARG;
+  if (T < 0 || T > kRouteMaxTokens || r.E < 1 || r.E > kRouteMaxExperts || r.top_k < 1 ||
+      r.top_k > kRouteMaxTopK || r.top_k > r.E || r.groups < 1 || r.groups > 64 || r.E % r.groups ||
+      r.group_k < 1 || r.group_k > r.groups)
+    return MM_ERR_SHAPE;
   if (T == 0) return MM_OK;
-  const bool f8 = l.type == MM_TYPE_F8;
-  if (!x || !dst || !l.router || !l.gate || !l.up || !l.down) return MM_ERR_NULL;
-  if (f8 && (!l.gate_scale || !l.up_scale || !l.down_scale)) return MM_ERR_NULL;
-  const auto off = [](const void* v, uintptr_t a) { return (uintptr_t)v % a != 0; };
-  if (off(x, 16) || off(l.router, 16) || off(l.gate, 16) || off(l.up, 16) || off(l.down, 16) ||
-      off(dst, 4) || off(ids, 4) || off(weights, 4))
-    return MM_ERR_ALIGN;
-  if (f8 && (off(l.gate_scale, 4) || off(l.up_scale, 4) || off(l.down_scale, 4))) return MM_ERR_ALIGN;
-  if (!ws || ws_bytes < p.ws_bytes) return MM_ERR_WORKSPACE;
-  if (off(ws, 256)) return MM_ERR_ALIGN;
-  const size_t xb = (size_t)(T * l.D) * 4, kb = (size_t)(T * l.top_k) * 4;
-  const struct { const void* p; size_t n; } in[8] = {
-      {x, xb}, {l.router, (size_t)(l.E * l.D) * 4},
-      {l.gate, moe_matrix_bytes(l, l.F, l.D)}, {l.up, moe_matrix_bytes(l, l.F, l.D)},
-      {l.down, moe_matrix_bytes(l, l.D, l.F)},
-      {f8 ? l.gate_scale : nullptr, moe_scale_bytes(l, l.F, l.D)},
-      {f8 ? l.up_scale : nullptr, moe_scale_bytes(l, l.F, l.D)},
-      {f8 ? l.down_scale : nullptr, moe_scale_bytes(l, l.D, l.F)}};
-  const struct { const void* p; size_t n; } out[4] = {
-      {dst, xb}, {ids, kb}, {weights, kb}, {ws, p.ws_bytes}};
-  for (int i = 0; i < 4; ++i) {
-    for (const auto& v : in)
-      if (ranges_overlap(out[i].p, out[i].n, v.p, v.n)) return MM_ERR_ALIAS;
-    for (int j = 0; j < i; ++j)
-      if (ranges_overlap(out[i].p, out[i].n, out[j].p, out[j].n)) return MM_ERR_ALIAS;
-  }
-  st = check_device();
+  if (!logits || !ids || !weights) return MM_ERR_NULL;
+  const auto off = [](const void* v) { return (uintptr_t)v % 4 != 0; };
+  if (off(logits) || off(r.bias) || off(ids) || off(weights)) return MM_ERR_ALIGN;
+  const size_t lb = (size_t)T * (size_t)r.E * 4, kb = (size_t)T * (size_t)r.top_k * 4;
+  if (ranges_overlap(ids, kb, logits, lb) || ranges_overlap(weights, kb, logits, lb) ||
+      ranges_overlap(ids, kb, r.bias, (size_t)r.E * 4) || ranges_overlap(weights, kb, r.bias, (size_t)r.E * 4) ||
+      ranges_overlap(ids, kb, weights, kb))
+    return MM_ERR_ALIAS;
+  const int st = check_device();
   if (st != MM_OK) return as_status(st);
-  uint8_t* const b = (uint8_t*)ws;
-  MoeArgs a;
-  a.x = x;
-  a.router = l.router;
-  a.gate = (const uint8_t*)l.gate; a.up = (const uint8_t*)l.up; a.down = (const uint8_t*)l.down;
-  a.gate_scale = l.gate_scale; a.up_scale = l.up_scale; a.down_scale = l.down_scale;
-  a.dst = dst;
-  a.logits = (double*)(b + p.off_logits);
-  a.ids = ids ? ids : (int*)(b + p.off_ids);
-  a.weights = weights ? weights : (float*)(b + p.off_weights);
-  a.xp = b + p.off_xp; a.xs = (float*)(b + p.off_xs);
-  a.hp = b + p.off_hp; a.hs = (float*)(b + p.off_hs);
-  a.T = (int)T; a.D = (int)l.D; a.F = (int)l.F; a.E = (int)l.E;
-  a.top_k = l.top_k; a.norm = l.norm != 0;
-  a.fold = p.fold;
-  a.up_groups = p.up_groups;
-  return as_status(hip_status(launch_moe(l.type, p, a, (float*)(b + p.off_part), (hipStream_t)stream)));
+  RouteArgs a;
+  a.logits = logits; a.bias = r.bias; a.ids = ids; a.weights = weights;
+  a.T = T; a.E = (int)r.E; a.top_k = r.top_k;
+  // every group taken: no groups
+  a.groups = r.group_k < r.groups ? r.groups : 1;
+  a.group_k = r.group_k; a.group_top = r.group_top;
+  a.lanes_per_group = 1;
+  while (2 * a.lanes_per_group * a.groups <= 64) a.lanes_per_group *= 2;
+  a.softmax = r.score == MM_SCORE_SOFTMAX; a.norm = r.norm != 0; a.scale = r.scale;
+  return as_status(hip_status(launch_route(a, (hipStream_t)stream)));
+}
+
+mm_status mm_rms_norm_f32(const float* x, const float* residual, const float* weight, float eps,
+                          float* sum, int out_type, void* y, void* scales, int64_t T, int64_t D,
+                          void* stream) {
+  if (out_type != MM_TYPE_F32 && out_type != MM_TYPE_F8 && out_type != MM_TYPE_MXFP4) return MM_ERR_ARG;
+  if (!(eps >= 0.0f)) return MM_ERR_ARG;
+  const bool scaled = out_type != MM_TYPE_F32;
+  if (T < 0 || D < 0 || D > kNormMaxDim || (scaled && D % kQK)) return MM_ERR_SHAPE;
+  if (T == 0 || D == 0) return MM_OK;
+  int waves, rows;
+  norm_shape(T, D, &waves, &rows);
+  if (T > kF8MaxK * 256 || (T + rows - 1) / rows * (64 * waves * rows) > 0xffffffffll) return MM_ERR_SHAPE;
+  if (!x || !y || (scaled && !scales)) return MM_ERR_NULL;
+  const auto off = [](const void* v, uintptr_t a) { return (uintptr_t)v % a != 0; };
+  if (off(x, 4) || off(residual, 4) || off(weight, 4) || off(sum, 4) || off(y, scaled ? 16 : 4) ||
+      (scaled && off(scales, 4)))
+    return MM_ERR_ALIGN;
+  const size_t n = (size_t)T * (size_t)D, xb = n * 4, wb = (size_t)D * 4;
+  const size_t yb = out_type == MM_TYPE_F32 ? xb : out_type == MM_TYPE_F8 ? n : n / 2;
+  const size_t sb = scaled ? (size_t)T * (size_t)((D + 127) / 128) * 4 : 0;
+  // the sum may take the place of x or of the residual, nothing else may overlap
+  if ((sum != x && ranges_overlap(sum, xb, x, xb)) || (sum != residual && ranges_overlap(sum, xb, residual, xb)) ||
+      ranges_overlap(sum, xb, weight, wb) || ranges_overlap(sum, xb, y, yb) || ranges_overlap(sum, xb, scales, sb))
+    return MM_ERR_ALIAS;
+  const struct { const void* p; size_t n; } in[3] = {{x, xb}, {residual, xb}, {weight, wb}};
+  for (const auto& v : in)
+    if (ranges_overlap(y, yb, v.p, v.n) || ranges_overlap(scales, sb, v.p, v.n)) return MM_ERR_ALIAS;
+  if (ranges_overlap(y, yb, scales, sb)) return MM_ERR_ALIAS;
+  const int st = check_device();
+  if (st != MM_OK) return as_status(st);
+  NormArgs a;
+  a.x = x; a.residual = residual; a.weight = weight; a.sum = sum; a.y = y; a.scales = scales;
+  a.T = T; a.D = (int)D; a.eps = eps;
+  return as_status(hip_status(launch_rms_norm(out_type, a, (hipStream_t)stream)));
 }
 
 size_t mm_mul_mat_q4_0_group_workspace_size(int count, const int64_t* Ns, int64_t M, int64_t K) {
@@ -558,6 +717,7 @@ mm_status mm_mul_mat_q4_0_f32_group(int count, const void* const* src0s, float* 
 
 size_t mm_mul_mat_workspace_size(int type, int64_t M, int64_t N, int64_t K) {
   if (type == MM_TYPE_F8) return mm_mul_mat_f8_workspace_size(M, N, K, 0);
+  if (type == MM_TYPE_MXFP4) return mm_mul_mat_mxfp4_workspace_size(M, N, K, 0);
   Plan p;
   if (make_plan(type, M, N, K, 0, &p) != MM_OK) return 0;
   return p.ws_bytes;

@@ -112,6 +112,16 @@ hipError_t launch_f8_quantize(const float* x, uint8_t* codes, float* scales, int
 hipError_t launch_f8_product(const F8Plan& p, const uint8_t* w, const float* wsc, const float* x,
                              const uint8_t* a, const float* asc, float* dst, int M, int N, int K,
                              void* ws, hipStream_t s);
+// MXFP4: x [nrows][k] <-> codes [nrows][k/2], scales [nrows][4 ceil(k/128)].
+hipError_t launch_mx4_quantize(const float* x, uint8_t* codes, uint8_t* scales, int64_t nrows,
+                               int64_t k, hipStream_t s);
+hipError_t launch_mx4_dequantize(const uint8_t* codes, const uint8_t* scales, float* y, int64_t nrows,
+                                 int64_t k, hipStream_t s);
+// Product with MXFP4 weights; x != NULL: src1 as f32 (a, asc unused), else as
+// codes a and scales asc.
+hipError_t launch_mx4_product(const Mx4Plan& p, const uint8_t* w, const uint8_t* wsc, const float* x,
+                              const uint8_t* a, const uint8_t* asc, float* dst, int M, int N, int K,
+                              void* ws, hipStream_t s);
 // dst[i] = sum over z = 0..slices-1, in that order, of part[z * n + i]; part 16-byte
 // aligned.  (k_splitk_reduce with several slices' loads under way.)
 hipError_t launch_join_slices(const float* part, float* dst, int64_t n, int slices, hipStream_t s);
@@ -121,7 +131,8 @@ struct MoeArgs {
   const float* x;                    // [T][D]
   const float* router;               // [E][D]
   const uint8_t *gate, *up, *down;   // [E][F][D], [E][F][D], [E][D][F] in `type`
-  const float *gate_scale, *up_scale, *down_scale;   // F8: [E][ceil(rows/128)][ceil(K/128)]
+  const void *gate_scale, *up_scale, *down_scale;   // F8: f32 [E][ceil(rows/128)][ceil(K/128)];
+                                                     // MXFP4: bytes [E][rows][4 ceil(K/128)]
   float* dst;                        // [T][D]
   double* logits;                    // [T][E]
   int* ids;                          // [T][top_k]
@@ -133,9 +144,34 @@ struct MoeArgs {
   int T, D, F, E, top_k, norm;
   int up_groups;                     // gate / up: workgroups along F per expert
   int fold;                          // the selection is made by the gate / up launch
+  const int* given_ids;              // the choice where it is an input (else NULL), [T][top_k],
+  const float* given_weights;        // and its weights; ids and weights then lie in the workspace
 };
 // part: slices of dst ([p.slices][T][D]; unused with one slice).
 hipError_t launch_moe(int type, const MoePlan& p, const MoeArgs& a, float* part, hipStream_t s);
+struct NormArgs {
+  const float *x, *residual;         // [T][D]; residual may be NULL
+  const float* weight;               // [D], may be NULL (ones)
+  float* sum;                        // [T][D], may be NULL; may be x or residual
+  void* y;                           // f32 [T][D], e4m3 codes [T][D] or MXFP4 codes [T][D/2]
+  void* scales;                      // F8: f32 [T][ceil(D/128)]; MXFP4: dwords [T][ceil(D/128)]
+  int64_t T;
+  int D;
+  float eps;
+};
+hipError_t launch_rms_norm(int type, const NormArgs& a, hipStream_t s);
+struct RouteArgs {
+  const float* logits;               // [T][E]
+  const float* bias;                 // [E], may be NULL
+  int* ids;                          // [T][top_k]
+  float* weights;                    // [T][top_k]
+  int64_t T;
+  int E, top_k, groups, group_k, group_top;
+  int lanes_per_group;               // a power of two; groups * lanes_per_group <= 64
+  int softmax, norm;
+  float scale;
+};
+hipError_t launch_route(const RouteArgs& a, hipStream_t s);
 hipError_t launch_zero(float* dst, int64_t n, hipStream_t s);
 // dst[i] = sum over z = 0..split-1, in that order, of part[z * n + i].
 hipError_t launch_splitk_reduce(const float* part, float* dst, int64_t n, int split, hipStream_t s);

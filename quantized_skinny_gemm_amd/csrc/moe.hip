@@ -5,6 +5,8 @@
 //   h = silu(gate_e x[t]) * (up_e x[t]);  dst[t] = sum over the chosen of
 //   w * down_e h.
 //
+// The choice of experts and their weights may be inputs instead (k_moe_take).
+//
 // Launches on one stream: the router's logits (and x in split form); the
 // selection, unless it is small enough for every workgroup of the next
 // launch to make it for itself; gate, up and h; down and the weighted sum
@@ -13,7 +15,7 @@
 // is arranged around that stream:
 //
 // * Products run on v_mfma_f32_16x16x32_f16, weights decoded to binary16 in
-//   registers (Q4_0 codes - 8, e4m3 codes and binary16 are all exact in it)
+//   registers (Q4_0 codes - 8, e4m3 and e2m1 codes and binary16 are all exact in it)
 //   as operand B, tokens as the 16 rows of operand A.  One MFMA covers one
 //   block of 32 k.
 // * Activations stay fp32 in effect: each row's block of 32 values is scaled
@@ -103,6 +105,58 @@ __device__ __forceinline__ float half_wave_max(float v) {
   return fmaxf(v, __shfl_xor(v, 16, 64));
 }
 
+// Splits 8 blocks of 32 values, 8 part .. 8 part + 7, of TT tokens from t0: a half
+// wave (of 256 threads) each.
+template <int TY, int TT>
+__device__ __forceinline__ void split_rows(const float* __restrict__ x, uint8_t* __restrict__ xp,
+                                           float* __restrict__ xs, int T, int D, int t0, int part) {
+  const int tid = threadIdx.x;
+  const int nb = D / 32, nbp = (nb + 3) & ~3, c = tid & 31;
+  const int b = part * 8 + (tid >> 5);
+  if (b >= nbp) return;
+  float v[TT];
+#pragma unroll
+  for (int j = 0; j < TT; ++j)
+    v[j] = b < nb ? x[(int64_t)min(t0 + j, T - 1) * D + 32 * b + c] : 0.0f;
+#pragma unroll
+  for (int j = 0; j < TT; ++j) {
+    const int t = t0 + j;
+    if (t >= T) break;
+    float s = 0.0f;
+    if (b < nb) s = split_store<TY>(xp + ((int64_t)t * nb + b) * 128, c, v[j], half_wave_max(fabsf(v[j])));
+    if (c == 0) xs[(int64_t)t * nbp + b] = s;
+  }
+}
+
+// A routing that is given: x in split form, and (one workgroup) the choice made
+// fit for the launches behind it: what names no expert becomes -1, an expert that
+// a token names several times is kept once, with the sum of its weights (so that
+// no expert has more rows than there are tokens, and no two rows of one job add
+// to the same sum).
+template <int TY, int TT>
+__global__ __launch_bounds__(256) void k_moe_take(MoeArgs a, int splits) {
+  if ((int)blockIdx.x < splits) {
+    split_rows<TY, TT>(a.x, a.xp, a.xs, a.T, a.D, blockIdx.y * TT, blockIdx.x);
+    return;
+  }
+  if (blockIdx.y) return;
+  const int k = a.top_k;
+  for (int i = threadIdx.x; i < a.T * k; i += 256) {
+    const int first = i / k * k;
+    int id = a.given_ids[i];
+    float w = a.given_weights[i];
+    if (id < 0 || id >= a.E) id = -1;
+    if (id >= 0) {
+      for (int j = first; j < i; ++j)
+        if (a.given_ids[j] == id) { id = -1; break; }
+      for (int j = i + 1; j < first + k && id >= 0; ++j)
+        if (a.given_ids[j] == id) w += a.given_weights[j];
+    }
+    a.ids[i] = id;
+    a.weights[i] = w;
+  }
+}
+
 // ---------------------------------------------------------------- router
 
 // Logits in fp64 (the products of two fp32 values are exact there): the
@@ -119,21 +173,7 @@ __global__ __launch_bounds__(256) void k_moe_router(const float* __restrict__ x,
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int t0 = blockIdx.y * TT;
   if ((int)blockIdx.x >= E) {
-    const int nb = D / 32, nbp = (nb + 3) & ~3, c = tid & 31;
-    const int b = ((int)blockIdx.x - E) * 8 + (tid >> 5);              // per half wave
-    if (b >= nbp) return;
-    float v[TT];
-#pragma unroll
-    for (int j = 0; j < TT; ++j)
-      v[j] = b < nb ? x[(int64_t)min(t0 + j, T - 1) * D + 32 * b + c] : 0.0f;
-#pragma unroll
-    for (int j = 0; j < TT; ++j) {
-      const int t = t0 + j;
-      if (t >= T) break;
-      float s = 0.0f;
-      if (b < nb) s = split_store<TY>(xp + ((int64_t)t * nb + b) * 128, c, v[j], half_wave_max(fabsf(v[j])));
-      if (c == 0) xs[(int64_t)t * nbp + b] = s;
-    }
+    split_rows<TY, TT>(x, xp, xs, T, D, t0, (int)blockIdx.x - E);
     return;
   }
   const int e = blockIdx.x;
@@ -249,7 +289,7 @@ struct Tile<MM_TYPE_Q4_0R> {
   const uint8_t* base;
   v4u c;                         // whole vectors, so that they stay in the registers that
   v2u d;                         // the loads fill
-  __device__ __forceinline__ void bind(const uint8_t* w, const float*, int64_t e, int N, int K,
+  __device__ __forceinline__ void bind(const uint8_t* w, const void*, int64_t e, int N, int K,
                                        int row0, int lane) {
     const int64_t phases = (K + 255) / 256;
     base = w + (e * (N / 16) + row0 / 16) * phases * kQ4RChunk + 16 * lane;
@@ -293,12 +333,12 @@ struct Tile<MM_TYPE_F8> {
   int chunk, K;
   uint2 c[4];
   float d, dnext;
-  __device__ __forceinline__ void bind(const uint8_t* w, const float* s, int64_t e, int N, int k,
+  __device__ __forceinline__ void bind(const uint8_t* w, const void* s, int64_t e, int N, int k,
                                        int row0, int lane) {
     const int64_t nkb = (k + 127) / 128;
     K = k;
     base = w + (e * N + row0) * k;
-    sc = s + (e * ((N + 127) / 128) + row0 / 128) * nkb;
+    sc = (const float*)s + (e * ((N + 127) / 128) + row0 / 128) * nkb;
     // piece q: rows 8 q + lane / 8, position lane % 8; (row / 2) % 8
 #pragma unroll
     for (int q = 0; q < 2; ++q) off[q] = (uint32_t)(8 * q + (lane >> 3)) * (uint32_t)k;
@@ -329,12 +369,63 @@ struct Tile<MM_TYPE_F8> {
   __device__ __forceinline__ float scale(int) const { return d; }
 };
 
+// MXFP4 goes through LDS too (16 rows of 64 bytes, a unit's four blocks of 16
+// bytes permuted by (row / 4) % 4): a lane's operand is 4 bytes of its row's block.
+// Its four scale bytes are one dword of its row.
+template <>
+struct Tile<MM_TYPE_MXFP4> {
+  static constexpr int kLds = 1024;
+  const uint8_t* base;           // uniform
+  const uint32_t* sc;
+  uint32_t off;                  // the row and block this lane copies
+  int last, nb;
+  uint32_t c[4];
+  uint32_t d, dnext, keep;
+  __device__ __forceinline__ void bind(const uint8_t* w, const void* s, int64_t e, int N, int k,
+                                       int row0, int lane) {
+    nb = k / 32;
+    last = k / 2 - 16;
+    base = w + (e * N + row0) * (k / 2);
+    sc = (const uint32_t*)s + (e * N + row0 + (lane & 15)) * ((k + 127) / 128);
+    off = (uint32_t)(lane >> 2) * (uint32_t)(k / 2);
+  }
+  __device__ __forceinline__ void load(int u, int, int lane, uint32_t lds) {
+    dnext = sc[u];
+    // blocks past K: the last one again, with scale 1 (they meet activations of scale 0)
+    const int left = nb - 4 * u;
+    keep = left >= 4 ? ~0u : (1u << (8 * left)) - 1;
+    const int at = 64 * u + 16 * ((lane & 3) ^ ((lane >> 4) & 3));
+    copy16(lds, base, off + (uint32_t)min(at, last));
+  }
+  __device__ __forceinline__ void fetch(const uint8_t* lds, int lane) {
+    const int r = lane & 15, g = lane >> 4;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      c[j] = *reinterpret_cast<const uint32_t*>(lds + 64 * r + 16 * (j ^ ((r >> 2) & 3)) + 4 * g);
+    asm volatile("" : "+v"(dnext));
+    d = (dnext & keep) | (0x7f7f7f7fu & ~keep);
+  }
+  __device__ __forceinline__ v8h operand(int j) const {
+    const v2h a = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(c[j], 1.0f, 0);
+    const v2h b = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(c[j], 1.0f, 1);
+    const v2h e = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(c[j], 1.0f, 2);
+    const v2h f = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(c[j], 1.0f, 3);
+    return (v8h){a[0], a[1], b[0], b[1], e[0], e[1], f[0], f[1]};
+  }
+  // 2^(byte - 127): the byte as an exponent, but for 0 (2^-127 is subnormal) and 255
+  // (NaN), which take the fraction's top bit
+  __device__ __forceinline__ float scale(int j) const {
+    const uint32_t x = ((d >> (8 * j)) & 255) << 23;
+    return __builtin_bit_cast(float, ((x + 0x00800000u) & 0x7f000000u) ? x : x | 0x00400000u);
+  }
+};
+
 template <>
 struct Tile<MM_TYPE_F16> {
   static constexpr int kLds = 0;
   const uint8_t* base;
   uint4 c[4];
-  __device__ __forceinline__ void bind(const uint8_t* w, const float*, int64_t e, int N, int K,
+  __device__ __forceinline__ void bind(const uint8_t* w, const void*, int64_t e, int N, int K,
                                        int row0, int lane) {
     base = w + 2 * ((e * N + row0 + (lane & 15)) * K + 8 * (lane >> 4));
   }
@@ -481,7 +572,7 @@ constexpr int kUpWaves = 8;
 // Partial sums kept apart in the join: one per wave, or one per pair of waves
 // (w, w + 4) where e4m3's staging leaves no room for eight.
 template <int TY, bool kFew>
-constexpr int up_parts() { return Tile<TY>::kLds > 0 && !kFew ? kUpWaves / 2 : kUpWaves; }
+constexpr int up_parts() { return Tile<TY>::kLds > 1024 && !kFew ? kUpWaves / 2 : kUpWaves; }
 
 // Dynamic LDS of the gate / up kernel: the waves' staging, then their partial
 // sums (before both, the logits where it makes the selection).
@@ -645,12 +736,14 @@ __global__ __launch_bounds__(64 * kUpWaves, 2) void k_moe_up(MoeArgs a) {
   int e, n = 1;
   if (a.T == 1) {
     e = sids[blockIdx.y];
+    if (e >= E) return;                              // a slot without an expert
     if (tid == 0) list[0] = blockIdx.y;
     __syncthreads();
   } else {
     if (tid < kMoeMaxExperts / 32) bits[tid] = 0;
     __syncthreads();
-    for (int i = tid; i < assigned; i += 64 * W) atomicOr(&bits[sids[i] >> 5], 1u << (sids[i] & 31));
+    for (int i = tid; i < assigned; i += 64 * W)
+      if (sids[i] < E) atomicOr(&bits[sids[i] >> 5], 1u << (sids[i] & 31));
     __syncthreads();
     int left = blockIdx.y, word = 0;
     while (word < kMoeMaxExperts / 32 && left >= __popc(bits[word])) left -= __popc(bits[word++]);
@@ -701,25 +794,34 @@ struct Jobs {
   int count;
 };
 
-// Groups the assignments by expert, in ascending order within one (the order
-// decides which job a token of a much used expert falls into, and with it how
+// Groups the assignments by expert (an id of -1: none), in ascending order within
+// one (the order decides which job a token of a much used expert falls into, and with it how
 // the waves cut its sum).
 __device__ __forceinline__ void make_jobs(Jobs& js, const int* ids, int T, int assigned, int E,
                                           int lane, int wave) {
   const int tid = threadIdx.x, nt = blockDim.x;
   if (T == 1) {                                      // every assignment is a job
-    if (tid < assigned) {
-      js.e[tid] = (uint16_t)ids[tid];
-      js.first[tid] = js.order[tid] = (uint16_t)tid;
-      js.rows[tid] = 1;
+    if (wave == 0) {
+      const int id = lane < assigned ? ids[lane] : -1;
+      const uint64_t vote = __ballot(id >= 0);
+      const int j = __popcll(vote & ((1ull << lane) - 1));
+      if (id >= 0) {
+        js.e[j] = (uint16_t)id;
+        js.first[j] = (uint16_t)j;
+        js.order[j] = (uint16_t)lane;
+        js.rows[j] = 1;
+      }
+      if (lane == 0) js.count = __popcll(vote);
     }
-    if (tid == 0) js.count = assigned;
     __syncthreads();
     return;
   }
   for (int e = tid; e < E; e += nt) js.cnt[e] = 0;
   __syncthreads();
-  for (int i = tid; i < assigned; i += nt) atomicAdd(&js.cnt[ids[i]], 1);
+  for (int i = tid; i < assigned; i += nt) {
+    const int id = ids[i];
+    if (id >= 0) atomicAdd(&js.cnt[id], 1);
+  }
   __syncthreads();
   if (wave == 0) {
     int base = 0, jobs = 0;
@@ -753,8 +855,9 @@ __device__ __forceinline__ void make_jobs(Jobs& js, const int* ids, int T, int a
   if (wave == 0) {
     // 64 at a time: the lanes of the same expert by one vote per bit of its index
     for (int b = 0; b < assigned; b += 64) {
-      const bool in = b + lane < assigned;
-      const int e = in ? ids[b + lane] : 0;
+      const int id = b + lane < assigned ? ids[b + lane] : -1;
+      const bool in = id >= 0;
+      const int e = in ? id : 0;
       uint64_t same = __ballot(in);
 #pragma unroll
       for (int bit = 1; bit < kMoeMaxExperts; bit <<= 1) {
@@ -871,13 +974,16 @@ hipError_t up(dim3 grid, const MoeArgs& a, hipStream_t s) {
 template <int TY>
 hipError_t run(const MoePlan& p, const MoeArgs& a, float* part, hipStream_t s) {
   const int splits = (((a.D / 32 + 3) & ~3) + 7) / 8;
-  if (a.T == 1)
+  if (a.given_ids) {
+    if (a.T == 1) hipLaunchKernelGGL((k_moe_take<TY, 1>), dim3(splits + 1, 1), dim3(256), 0, s, a, splits);
+    else hipLaunchKernelGGL((k_moe_take<TY, 4>), dim3(splits + 1, (a.T + 3) / 4), dim3(256), 0, s, a, splits);
+  } else if (a.T == 1)
     hipLaunchKernelGGL((k_moe_router<TY, 1>), dim3(a.E + splits, 1), dim3(256), 0, s, a.x, a.router, a.logits, a.xp, a.xs, a.T, a.D, a.E);
   else
     hipLaunchKernelGGL((k_moe_router<TY, 4>), dim3(a.E + splits, (a.T + 3) / 4), dim3(256), 0, s, a.x, a.router, a.logits, a.xp, a.xs, a.T, a.D, a.E);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  if (!a.fold) {
+  if (!a.fold && !a.given_ids) {
     hipLaunchKernelGGL(k_moe_select, dim3(a.T), dim3(512), 0, s, a.logits, a.ids, a.weights, a.E, a.top_k, a.norm);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
@@ -903,6 +1009,7 @@ hipError_t launch_moe(int type, const MoePlan& p, const MoeArgs& a, float* part,
     case MM_TYPE_Q4_0R: return run<MM_TYPE_Q4_0R>(p, a, part, s);
     case MM_TYPE_F8: return run<MM_TYPE_F8>(p, a, part, s);
     case MM_TYPE_F16: return run<MM_TYPE_F16>(p, a, part, s);
+    case MM_TYPE_MXFP4: return run<MM_TYPE_MXFP4>(p, a, part, s);
     default: return hipErrorInvalidValue;
   }
 }

@@ -12,9 +12,11 @@ size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 
 }  // namespace
 
-int make_moe_plan(int type, int64_t T, int64_t D, int64_t F, int64_t E, int64_t top_k, MoePlan* p) {
+int make_moe_plan(int type, int64_t T, int64_t D, int64_t F, int64_t E, int64_t top_k, MoePlan* p,
+                  bool routed) {
   *p = MoePlan();
-  if (type != MM_TYPE_Q4_0R && type != MM_TYPE_F8 && type != MM_TYPE_F16) return MM_ERR_ARG;
+  if (type != MM_TYPE_Q4_0R && type != MM_TYPE_F8 && type != MM_TYPE_F16 && type != MM_TYPE_MXFP4)
+    return MM_ERR_ARG;
   if (T < 0 || T > kMoeMaxTokens || D < 1 || D > kMoeMaxDim || D % kQK || F < 1 || F > kMoeMaxDim ||
       F % kQK || E < 1 || E > kMoeMaxExperts || top_k < 1 || top_k > kMoeMaxTopK || top_k > E)
     return MM_ERR_SHAPE;
@@ -26,7 +28,7 @@ int make_moe_plan(int type, int64_t T, int64_t D, int64_t F, int64_t E, int64_t 
     return at;
   };
   const size_t slots = (size_t)(T * top_k);
-  p->off_logits = take((size_t)(T * E) * 8);
+  if (!routed) p->off_logits = take((size_t)(T * E) * 8);
   p->off_ids = take(slots * 4);
   p->off_weights = take(slots * 4);
   p->off_xp = take((size_t)(T * D) * 4);
@@ -35,7 +37,7 @@ int make_moe_plan(int type, int64_t T, int64_t D, int64_t F, int64_t E, int64_t 
   p->off_hs = take(slots * align_up((size_t)(F / kQK), 4) * 4);
   // The selection costs each workgroup of the next launch about T E^2 / 512
   // steps per thread where it makes it itself.
-  p->fold = T * E * E <= 65536;
+  p->fold = !routed && T * E * E <= 65536;
   // Down: 16 rows per workgroup while an expert serves few tokens; with more,
   // 64 rows share each activation load (activations are 4 bytes a value, the
   // weights as few as half a byte) and the sequence of (expert, unit) pairs
@@ -52,9 +54,10 @@ int make_moe_plan(int type, int64_t T, int64_t D, int64_t F, int64_t E, int64_t 
   const bool many = T * top_k > 2 * used;
   const bool few = T <= kMoeFewTokens;
   // (the per-wave sums of T tokens x 16 rt rows, 8 waves, share the LDS with
-  // the staging, which e4m3 weights need too)
+  // the staging, which e4m3 and MXFP4 weights need too)
   const bool f8 = type == MM_TYPE_F8;
-  p->rt = few || !many ? 1 : !f8 && D % 64 == 0 && T <= 32 ? 4 : D % 32 == 0 && T <= (f8 ? 32 : 64) ? 2 : 1;
+  const int64_t most4 = type == MM_TYPE_MXFP4 ? 24 : 32;
+  p->rt = few || !many ? 1 : !f8 && D % 64 == 0 && T <= most4 ? 4 : D % 32 == 0 && T <= (f8 ? 32 : 64) ? 2 : 1;
   const int64_t tiles = D / (16 * p->rt), units = used * ((F / kQK + 3) / 4);
   int64_t slices = few ? 1 : p->rt > 1 ? (2 * kCUs + tiles - 1) / tiles : kCUs / tiles;
   if (slices > units / 64) slices = units / 64;

@@ -1,0 +1,566 @@
+// Microscaled 4-bit floating point (MXFP4): quantizer, its inverse and the
+// product, for gfx950.
+//
+// Product: dst[m][n] = sum_b 2^(ea[m][b] + ew[n][b]) S_b[m][n], S_b the dot of the
+// 32 code pairs of block b, on the scaled matrix instructions
+// (v_mfma_scale_f32_16x16x128_f8f6f4 and 32x32x64, both operands e2m1), which
+// take the blocks' scale bytes as they are stored.  Code products are multiples
+// of 1/4 up to 36, so S_b is exact in 13 bits; an instruction's sum and the fp32
+// accumulation are exact too while the blocks' scales lie within a few binades
+// (measured: 0 with scales within 2^4 of each other, 1e-7 to 2.6e-7 in the
+// 2-norm, K up to 16384, with scales spread over 2^24).  src1 is operand A and the
+// weights operand B, so that 16 or 32 neighbouring lanes hold neighbouring
+// outputs of one row.
+//
+// A lane's operand is one whole block: 16 consecutive bytes of codes and one
+// byte of scale.
+#include <type_traits>
+
+#include "kernels.h"
+#include "mx4.h"
+
+namespace qsg {
+
+namespace {
+
+typedef float v4f __attribute__((ext_vector_type(4)));
+typedef float v2f __attribute__((ext_vector_type(2)));
+typedef int v8i __attribute__((ext_vector_type(8)));
+
+constexpr int kGrp = kMx4Group;         // 128: four blocks, one dword of scale bytes
+
+__device__ __forceinline__ v8i operand(const uint4& c) {
+  return (v8i){(int)c.x, (int)c.y, (int)c.z, (int)c.w, 0, 0, 0, 0};
+}
+
+// ---------------------------------------------------------------- quantizer
+
+// 16 lanes per group of 128 values: one 32-byte load, one 4-byte store of codes
+// per lane.  Bound: HBM (4.53 bytes per value).
+__global__ __launch_bounds__(256) void k_mx4_quantize(const float* __restrict__ x,
+                                                      uint8_t* __restrict__ codes,
+                                                      uint32_t* __restrict__ scales, int K, int ng,
+                                                      int64_t groups) {
+  const int lane = threadIdx.x & 63, i = lane & 15;
+  for (int64_t at = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4); at < groups;
+       at += (int64_t)gridDim.x * 16) {              // whole groups of 16 lanes
+    const int64_t row = at / ng;
+    const int k = (int)(at - row * ng) * kGrp + 8 * i;
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
+    if (k < K) {                                     // K % 32 == 0: all 8 values or none
+      const float4* p = reinterpret_cast<const float4*>(x + row * K + k);
+      a = p[0]; b = p[1];
+    }
+    uint32_t bytes;
+    const uint32_t c = mx4_group(a, b, k < K, lane, bytes);
+    if (k < K) *reinterpret_cast<uint32_t*>(codes + (row * K + k) / 2) = c;
+    if (i == 0) scales[at] = bytes;
+  }
+}
+
+// Eight values per lane.  Bound: HBM.
+__global__ __launch_bounds__(256) void k_mx4_dequantize(const uint8_t* __restrict__ codes,
+                                                        const uint8_t* __restrict__ scales,
+                                                        float* __restrict__ y, int K, int ng,
+                                                        int64_t pieces) {
+  const int per = K / 8;
+  for (int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x; at < pieces;
+       at += (int64_t)gridDim.x * 256) {
+    const int64_t row = at / per;
+    const int p = (int)(at - row * per);
+    const uint32_t c = *reinterpret_cast<const uint32_t*>(codes + 4 * at);
+    const int byte = scales[row * 4 * ng + p / 4];
+    v2f v[4];
+    v[0] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, 1.0f, 0);
+    v[1] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, 1.0f, 1);
+    v[2] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, 1.0f, 2);
+    v[3] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, 1.0f, 3);
+    float f[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      f[j] = __builtin_amdgcn_ldexpf(v[j / 2][j % 2], byte - 127);
+      if (byte == 255) f[j] = __builtin_nanf("");
+    }
+    float4* const out = reinterpret_cast<float4*>(y + 8 * at);
+    out[0] = make_float4(f[0], f[1], f[2], f[3]);
+    out[1] = make_float4(f[4], f[5], f[6], f[7]);
+  }
+}
+
+// ---------------------------------------------------------------- product, few src1 rows
+
+// A lane's block (k = 128 kb + 32 g) of a row, and its scale byte; a block past K
+// is zeros with scale 1 (what is stored there is not read).
+struct Block {
+  uint4 c;
+  int s;
+};
+__device__ __forceinline__ Block load_block(const uint8_t* __restrict__ codes,
+                                            const uint8_t* __restrict__ scales, int kb, int g, int K) {
+  Block b;
+  const int k = kb * kGrp + 32 * g;
+  if ((kb + 1) * kGrp <= K) {                         // uniform: a whole group
+    b.c = *reinterpret_cast<const uint4*>(codes + k / 2);
+    b.s = scales[k / 32];
+  } else {
+    b.c = make_uint4(0, 0, 0, 0);
+    b.s = 127;
+    if (k < K) {
+      b.c = *reinterpret_cast<const uint4*>(codes + k / 2);
+      b.s = scales[k / 32];
+    }
+  }
+  return b;
+}
+
+// Each workgroup takes 16 weight rows and all src1 rows, at most NT tiles of 16;
+// its waves take runs of U groups of 128 k in turn (a wave's loads cover 64 U
+// consecutive bytes of each row); the waves' partial tiles are added in LDS in
+// wave order.
+template <int NT>
+__global__ __launch_bounds__(512) void k_mx4_skinny(
+    const uint8_t* __restrict__ w, const uint8_t* __restrict__ wsc, const uint8_t* __restrict__ a,
+    const uint8_t* __restrict__ asc, int M, int N, int K, float* __restrict__ dst) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+  constexpr int U = 4;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int W = blockDim.x >> 6;
+  const int g = lane >> 4, i16 = lane & 15;
+  const int ng = (K + kGrp - 1) / kGrp;
+  const int n0 = blockIdx.x * 16;
+
+  const int64_t wr = min(n0 + i16, N - 1);
+  const uint8_t* const wrow = w + wr * (K / 2);
+  const uint8_t* const wsr = wsc + wr * 4 * ng;
+  const uint8_t* arow[NT];
+  const uint8_t* asr[NT];
+  bool live[NT];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    const int m = 16 * t + i16;
+    live[t] = m < M;
+    arow[t] = a + (int64_t)(live[t] ? m : 0) * (K / 2);
+    asr[t] = asc + (int64_t)(live[t] ? m : 0) * 4 * ng;
+  }
+  v4f acc[NT];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) acc[t] = (v4f){0.f, 0.f, 0.f, 0.f};
+
+  for (int kb0 = wave * U; kb0 < ng; kb0 += W * U) {
+    Block wb[U], ab[U][NT];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int kb = min(kb0 + u, ng - 1);            // valid addresses throughout
+      wb[u] = load_block(wrow, wsr, kb, g, K);
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        ab[u][t].c = make_uint4(0, 0, 0, 0);
+        ab[u][t].s = 127;
+        if (live[t]) ab[u][t] = load_block(arow[t], asr[t], kb, g, K);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (kb0 + u >= ng) continue;                    // uniform
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+        acc[t] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+            operand(ab[u][t].c), operand(wb[u].c), acc[t], 4, 4, 0, ab[u][t].s, 0, wb[u].s);
+    }
+  }
+
+  // join the waves' partial tiles: [wave][m][n], n fastest
+  float* const part = reinterpret_cast<float*>(lds);
+  constexpr int TILE = 256 * NT;
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) part[wave * TILE + (16 * t + 4 * g + e) * 16 + i16] = acc[t][e];
+  __syncthreads();
+  for (int e = tid; e < TILE; e += blockDim.x) {
+    float s = part[e];
+    for (int v = 1; v < W; ++v) s += part[v * TILE + e];
+    const int m = e / 16, n = n0 + e % 16;
+    if (m < M && n < N) dst[(int64_t)m * N + n] = s;
+  }
+}
+
+// A few src1 rows given as f32: every workgroup quantizes them into LDS itself
+// (16 lanes per group of 128; no INIT launch, no workspace), then walks groups of
+// 16 weight rows, blockIdx.x, blockIdx.x + gridDim.x, ...  The first rows'
+// weights are requested before the quantization waits for src1, each next
+// round's before the current one is computed; the barriers wait for LDS only,
+// so that these loads stay under way.
+template <int ROUNDS>
+__global__ __launch_bounds__(512) void k_mx4_fused(
+    const float* __restrict__ x, const uint8_t* __restrict__ w, const uint8_t* __restrict__ wsc,
+    float* __restrict__ dst, int M, int N, int K, int tiles) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+  constexpr int U = 4, W = 8;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int g = lane >> 4, i16 = lane & 15;
+  const int ng = (K + kGrp - 1) / kGrp, pitch = ng * (kGrp / 2) + 16;   // 16: rows in different banks
+  // codes [M][pitch], scales [M][ng] dwords, the waves' partial tiles
+  uint32_t* const sscale = reinterpret_cast<uint32_t*>(lds + M * pitch);
+  float* const part = reinterpret_cast<float*>(lds + M * pitch + (M * ng * 4 + 15) / 16 * 16);
+
+  // src1: M * ng <= 32 ROUNDS groups of 128, all requested at once
+  const int total = M * ng;
+  float4 p[ROUNDS], q[ROUNDS];
+#pragma unroll
+  for (int r = 0; r < ROUNDS; ++r) {
+    const int b = min((tid >> 4) + 32 * r, total - 1), m = b / ng;
+    const int k = (b - m * ng) * kGrp + 8 * i16;
+    p[r] = q[r] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (k < K) {
+      const float4* s = reinterpret_cast<const float4*>(x + (int64_t)m * K + k);
+      p[r] = s[0]; q[r] = s[1];
+    }
+  }
+  struct Round { Block b[U]; };
+  const auto load = [&](Round& r, int tile, int kb0) {
+    const int64_t row = min(16 * tile + i16, N - 1);
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      r.b[u] = load_block(w + row * (K / 2), wsc + row * 4 * ng, min(kb0 + wave * U + u, ng - 1), g, K);
+  };
+  int tile = blockIdx.x, kb0 = 0;
+  Round cur;
+  load(cur, tile, 0);
+  __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+  for (int r = 0; r < ROUNDS; ++r) {
+    const int b = (tid >> 4) + 32 * r, bc = min(b, total - 1), m = bc / ng;
+    const int k = (bc - m * ng) * kGrp + 8 * i16;
+    uint32_t bytes;
+    const uint32_t c = mx4_group(p[r], q[r], k < K, lane, bytes);
+    if (b < total) {
+      *reinterpret_cast<uint32_t*>(lds + m * pitch + k / 2) = c;
+      if (i16 == 0) sscale[b] = bytes;
+    }
+  }
+  lds_barrier();
+
+  v4f acc = {0.f, 0.f, 0.f, 0.f};
+  while (tile < tiles) {
+    const bool last = kb0 + W * U >= ng;
+    const int ntile = last ? tile + (int)gridDim.x : tile, nkb0 = last ? 0 : kb0 + W * U;
+    Round next;
+    if (ntile < tiles) load(next, ntile, nkb0);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int kb = kb0 + wave * U + u;
+      if (kb >= ng) continue;                          // uniform
+      uint4 c = make_uint4(0, 0, 0, 0);
+      uint32_t s = 0x7f7f7f7fu;
+      if (i16 < M) {
+        c = *reinterpret_cast<const uint4*>(lds + i16 * pitch + kb * (kGrp / 2) + 16 * g);
+        s = sscale[i16 * ng + kb];
+      }
+      acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+          operand(c), operand(cur.b[u].c), acc, 4, 4, 0, (int)(s >> (8 * g)), 0, cur.b[u].s);
+    }
+    if (last) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (4 * g + e < M) part[(wave * M + 4 * g + e) * 16 + i16] = acc[e];
+      lds_barrier();
+      for (int e = tid; e < 16 * M; e += 512) {
+        float s = part[e];
+#pragma unroll
+        for (int v = 1; v < W; ++v) s += part[v * 16 * M + e];
+        const int n = 16 * tile + e % 16;
+        if (n < N) dst[(int64_t)(e / 16) * N + n] = s;
+      }
+      lds_barrier();                                   // the partial tiles are read
+      acc = (v4f){0.f, 0.f, 0.f, 0.f};
+    }
+    cur = next;
+    tile = ntile;
+    kb0 = nkb0;
+  }
+}
+
+// ---------------------------------------------------------------- product, many src1 rows
+
+// Output tile of BM src1 rows x BN weight rows per workgroup; a stage is 256 k
+// (128 bytes of codes and two dwords of scales per row), copied into LDS straight
+// from memory, STAGES of them.  A stage is four steps of 64 k: lane half h holds
+// blocks 4 h + q of the stage in step q, so that its scales are one dword, whose
+// byte q the instruction picks.  Operands are read one step ahead of the products.
+// The one barrier per stage stands before its last step's products: there every
+// wave has read the whole stage, so the copy of the stage STAGES further can
+// start, and the next stage has arrived.
+//
+// In LDS a row's eight 16-byte chunks are permuted by (row / 2) % 8, so that the
+// rows of an operand read lie in different banks; scales are [dword][row].
+//
+// Where K ends inside the last stage, copies past a row's end take its first
+// codes and its last scales instead; src1's codes are then replaced by zeros and
+// all scales by 1 in registers.
+constexpr int kStageK = 256;
+
+template <int BM, int BN, int WAVES_M, int WAVES_N, int STAGES>
+__global__ __launch_bounds__(64 * WAVES_M * WAVES_N, 1) void k_mx4_wide(
+    const uint8_t* __restrict__ w, const uint8_t* __restrict__ wsc, const uint8_t* __restrict__ a,
+    const uint8_t* __restrict__ asc, int M, int N, int K, float* __restrict__ dst, int tiles_m,
+    int tiles, int split, int kchunk) {
+  constexpr int NW = WAVES_M * WAVES_N;
+  constexpr int WTM = BM / WAVES_M, WTN = BN / WAVES_N;
+  constexpr int TM = WTM / 32, TN = WTN / 32;
+  constexpr int kRow = kStageK / 2;                            // 128 bytes
+  constexpr int kA = BN * kRow, kWS = kA + BM * kRow, kAS = kWS + BN * 8;
+  constexpr int STAGE = kAS + BM * 8;
+  constexpr int WL = BN / 8 / NW, AL = BM / 8 / NW;            // pieces of 8 rows, 1 KB, per wave
+  constexpr int SL = (BM + BN) / 32 / NW;                      // pieces of 64 rows' scale dwords
+  constexpr int kCopies = WL + AL + SL;
+  static_assert((STAGES - 1) * kCopies < 64, "wait counts");
+  static_assert(BN % (8 * NW) == 0 && BM % (8 * NW) == 0 && BM % 64 == 0 && BN % 64 == 0 &&
+                    (BM + BN) % (32 * NW) == 0, "whole pieces");
+  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave % WAVES_M, wn = wave / WAVES_M;
+  const int h = lane >> 5, l32 = lane & 31;
+  const int ng = (K + kGrp - 1) / kGrp, nst = (K + kStageK - 1) / kStageK;
+  const int t = xcd_remap(blockIdx.x, tiles * split);
+  const int z = t / tiles, tt = t - z * tiles;
+  const int tm = tt % tiles_m, tn = tt / tiles_m;    // m fastest: same weight tile adjacent
+  const int m0 = tm * BM, n0 = tn * BN;
+  const int st0 = z * kchunk, s1 = min(st0 + kchunk, nst) - st0;   // first stage, stages
+  const int ragged = K % kStageK ? nst - 1 - st0 : -1;         // the stage that K ends in
+
+  // this lane's part of each piece
+  const uint8_t* const wbase = w + (int64_t)n0 * (K / 2);
+  const uint8_t* const abase = a + (int64_t)m0 * (K / 2);
+  uint32_t woff[WL], aoff[AL];
+  int chunk[WL > AL ? WL : AL];
+#pragma unroll
+  for (int i = 0; i < WL; ++i) woff[i] = (uint32_t)min((i * NW + wave) * 8 + (lane >> 3), N - 1 - n0) * (uint32_t)(K / 2);
+#pragma unroll
+  for (int i = 0; i < AL; ++i) aoff[i] = (uint32_t)min((i * NW + wave) * 8 + (lane >> 3), M - 1 - m0) * (uint32_t)(K / 2);
+#pragma unroll
+  for (int i = 0; i < (WL > AL ? WL : AL); ++i)      // (row / 2) % 8 of row 8 (i NW + wave) + lane / 8
+    chunk[i] = (lane & 7) ^ ((4 * ((i * NW + wave) & 1) + (lane >> 4)) & 7);
+  // scale pieces: dword p % 2 of 64 rows, weights first
+  const uint8_t* sbase[SL];
+  uint32_t soff[SL], sdst[SL];
+  int sdw[SL];
+#pragma unroll
+  for (int i = 0; i < SL; ++i) {
+    const int p = i * NW + wave;
+    const bool isw = p < BN / 32;
+    const int pp = isw ? p : p - BN / 32, r = (pp >> 1) * 64;
+    sdw[i] = pp & 1;
+    sbase[i] = isw ? wsc + (int64_t)n0 * 4 * ng : asc + (int64_t)m0 * 4 * ng;
+    soff[i] = (uint32_t)min(r + lane, (isw ? N - 1 - n0 : M - 1 - m0)) * (uint32_t)ng;
+    sdst[i] = (uint32_t)((isw ? kWS + sdw[i] * BN * 4 : kAS + sdw[i] * BM * 4) + 4 * r);
+  }
+  const uint32_t lds0 = lds_offset(lds);
+  const auto copy_stage = [&](int s, int buf) {
+    const uint32_t base = lds0 + buf * STAGE;
+    const int kb = (st0 + s) * kRow;                 // bytes
+#pragma unroll
+    for (int i = 0; i < WL; ++i) {
+      const int at = kb + 16 * chunk[i];
+      copy16(base + (i * NW + wave) * 1024, wbase, woff[i] + (at < K / 2 ? at : 0));
+    }
+#pragma unroll
+    for (int i = 0; i < AL; ++i) {
+      const int at = kb + 16 * chunk[i];
+      copy16(base + kA + (i * NW + wave) * 1024, abase, aoff[i] + (at < K / 2 ? at : 0));
+    }
+#pragma unroll
+    for (int i = 0; i < SL; ++i)
+      copy4(base + sdst[i], sbase[i], 4 * (soff[i] + (uint32_t)min(2 * (st0 + s) + sdw[i], ng - 1)));
+  };
+
+  v16f acc[TM][TN];
+#pragma unroll
+  for (int i = 0; i < TM; ++i)
+#pragma unroll
+    for (int j = 0; j < TN; ++j)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
+
+  const int wrow = (wn * WTN + l32) * kRow, arow = kA + (wm * WTM + l32) * kRow;
+  const int x8 = (l32 >> 1) & 7;
+  uint4 wr[2][TN], ar[2][TM];
+  const auto read = [&](const uint8_t* base, int q) {
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+      ar[q % 2][i] = *reinterpret_cast<const uint4*>(base + arow + 32 * i * kRow + 16 * ((4 * h + q) ^ x8));
+#pragma unroll
+    for (int j = 0; j < TN; ++j)
+      wr[q % 2][j] = *reinterpret_cast<const uint4*>(base + wrow + 32 * j * kRow + 16 * ((4 * h + q) ^ x8));
+  };
+  uint32_t ws[TN], as[TM];
+  const auto read_scales = [&](const uint8_t* base) {
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+      as[i] = *reinterpret_cast<const uint32_t*>(base + kAS + 4 * (h * BM + wm * WTM + 32 * i + l32));
+#pragma unroll
+    for (int j = 0; j < TN; ++j)
+      ws[j] = *reinterpret_cast<const uint32_t*>(base + kWS + 4 * (h * BN + wn * WTN + 32 * j + l32));
+  };
+
+#pragma unroll
+  for (int s = 0; s < STAGES; ++s)
+    if (s < s1) copy_stage(s, s);
+  if (s1 >= STAGES) wait_copies<(STAGES - 1) * kCopies>();
+  else wait_copies<0>();
+  __builtin_amdgcn_s_barrier();
+  read(lds, 0);
+  read_scales(lds);
+
+  int buf = 0;
+  for (int s = 0; s < s1; ++s) {
+    const uint8_t* const base = lds + buf * STAGE;
+    const int next = buf + 1 == STAGES ? 0 : buf + 1;
+    if (s == ragged) {                               // uniform; bytes of blocks past K: scale 1
+      const int left = (K - (st0 + s) * kStageK - kGrp * h) / 32;      // this half's blocks inside K
+      const uint32_t keep = left >= 4 ? ~0u : left <= 0 ? 0u : (1u << (8 * left)) - 1;
+#pragma unroll
+      for (int i = 0; i < TM; ++i) as[i] = (as[i] & keep) | (0x7f7f7f7fu & ~keep);
+#pragma unroll
+      for (int j = 0; j < TN; ++j) ws[j] = (ws[j] & keep) | (0x7f7f7f7fu & ~keep);
+    }
+    const auto step = [&](auto qc) {
+      constexpr int q = decltype(qc)::value;
+      uint32_t asq[TM], wsq[TN];
+#pragma unroll
+      for (int i = 0; i < TM; ++i) asq[i] = as[i];
+#pragma unroll
+      for (int j = 0; j < TN; ++j) wsq[j] = ws[j];
+      if constexpr (q < 3) {
+        read(base, q + 1);
+      } else {
+        // the next stage is here and this wave's reads of this one are done
+        if (s + STAGES - 1 < s1) wait_copies<(STAGES - 2) * kCopies>();
+        else wait_copies<0>();
+        __builtin_amdgcn_s_barrier();
+        if (s + STAGES < s1) copy_stage(s + STAGES, buf);
+        read(lds + next * STAGE, 0);
+        read_scales(lds + next * STAGE);
+      }
+      __builtin_amdgcn_sched_barrier(0);             // the reads stay ahead of the products
+      if (s == ragged) {                             // uniform
+        if ((st0 + s) * kStageK + kGrp * h + 32 * q >= K)
+#pragma unroll
+          for (int i = 0; i < TM; ++i) ar[q % 2][i] = make_uint4(0, 0, 0, 0);
+      }
+#pragma unroll
+      for (int i = 0; i < TM; ++i)
+#pragma unroll
+        for (int j = 0; j < TN; ++j)
+          acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+              operand(ar[q % 2][i]), operand(wr[q % 2][j]), acc[i][j], 4, 4, q, (int)asq[i], q, (int)wsq[j]);
+    };
+    step(std::integral_constant<int, 0>());
+    step(std::integral_constant<int, 1>());
+    step(std::integral_constant<int, 2>());
+    step(std::integral_constant<int, 3>());
+    buf = next;
+  }
+
+  // lane: weight row of column l32, src1 rows 8 (r / 4) + 4 h + r % 4
+  float* const out = dst + (int64_t)z * M * N;
+#pragma unroll
+  for (int j = 0; j < TN; ++j) {
+    const int n = n0 + wn * WTN + 32 * j + l32;
+    if (n >= N) continue;
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        const int m = m0 + wm * WTM + 32 * i + 8 * (r / 4) + 4 * h + r % 4;
+        if (m < M) out[(int64_t)m * N + n] = acc[i][j][r];
+      }
+  }
+}
+
+template <int NT>
+hipError_t skinny(const Mx4Plan& p, const uint8_t* w, const uint8_t* wsc, const uint8_t* a,
+                  const uint8_t* asc, float* dst, int M, int N, int K, hipStream_t s) {
+  if (M > 16 * NT) return hipErrorInvalidValue;       // the plan gives it no more rows
+  hipLaunchKernelGGL((k_mx4_skinny<NT>), dim3((unsigned)p.grid_n), dim3(64 * p.waves), p.lds, s, w,
+                     wsc, a, asc, M, N, K, dst);
+  return hipGetLastError();
+}
+
+template <int ROUNDS>
+hipError_t fused(const Mx4Plan& p, const float* x, const uint8_t* w, const uint8_t* wsc, float* dst,
+                 int M, int N, int K, hipStream_t s) {
+  hipLaunchKernelGGL((k_mx4_fused<ROUNDS>), dim3((unsigned)p.grid_n), dim3(512), p.lds, s, x, w, wsc,
+                     dst, M, N, K, (N + 15) / 16);
+  return hipGetLastError();
+}
+
+template <int BM, int BN, int WAVES_M, int WAVES_N, int STAGES>
+hipError_t wide(const Mx4Plan& p, const uint8_t* w, const uint8_t* wsc, const uint8_t* a,
+                const uint8_t* asc, float* dst, int M, int N, int K, void* ws, hipStream_t s) {
+  constexpr int kLds = STAGES * (BN + BM) * (kStageK / 2 + 8);
+  auto* const kern = k_mx4_wide<BM, BN, WAVES_M, WAVES_N, STAGES>;
+  if (kLds > 65536) {
+    static std::atomic<uint64_t> raised{0};          // devices whose limit is set already
+    const hipError_t e = raise_lds(reinterpret_cast<const void*>(kern), kLds, raised);
+    if (e != hipSuccess) return e;
+  }
+  float* const out = p.split > 1 ? reinterpret_cast<float*>((uint8_t*)ws + p.off_part) : dst;
+  hipLaunchKernelGGL(kern, dim3((unsigned)(p.tiles_m * p.tiles_n * p.split)),
+                     dim3(64 * WAVES_M * WAVES_N), kLds, s, w, wsc, a, asc, M, N, K, out,
+                     (int)p.tiles_m, (int)(p.tiles_m * p.tiles_n), p.split, (int)p.kchunk);
+  hipError_t e = hipGetLastError();
+  if (e == hipSuccess && p.split > 1) e = launch_join_slices(out, dst, (int64_t)M * N, p.split, s);
+  return e;
+}
+
+}  // namespace
+
+hipError_t launch_mx4_quantize(const float* x, uint8_t* codes, uint8_t* scales, int64_t nrows,
+                               int64_t k, hipStream_t s) {
+  const int64_t ng = (k + kGrp - 1) / kGrp, groups = nrows * ng, grid = (groups + 15) / 16;
+  hipLaunchKernelGGL(k_mx4_quantize, dim3((unsigned)(grid < kMaxGridX ? grid : kMaxGridX)), dim3(256),
+                     0, s, x, codes, reinterpret_cast<uint32_t*>(scales), (int)k, (int)ng, groups);
+  return hipGetLastError();
+}
+
+hipError_t launch_mx4_dequantize(const uint8_t* codes, const uint8_t* scales, float* y, int64_t nrows,
+                                 int64_t k, hipStream_t s) {
+  const int64_t ng = (k + kGrp - 1) / kGrp, pieces = nrows * (k / 8), grid = (pieces + 255) / 256;
+  hipLaunchKernelGGL(k_mx4_dequantize, dim3((unsigned)(grid < kMaxGridX ? grid : kMaxGridX)), dim3(256),
+                     0, s, codes, scales, y, (int)k, (int)ng, pieces);
+  return hipGetLastError();
+}
+
+hipError_t launch_mx4_product(const Mx4Plan& p, const uint8_t* w, const uint8_t* wsc, const float* x,
+                              const uint8_t* a, const uint8_t* asc, float* dst, int M, int N, int K,
+                              void* ws, hipStream_t s) {
+  if (p.kind == MX4_FUSED) {
+    if (p.nt == 1) return fused<1>(p, x, w, wsc, dst, M, N, K, s);
+    if (p.nt == 2) return fused<2>(p, x, w, wsc, dst, M, N, K, s);
+    if (p.nt == 4) return fused<4>(p, x, w, wsc, dst, M, N, K, s);
+    if (p.nt == 8) return fused<8>(p, x, w, wsc, dst, M, N, K, s);
+    return hipErrorInvalidValue;
+  }
+  if (x) {                                            // INIT
+    uint8_t* const codes = (uint8_t*)ws + p.off_a;
+    uint8_t* const scales = (uint8_t*)ws + p.off_as;
+    const hipError_t e = launch_mx4_quantize(x, codes, scales, M, K, s);
+    if (e != hipSuccess) return e;
+    a = codes;
+    asc = scales;
+  }
+  if (p.kind == MX4_SKINNY) {
+    if (p.nt == 1) return skinny<1>(p, w, wsc, a, asc, dst, M, N, K, s);
+    if (p.nt == 2) return skinny<2>(p, w, wsc, a, asc, dst, M, N, K, s);
+    return hipErrorInvalidValue;
+  }
+  if (p.bm == 256 && p.bn == 256) return wide<256, 256, 2, 2, 2>(p, w, wsc, a, asc, dst, M, N, K, ws, s);
+  if (p.bm == 128 && p.bn == 256) return wide<128, 256, 2, 2, 3>(p, w, wsc, a, asc, dst, M, N, K, ws, s);
+  if (p.bm == 128 && p.bn == 128) return wide<128, 128, 2, 2, 4>(p, w, wsc, a, asc, dst, M, N, K, ws, s);
+  if (p.bm == 64 && p.bn == 128) return wide<64, 128, 1, 2, 4>(p, w, wsc, a, asc, dst, M, N, K, ws, s);
+  return hipErrorInvalidValue;
+}
+
+}  // namespace qsg

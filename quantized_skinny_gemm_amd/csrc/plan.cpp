@@ -37,6 +37,7 @@ int64_t row_bytes(int type, int64_t K) {
     case MM_TYPE_Q4_0: return (K % kQK) ? -1 : K / kQK * kQ4Bytes;
     case MM_TYPE_Q8_0: return (K % kQK) ? -1 : K / kQK * kQ8Bytes;
     case MM_TYPE_F8: return (K % kQK || K > kF8MaxK) ? -1 : K;
+    case MM_TYPE_MXFP4: return (K % kQK || K > kF8MaxK) ? -1 : K / 2;
     case MM_TYPE_Q4_0R: return -1;                 // tiled, not row-major (repacked_bytes)
     default: return -1;
   }

@@ -34,6 +34,7 @@ constexpr int64_t kMaxGridY = 65535; // documented limit of a grid's y dimension
 constexpr int64_t kMaxGridX = 1 << 20; // workgroups of the grid-stride F8 quantizer
 constexpr int kF8Block = 128;      // values per scale of the e4m3 type, along K and (weights) N
 constexpr int64_t kF8MaxK = 1 << 23;   // F8 kernels: 32-bit byte offsets over a tile's rows
+constexpr int kMx4Group = 128;     // values per dword of scale bytes of the MXFP4 type (four blocks of 32)
 constexpr int kMoeMaxTokens = 128;     // mixture-of-experts layer: tokens per call,
 constexpr int kMoeMaxExperts = 512;    // experts,
 constexpr int kMoeMaxTopK = 16;        // experts per token,
@@ -153,6 +154,34 @@ int validate_f8(const void* src0, const void* scale0, const void* src1, const vo
 int validate_f8_quantize(const void* x, const void* codes, const void* scales, int64_t nrows,
                          int64_t k, int block_rows);
 
+// Plan of the product with MXFP4 weights (mx4.hip).
+enum Mx4Kind { MX4_NONE = 0, MX4_ZERO = 1, MX4_FUSED = 2, MX4_SKINNY = 3, MX4_WIDE = 4 };
+
+struct Mx4Plan {
+  int kind = MX4_NONE;
+  int nt = 1;                  // skinny: tiles of 16 src1 rows; fused: rounds of the
+                               // quantization (32 groups of 128 each)
+  int waves = 8;               // skinny: waves per workgroup (they split K)
+  int64_t grid_n = 1;          // skinny, fused: workgroups
+  size_t lds = 0;              // skinny, fused: LDS bytes
+  int bm = 0, bn = 0;          // wide: output tile (src1 rows, weight rows)
+  int64_t tiles_m = 1, tiles_n = 1, kchunk = 0;   // wide: stages of 256 k per split
+  int split = 1;
+  size_t off_a = 0, off_as = 0, off_part = 0;     // workspace: src1 codes, scales, partials
+  size_t ws_bytes = 0;
+};
+
+// given: src1 comes as codes and scales (no INIT).
+int make_mx4_plan(int64_t M, int64_t N, int64_t K, bool given, Mx4Plan* p);
+
+int validate_mx4(const void* src0, const void* scale0, const void* src1, const void* scale1,
+                 const void* dst, int64_t M, int64_t N, int64_t K, bool given, const void* ws,
+                 size_t ws_bytes, const Mx4Plan& p);
+
+// Quantizer (values -> codes, scales) and its inverse: the same checks.
+int validate_mx4_quantize(const void* x, const void* codes, const void* scales, int64_t nrows,
+                          int64_t k);
+
 // Plan of the mixture-of-experts layer (moe.hip).
 constexpr int kMoeFewTokens = 4;      // up to this many tokens: kernels for passes of 4
 constexpr int kMoeMaxLds = 150528;     // dynamic LDS of the down kernel (160 KB less its static part)
@@ -164,7 +193,17 @@ struct MoePlan {
   size_t off_part = 0;
   size_t ws_bytes = 0;
 };
-int make_moe_plan(int type, int64_t T, int64_t D, int64_t F, int64_t E, int64_t top_k, MoePlan* p);
+// routed: the choice of experts is an input (no logits, no selection).
+int make_moe_plan(int type, int64_t T, int64_t D, int64_t F, int64_t E, int64_t top_k, MoePlan* p,
+                  bool routed = false);
+
+// The norm (norm.hip) and the routing (route.hip).
+constexpr int64_t kNormMaxDim = kF8MaxK;         // 32-bit offsets within a row
+constexpr int64_t kRouteMaxTokens = 1 << 25;     // 64 threads each: below 2^32
+constexpr int kRouteMaxExperts = 512;
+constexpr int kRouteMaxTopK = 64;                // a lane each
+// Waves per row and rows per workgroup of the norm.
+void norm_shape(int64_t T, int64_t D, int* waves, int* rows);
 
 // Bytes of N x K Q4_0 weights in the repacked layout (repack.hip): tiles of
 // 16 rows x phases of 8 blocks, padded; -1 for an invalid shape.
