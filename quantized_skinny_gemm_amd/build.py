@@ -35,15 +35,18 @@ HIPCC_FLAGS = [
     f"--offload-arch={ARCH}", "-O3", "-fPIC", "-std=c++17",
     # packed fp32 VALU ops stay disabled (no v_pk_*_f32 in any kernel)
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
-    # MFMA results in ordinary VGPRs: the scale epilogues read every output
-    # register, and an accumulation-register result costs one extra move each
-    "-mllvm", "-amdgpu-mfma-vgpr-form",
     # the leading kernel arguments (up to 14 dwords) arrive in scalar
     # registers at wave launch instead of through a load from the kernel
     # argument segment: a wave can address its first loads at once
     "-mllvm", "-amdgpu-kernarg-preload-count=14",
     "-Wno-unused-command-line-argument",
 ]
+# MFMA results in ordinary VGPRs: the scale epilogues read every output
+# register, and an accumulation-register result costs one extra move each.
+# (Not for the MXFP4 products, which accumulate in the instruction: their sums
+# may live in accumulation registers at no cost.)
+VGPR_FORM = ["-mllvm", "-amdgpu-mfma-vgpr-form"]
+VGPR_FORM_NOT = ("mx4.hip",)
 CXX_FLAGS = ["-O2", "-fPIC", "-std=c++17", "-Wall"]
 
 
@@ -69,7 +72,8 @@ def build(verbose: bool = False) -> str:
     for src in HIP_SOURCES:
         obj = os.path.join(BUILD, src + ".o")
         objs.append(obj)
-        jobs.append([hipcc, *HIPCC_FLAGS, "-c", os.path.join(CSRC, src), "-o", obj])
+        form = [] if src in VGPR_FORM_NOT else VGPR_FORM
+        jobs.append([hipcc, *HIPCC_FLAGS, *form, "-c", os.path.join(CSRC, src), "-o", obj])
     for src in CXX_SOURCES:
         obj = os.path.join(BUILD, src + ".o")
         objs.append(obj)
@@ -84,7 +88,7 @@ def build(verbose: bool = False) -> str:
     os.replace(tmp, LIB)
     if os.path.exists(BENCH_SRC):
         tmp = BENCH_LIB + ".tmp"
-        _run([hipcc, *HIPCC_FLAGS, "-shared", BENCH_SRC, "-o", tmp])
+        _run([hipcc, *HIPCC_FLAGS, *VGPR_FORM, "-shared", BENCH_SRC, "-o", tmp])
         os.replace(tmp, BENCH_LIB)
     return LIB
 

@@ -29,6 +29,14 @@ typedef int v8i __attribute__((ext_vector_type(8)));
 
 constexpr int kGrp = kMx4Group;         // 128: four blocks, one dword of scale bytes
 
+// Sums that are complete here: the compiler may move a scaled matrix instruction
+// down to its result's first use, into a branch that leaves out lanes whose operands
+// it needs.
+template <class T>
+__device__ __forceinline__ void settle(T& sums) {
+  asm volatile("" : "+v"(sums));
+}
+
 __device__ __forceinline__ v8i operand(const uint4& c) {
   return (v8i){(int)c.x, (int)c.y, (int)c.z, (int)c.w, 0, 0, 0, 0};
 }
@@ -89,40 +97,51 @@ __global__ __launch_bounds__(256) void k_mx4_dequantize(const uint8_t* __restric
 
 // ---------------------------------------------------------------- product, few src1 rows
 
-// A lane's block (k = 128 kb + 32 g) of a row, and its scale byte; a block past K
-// is zeros with scale 1 (what is stored there is not read).
-struct Block {
-  uint4 c;
-  int s;
+// A unit is 4 groups of 128 k of a row: lane group g holds block g of each, and the
+// row's 16 scale bytes (one load: an access of a few bytes per row costs the address
+// units as much as one of 64).
+constexpr int kUnit = 4;
+typedef uint32_t v4u __attribute__((ext_vector_type(4), aligned(4)));
+struct Unit {
+  uint4 c[kUnit];
+  v4u s;
 };
-__device__ __forceinline__ Block load_block(const uint8_t* __restrict__ codes,
-                                            const uint8_t* __restrict__ scales, int kb, int g, int K) {
-  Block b;
-  const int k = kb * kGrp + 32 * g;
-  if ((kb + 1) * kGrp <= K) {                         // uniform: a whole group
-    b.c = *reinterpret_cast<const uint4*>(codes + k / 2);
-    b.s = scales[k / 32];
+
+// Groups kb0 .. kb0 + 3 of a row; those past its end repeat the last one, blocks
+// past K are zeros (what is stored there is not read).
+__device__ __forceinline__ Unit load_unit(const uint8_t* __restrict__ codes,
+                                          const uint8_t* __restrict__ scales, int kb0, int g, int K, int ng) {
+  Unit r;
+  const uint32_t* const sc = reinterpret_cast<const uint32_t*>(scales);
+  if ((kb0 + kUnit) * kGrp <= K) {                    // uniform: a whole unit
+#pragma unroll
+    for (int u = 0; u < kUnit; ++u)
+      r.c[u] = *reinterpret_cast<const uint4*>(codes + (kb0 + u) * (kGrp / 2) + 16 * g);
+    r.s = *reinterpret_cast<const v4u*>(sc + kb0);
   } else {
-    b.c = make_uint4(0, 0, 0, 0);
-    b.s = 127;
-    if (k < K) {
-      b.c = *reinterpret_cast<const uint4*>(codes + k / 2);
-      b.s = scales[k / 32];
+#pragma unroll
+    for (int u = 0; u < kUnit; ++u) {
+      const int kb = min(kb0 + u, ng - 1), k = kb * kGrp + 32 * g;
+      r.c[u] = make_uint4(0, 0, 0, 0);
+      r.s[u] = 0x7f7f7f7fu;
+      if (k < K) {
+        r.c[u] = *reinterpret_cast<const uint4*>(codes + k / 2);
+        r.s[u] = sc[kb];
+      }
     }
   }
-  return b;
+  return r;
 }
 
 // Each workgroup takes 16 weight rows and all src1 rows, at most NT tiles of 16;
-// its waves take runs of U groups of 128 k in turn (a wave's loads cover 64 U
-// consecutive bytes of each row); the waves' partial tiles are added in LDS in
+// its waves take units of 4 groups in turn (a wave's loads cover 256 consecutive
+// bytes of each row); the waves' partial tiles are added in LDS in
 // wave order.
 template <int NT>
 __global__ __launch_bounds__(512) void k_mx4_skinny(
     const uint8_t* __restrict__ w, const uint8_t* __restrict__ wsc, const uint8_t* __restrict__ a,
     const uint8_t* __restrict__ asc, int M, int N, int K, float* __restrict__ dst) {
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
-  constexpr int U = 4;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int W = blockDim.x >> 6;
   const int g = lane >> 4, i16 = lane & 15;
@@ -146,32 +165,32 @@ __global__ __launch_bounds__(512) void k_mx4_skinny(
 #pragma unroll
   for (int t = 0; t < NT; ++t) acc[t] = (v4f){0.f, 0.f, 0.f, 0.f};
 
-  for (int kb0 = wave * U; kb0 < ng; kb0 += W * U) {
-    Block wb[U], ab[U][NT];
+  for (int kb0 = wave * kUnit; kb0 < ng; kb0 += W * kUnit) {
+    Unit ab[NT];
+    const Unit wb = load_unit(wrow, wsr, kb0, g, K, ng);
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int kb = min(kb0 + u, ng - 1);            // valid addresses throughout
-      wb[u] = load_block(wrow, wsr, kb, g, K);
+    for (int t = 0; t < NT; ++t) {
+      ab[t].s = (v4u){0x7f7f7f7fu, 0x7f7f7f7fu, 0x7f7f7f7fu, 0x7f7f7f7fu};
 #pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        ab[u][t].c = make_uint4(0, 0, 0, 0);
-        ab[u][t].s = 127;
-        if (live[t]) ab[u][t] = load_block(arow[t], asr[t], kb, g, K);
-      }
+      for (int u = 0; u < kUnit; ++u) ab[t].c[u] = make_uint4(0, 0, 0, 0);
+      if (live[t]) ab[t] = load_unit(arow[t], asr[t], kb0, g, K, ng);
     }
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
+    for (int u = 0; u < kUnit; ++u) {
       if (kb0 + u >= ng) continue;                    // uniform
 #pragma unroll
       for (int t = 0; t < NT; ++t)
         acc[t] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-            operand(ab[u][t].c), operand(wb[u].c), acc[t], 4, 4, 0, ab[u][t].s, 0, wb[u].s);
+            operand(ab[t].c[u]), operand(wb.c[u]), acc[t], 4, 4, 0, (int)(ab[t].s[u] >> (8 * g)), 0,
+            (int)(wb.s[u] >> (8 * g)));
     }
   }
 
   // join the waves' partial tiles: [wave][m][n], n fastest
   float* const part = reinterpret_cast<float*>(lds);
   constexpr int TILE = 256 * NT;
+#pragma unroll
+  for (int t = 0; t < NT; ++t) settle(acc[t]);
 #pragma unroll
   for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -196,7 +215,7 @@ __global__ __launch_bounds__(512) void k_mx4_fused(
     const float* __restrict__ x, const uint8_t* __restrict__ w, const uint8_t* __restrict__ wsc,
     float* __restrict__ dst, int M, int N, int K, int tiles) {
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
-  constexpr int U = 4, W = 8;
+  constexpr int U = kUnit, W = 8;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int g = lane >> 4, i16 = lane & 15;
   const int ng = (K + kGrp - 1) / kGrp, pitch = ng * (kGrp / 2) + 16;   // 16: rows in different banks
@@ -217,15 +236,12 @@ __global__ __launch_bounds__(512) void k_mx4_fused(
       p[r] = s[0]; q[r] = s[1];
     }
   }
-  struct Round { Block b[U]; };
-  const auto load = [&](Round& r, int tile, int kb0) {
+  const auto load = [&](Unit& r, int tile, int kb0) {
     const int64_t row = min(16 * tile + i16, N - 1);
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-      r.b[u] = load_block(w + row * (K / 2), wsc + row * 4 * ng, min(kb0 + wave * U + u, ng - 1), g, K);
+    r = load_unit(w + row * (K / 2), wsc + row * 4 * ng, min(kb0 + wave * U, ng - 1), g, K, ng);
   };
   int tile = blockIdx.x, kb0 = 0;
-  Round cur;
+  Unit cur;
   load(cur, tile, 0);
   __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
@@ -245,7 +261,7 @@ __global__ __launch_bounds__(512) void k_mx4_fused(
   while (tile < tiles) {
     const bool last = kb0 + W * U >= ng;
     const int ntile = last ? tile + (int)gridDim.x : tile, nkb0 = last ? 0 : kb0 + W * U;
-    Round next;
+    Unit next;
     if (ntile < tiles) load(next, ntile, nkb0);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -258,9 +274,10 @@ __global__ __launch_bounds__(512) void k_mx4_fused(
         s = sscale[i16 * ng + kb];
       }
       acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-          operand(c), operand(cur.b[u].c), acc, 4, 4, 0, (int)(s >> (8 * g)), 0, cur.b[u].s);
+          operand(c), operand(cur.c[u]), acc, 4, 4, 0, (int)(s >> (8 * g)), 0, (int)(cur.s[u] >> (8 * g)));
     }
     if (last) {
+      settle(acc);
 #pragma unroll
       for (int e = 0; e < 4; ++e)
         if (4 * g + e < M) part[(wave * M + 4 * g + e) * 16 + i16] = acc[e];
@@ -293,15 +310,26 @@ __global__ __launch_bounds__(512) void k_mx4_fused(
 // start, and the next stage has arrived.
 //
 // In LDS a row's eight 16-byte chunks are permuted by (row / 2) % 8, so that the
-// rows of an operand read lie in different banks; scales are [dword][row].
+// rows of an operand read lie in different banks.  Scales are copied for two stages
+// at a time (an epoch), 16 bytes of a row by four lanes, half of the rows with every
+// stage.  A copy keeps the address units busy for about 2.2 cycles per line of 128
+// bytes that it touches (1 KB of whole lines 18 cycles; measured on resident data),
+// so 4 bytes per row and copy cost as much as all the codes.  (Four stages at a
+// time: no faster on large grids and slower on small ones, whose first stage waits
+// for more copies: 64 x 4096 x 4096 7.5 us against 6.8.)
 //
 // Where K ends inside the last stage, copies past a row's end take its first
-// codes and its last scales instead; src1's codes are then replaced by zeros and
-// all scales by 1 in registers.
+// codes and its last scales instead; src1's codes there are replaced by zeros and
+// all scales by 1 in registers (in a set's last stage, or last two of KW = 2, whose
+// second set may end a stage further).
 constexpr int kStageK = 256;
 
-template <int BM, int BN, int WAVES_M, int WAVES_N, int STAGES>
-__global__ __launch_bounds__(64 * WAVES_M * WAVES_N, 1) void k_mx4_wide(
+//
+// KW = 2: two such sets of waves share the workgroup, each with half of the stages
+// and LDS of its own; the second one's sums are added through LDS at the end (small
+// grids, where a split over workgroups would need a second launch to join it).
+template <int BM, int BN, int WAVES_M, int WAVES_N, int STAGES, int KW>
+__global__ __launch_bounds__(64 * WAVES_M * WAVES_N * KW, 1) void k_mx4_wide(
     const uint8_t* __restrict__ w, const uint8_t* __restrict__ wsc, const uint8_t* __restrict__ a,
     const uint8_t* __restrict__ asc, int M, int N, int K, float* __restrict__ dst, int tiles_m,
     int tiles, int split, int kchunk) {
@@ -309,26 +337,33 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N, 1) void k_mx4_wide(
   constexpr int WTM = BM / WAVES_M, WTN = BN / WAVES_N;
   constexpr int TM = WTM / 32, TN = WTN / 32;
   constexpr int kRow = kStageK / 2;                            // 128 bytes
-  constexpr int kA = BN * kRow, kWS = kA + BM * kRow, kAS = kWS + BN * 8;
-  constexpr int STAGE = kAS + BM * 8;
+  constexpr int kA = BN * kRow, STAGE = kA + BM * kRow;
+  // scales: buffers of [weight rows, src1 rows][16 bytes] behind the stages
+  constexpr int kScales = STAGES * STAGE, SBUF = (BM + BN) * 16, NB = STAGES;
   constexpr int WL = BN / 8 / NW, AL = BM / 8 / NW;            // pieces of 8 rows, 1 KB, per wave
-  constexpr int SL = (BM + BN) / 32 / NW;                      // pieces of 64 rows' scale dwords
+  constexpr int SP = (BM + BN) / 32;                           // pieces of 16 rows' scales in a half,
+  constexpr int SL = (SP + NW - 1) / NW;                       // per wave (some copied twice, alike)
   constexpr int kCopies = WL + AL + SL;
-  static_assert((STAGES - 1) * kCopies < 64, "wait counts");
-  static_assert(BN % (8 * NW) == 0 && BM % (8 * NW) == 0 && BM % 64 == 0 && BN % 64 == 0 &&
-                    (BM + BN) % (32 * NW) == 0, "whole pieces");
-  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+  static_assert(STAGES >= 2 && STAGES <= 4 && (STAGES - 1) * kCopies < 64, "wait counts");
+  static_assert(BN % (8 * NW) == 0 && BM % (8 * NW) == 0 && BM % 32 == 0 && BN % 32 == 0,
+                "whole pieces");
+  extern __shared__ __attribute__((aligned(16))) uint8_t shared[];
+  constexpr int kSet = kScales + NB * SBUF;                    // LDS of a set of waves
+  static_assert(KW == 1 || (KW == 2 && BM * BN * 4 <= kSet), "the second set's sums lie in the first one's LDS");
 
-  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int tid = threadIdx.x, lane = tid & 63, wave_id = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int kw = wave_id / NW, wave = wave_id % NW;
   const int wm = wave % WAVES_M, wn = wave / WAVES_M;
+  uint8_t* const lds = shared + kw * kSet;
   const int h = lane >> 5, l32 = lane & 31;
   const int ng = (K + kGrp - 1) / kGrp, nst = (K + kStageK - 1) / kStageK;
   const int t = xcd_remap(blockIdx.x, tiles * split);
   const int z = t / tiles, tt = t - z * tiles;
   const int tm = tt % tiles_m, tn = tt / tiles_m;    // m fastest: same weight tile adjacent
   const int m0 = tm * BM, n0 = tn * BN;
-  const int st0 = z * kchunk, s1 = min(st0 + kchunk, nst) - st0;   // first stage, stages
-  const int ragged = K % kStageK ? nst - 1 - st0 : -1;         // the stage that K ends in
+  // this set's first stage and stages (the second set's last one may lie past `end`)
+  const int last = min(z * kchunk + kchunk, nst), end = min(last * kStageK, K);
+  const int s1 = (last - z * kchunk + KW - 1) / KW, st0 = z * kchunk + kw * s1;
 
   // this lane's part of each piece
   const uint8_t* const wbase = w + (int64_t)n0 * (K / 2);
@@ -342,21 +377,36 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N, 1) void k_mx4_wide(
 #pragma unroll
   for (int i = 0; i < (WL > AL ? WL : AL); ++i)      // (row / 2) % 8 of row 8 (i NW + wave) + lane / 8
     chunk[i] = (lane & 7) ^ ((4 * ((i * NW + wave) & 1) + (lane >> 4)) & 7);
-  // scale pieces: dword p % 2 of 64 rows, weights first
-  const uint8_t* sbase[SL];
-  uint32_t soff[SL], sdst[SL];
-  int sdw[SL];
+  const uint8_t* const wscale = wsc + (int64_t)n0 * 4 * ng;
+  const uint8_t* const ascale = asc + (int64_t)m0 * 4 * ng;
+  const uint32_t lds0 = lds_offset(lds);
+  // this lane's row in each half's pieces (the second one as the bits that differ: a
+  // choice between two arrays would be kept in scratch memory)
+  uint32_t soff[SL], sdiff[SL];
+  const auto scale_row = [&](int i, int half) {
+    const int r = 16 * ((i * NW + wave) % SP + half * SP);
+    const bool isw = r < BN;                         // BN % 16 == 0
+    return (uint32_t)min((isw ? r : r - BN) + (lane >> 2), isw ? N - 1 - n0 : M - 1 - m0) * (uint32_t)ng;
+  };
 #pragma unroll
   for (int i = 0; i < SL; ++i) {
-    const int p = i * NW + wave;
-    const bool isw = p < BN / 32;
-    const int pp = isw ? p : p - BN / 32, r = (pp >> 1) * 64;
-    sdw[i] = pp & 1;
-    sbase[i] = isw ? wsc + (int64_t)n0 * 4 * ng : asc + (int64_t)m0 * 4 * ng;
-    soff[i] = (uint32_t)min(r + lane, (isw ? N - 1 - n0 : M - 1 - m0)) * (uint32_t)ng;
-    sdst[i] = (uint32_t)((isw ? kWS + sdw[i] * BN * 4 : kAS + sdw[i] * BM * 4) + 4 * r);
+    soff[i] = scale_row(i, 0);
+    sdiff[i] = soff[i] ^ scale_row(i, 1);
   }
-  const uint32_t lds0 = lds_offset(lds);
+  // Half u % 2 of the rows' scales of epoch u / 2.  With one of them ahead of all, and
+  // u = s + 1 beside the codes of stage s, an epoch is whole when its first stage is.
+  // Buffers: half 0 of epoch e is copied at stage 2 e - STAGES - 1, after its barrier;
+  // epoch e - STAGES was last read in stage 2 (e - STAGES), which lies before.
+  const auto copy_scales = [&](int u) {
+    const int epoch = u >> 1, half = u & 1;
+    const uint32_t dword = (uint32_t)min(2 * st0 + 4 * epoch + (lane & 3), ng - 1);
+    const uint32_t base = lds0 + kScales + (uint32_t)(epoch % NB) * SBUF;
+#pragma unroll
+    for (int i = 0; i < SL; ++i) {
+      const int r = 16 * ((i * NW + wave) % SP + half * SP);
+      copy4(base + 16 * r, r < BN ? wscale : ascale, 4 * ((soff[i] ^ (sdiff[i] & -(uint32_t)half)) + dword));
+    }
+  };
   const auto copy_stage = [&](int s, int buf) {
     const uint32_t base = lds0 + buf * STAGE;
     const int kb = (st0 + s) * kRow;                 // bytes
@@ -370,9 +420,7 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N, 1) void k_mx4_wide(
       const int at = kb + 16 * chunk[i];
       copy16(base + kA + (i * NW + wave) * 1024, abase, aoff[i] + (at < K / 2 ? at : 0));
     }
-#pragma unroll
-    for (int i = 0; i < SL; ++i)
-      copy4(base + sdst[i], sbase[i], 4 * (soff[i] + (uint32_t)min(2 * (st0 + s) + sdw[i], ng - 1)));
+    copy_scales(s + 1);                              // and 0 ahead of all
   };
 
   v16f acc[TM][TN];
@@ -395,31 +443,37 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N, 1) void k_mx4_wide(
       wr[q % 2][j] = *reinterpret_cast<const uint4*>(base + wrow + 32 * j * kRow + 16 * ((4 * h + q) ^ x8));
   };
   uint32_t ws[TN], as[TM];
-  const auto read_scales = [&](const uint8_t* base) {
+  const auto read_scales = [&](int s) {
+    const uint8_t* const p = lds + kScales + (s >> 1) % NB * SBUF + 8 * (s & 1) + 4 * h;
 #pragma unroll
     for (int i = 0; i < TM; ++i)
-      as[i] = *reinterpret_cast<const uint32_t*>(base + kAS + 4 * (h * BM + wm * WTM + 32 * i + l32));
+      as[i] = *reinterpret_cast<const uint32_t*>(p + 16 * (BN + wm * WTM + 32 * i + l32));
 #pragma unroll
     for (int j = 0; j < TN; ++j)
-      ws[j] = *reinterpret_cast<const uint32_t*>(base + kWS + 4 * (h * BN + wn * WTN + 32 * j + l32));
+      ws[j] = *reinterpret_cast<const uint32_t*>(p + 16 * (wn * WTN + 32 * j + l32));
   };
 
+  copy_scales(0);
 #pragma unroll
   for (int s = 0; s < STAGES; ++s)
     if (s < s1) copy_stage(s, s);
-  if (s1 >= STAGES) wait_copies<(STAGES - 1) * kCopies>();
+  if (s1 >= STAGES) wait_copies<(STAGES - 1) * kCopies>();   // s1 >= 1
   else wait_copies<0>();
   __builtin_amdgcn_s_barrier();
   read(lds, 0);
-  read_scales(lds);
+  read_scales(0);
 
+  // One stage.  kLeft: stages left with this one (STAGES + 1: more than are in
+  // LDS, so the one STAGES further is copied).  No branches in here: the compiler
+  // would move the products behind them, past the wait.
   int buf = 0;
-  for (int s = 0; s < s1; ++s) {
+  const auto stage = [&](auto left, int s) {
+    constexpr int kLeft = decltype(left)::value;
     const uint8_t* const base = lds + buf * STAGE;
     const int next = buf + 1 == STAGES ? 0 : buf + 1;
-    if (s == ragged) {                               // uniform; bytes of blocks past K: scale 1
-      const int left = (K - (st0 + s) * kStageK - kGrp * h) / 32;      // this half's blocks inside K
-      const uint32_t keep = left >= 4 ? ~0u : left <= 0 ? 0u : (1u << (8 * left)) - 1;
+    const int inside = end - (st0 + s) * kStageK - kGrp * h;   // this half's k before `end`
+    if constexpr (kLeft <= KW) {                     // bytes of blocks past `end`: scale 1
+      const uint32_t keep = inside >= kGrp ? ~0u : inside <= 0 ? 0u : (1u << (inside / 4)) - 1;
 #pragma unroll
       for (int i = 0; i < TM; ++i) as[i] = (as[i] & keep) | (0x7f7f7f7fu & ~keep);
 #pragma unroll
@@ -434,20 +488,22 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N, 1) void k_mx4_wide(
       for (int j = 0; j < TN; ++j) wsq[j] = ws[j];
       if constexpr (q < 3) {
         read(base, q + 1);
-      } else {
+      } else if constexpr (kLeft > 1) {
         // the next stage is here and this wave's reads of this one are done
-        if (s + STAGES - 1 < s1) wait_copies<(STAGES - 2) * kCopies>();
-        else wait_copies<0>();
+        wait_copies<(kLeft > STAGES ? STAGES - 2 : kLeft - 2) * kCopies>();
         __builtin_amdgcn_s_barrier();
-        if (s + STAGES < s1) copy_stage(s + STAGES, buf);
+        if constexpr (kLeft > STAGES) copy_stage(s + STAGES, buf);
         read(lds + next * STAGE, 0);
-        read_scales(lds + next * STAGE);
+        read_scales(s + 1);
       }
       __builtin_amdgcn_sched_barrier(0);             // the reads stay ahead of the products
-      if (s == ragged) {                             // uniform
-        if ((st0 + s) * kStageK + kGrp * h + 32 * q >= K)
+      if constexpr (kLeft <= KW) {                   // blocks past `end`: zeros
 #pragma unroll
-          for (int i = 0; i < TM; ++i) ar[q % 2][i] = make_uint4(0, 0, 0, 0);
+        for (int i = 0; i < TM; ++i) {
+          uint4& v = ar[q % 2][i];
+          v = make_uint4(32 * q < inside ? v.x : 0, 32 * q < inside ? v.y : 0, 32 * q < inside ? v.z : 0,
+                         32 * q < inside ? v.w : 0);
+        }
       }
 #pragma unroll
       for (int i = 0; i < TM; ++i)
@@ -455,12 +511,53 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N, 1) void k_mx4_wide(
         for (int j = 0; j < TN; ++j)
           acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
               operand(ar[q % 2][i]), operand(wr[q % 2][j]), acc[i][j], 4, 4, q, (int)asq[i], q, (int)wsq[j]);
+      __builtin_amdgcn_sched_barrier(0);
     };
     step(std::integral_constant<int, 0>());
     step(std::integral_constant<int, 1>());
     step(std::integral_constant<int, 2>());
     step(std::integral_constant<int, 3>());
     buf = next;
+  };
+  int s = 0;
+  for (; s + STAGES < s1; ++s) stage(std::integral_constant<int, STAGES + 1>(), s);
+  if constexpr (STAGES >= 4)
+    if (s + 4 == s1) stage(std::integral_constant<int, 4>(), s++);
+  if constexpr (STAGES >= 3)
+    if (s + 3 == s1) stage(std::integral_constant<int, 3>(), s++);
+  if (s + 2 == s1) stage(std::integral_constant<int, 2>(), s++);
+  stage(std::integral_constant<int, 1>(), s);
+
+#pragma unroll
+  for (int i = 0; i < TM; ++i)
+#pragma unroll
+    for (int j = 0; j < TN; ++j) settle(acc[i][j]);
+  if constexpr (KW == 2) {
+    // the second set's sums, 16 bytes per lane: [tile][r / 4][lane]
+    __syncthreads();                                 // all reads of the stages are done
+    float4* const sums = reinterpret_cast<float4*>(shared) + wave * (TM * TN * 4 * 64) + lane;
+    if (kw == 1) {
+#pragma unroll
+      for (int i = 0; i < TM; ++i)
+#pragma unroll
+        for (int j = 0; j < TN; ++j)
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            sums[((i * TN + j) * 4 + r) * 64] = make_float4(acc[i][j][4 * r], acc[i][j][4 * r + 1],
+                                                            acc[i][j][4 * r + 2], acc[i][j][4 * r + 3]);
+    }
+    __syncthreads();
+    if (kw == 1) return;
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+      for (int j = 0; j < TN; ++j)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const float4 v = sums[((i * TN + j) * 4 + r) * 64];
+          acc[i][j][4 * r] += v.x; acc[i][j][4 * r + 1] += v.y;
+          acc[i][j][4 * r + 2] += v.z; acc[i][j][4 * r + 3] += v.w;
+        }
   }
 
   // lane: weight row of column l32, src1 rows 8 (r / 4) + 4 h + r % 4
@@ -496,11 +593,12 @@ hipError_t fused(const Mx4Plan& p, const float* x, const uint8_t* w, const uint8
   return hipGetLastError();
 }
 
-template <int BM, int BN, int WAVES_M, int WAVES_N, int STAGES>
+template <int BM, int BN, int WAVES_M, int WAVES_N, int STAGES, int KW = 1>
 hipError_t wide(const Mx4Plan& p, const uint8_t* w, const uint8_t* wsc, const uint8_t* a,
                 const uint8_t* asc, float* dst, int M, int N, int K, void* ws, hipStream_t s) {
-  constexpr int kLds = STAGES * (BN + BM) * (kStageK / 2 + 8);
-  auto* const kern = k_mx4_wide<BM, BN, WAVES_M, WAVES_N, STAGES>;
+  constexpr int kLds = KW * STAGES * (BN + BM) * (kStageK / 2 + 16);
+  static_assert(kLds <= 160 * 1024, "LDS of a CU");
+  auto* const kern = k_mx4_wide<BM, BN, WAVES_M, WAVES_N, STAGES, KW>;
   if (kLds > 65536) {
     static std::atomic<uint64_t> raised{0};          // devices whose limit is set already
     const hipError_t e = raise_lds(reinterpret_cast<const void*>(kern), kLds, raised);
@@ -508,7 +606,7 @@ hipError_t wide(const Mx4Plan& p, const uint8_t* w, const uint8_t* wsc, const ui
   }
   float* const out = p.split > 1 ? reinterpret_cast<float*>((uint8_t*)ws + p.off_part) : dst;
   hipLaunchKernelGGL(kern, dim3((unsigned)(p.tiles_m * p.tiles_n * p.split)),
-                     dim3(64 * WAVES_M * WAVES_N), kLds, s, w, wsc, a, asc, M, N, K, out,
+                     dim3(64 * WAVES_M * WAVES_N * KW), kLds, s, w, wsc, a, asc, M, N, K, out,
                      (int)p.tiles_m, (int)(p.tiles_m * p.tiles_n), p.split, (int)p.kchunk);
   hipError_t e = hipGetLastError();
   if (e == hipSuccess && p.split > 1) e = launch_join_slices(out, dst, (int64_t)M * N, p.split, s);
@@ -556,10 +654,13 @@ hipError_t launch_mx4_product(const Mx4Plan& p, const uint8_t* w, const uint8_t*
     if (p.nt == 2) return skinny<2>(p, w, wsc, a, asc, dst, M, N, K, s);
     return hipErrorInvalidValue;
   }
-  if (p.bm == 256 && p.bn == 256) return wide<256, 256, 2, 2, 2>(p, w, wsc, a, asc, dst, M, N, K, ws, s);
-  if (p.bm == 128 && p.bn == 256) return wide<128, 256, 2, 2, 3>(p, w, wsc, a, asc, dst, M, N, K, ws, s);
-  if (p.bm == 128 && p.bn == 128) return wide<128, 128, 2, 2, 4>(p, w, wsc, a, asc, dst, M, N, K, ws, s);
-  if (p.bm == 64 && p.bn == 128) return wide<64, 128, 1, 2, 4>(p, w, wsc, a, asc, dst, M, N, K, ws, s);
+  if (p.bm == 32 && p.bn == 32) return wide<32, 32, 1, 1, 4, 2>(p, w, wsc, a, asc, dst, M, N, K, ws, s);
+  if (p.bm == 64 && p.bn == 64) return wide<64, 64, 2, 2, 3>(p, w, wsc, a, asc, dst, M, N, K, ws, s);
+  if (p.bm == 64 && p.bn == 128) return wide<64, 128, 2, 4, 3>(p, w, wsc, a, asc, dst, M, N, K, ws, s);
+  if (p.bm == 128 && p.bn == 64) return wide<128, 64, 4, 2, 3>(p, w, wsc, a, asc, dst, M, N, K, ws, s);
+  if (p.bm == 128 && p.bn == 128) return wide<128, 128, 4, 2, 3>(p, w, wsc, a, asc, dst, M, N, K, ws, s);
+  if (p.bm == 256 && p.bn == 128) return wide<256, 128, 4, 2, 2>(p, w, wsc, a, asc, dst, M, N, K, ws, s);
+  if (p.bm == 256 && p.bn == 256) return wide<256, 256, 2, 4, 2>(p, w, wsc, a, asc, dst, M, N, K, ws, s);
   return hipErrorInvalidValue;
 }
 

@@ -32,11 +32,17 @@ int make_mx4_plan(int64_t M, int64_t N, int64_t K, bool given, Mx4Plan* p) {
   if (M == 0 || N == 0) return MM_OK;
   if (K == 0) { p->kind = MX4_ZERO; return MM_OK; }
   const int64_t ng = ceil_div(K, kMx4Group), tiles16 = ceil_div(N, 16);
-  if (!given && M <= 16 && M * ng <= 256) {
+
+  // Up to 8 rounds of 32 groups of 128: every workgroup quantizes src1 itself, in
+  // less time than an INIT launch takes (us per call, fused / INIT and product: 4096 x
+  // 4096, M = 1, 4, 8 4.3 / 6.8, 5.1 / 7.0, 6.3 / 7.2; 14336 x 4096, M = 8 11.7 / 11.3).
+  const int64_t groups = M * ng;
+  if (!given && M <= 16 && groups <= 256) {
     p->kind = MX4_FUSED;
-    const int64_t groups = M * ng;
     p->nt = groups <= 32 ? 1 : groups <= 64 ? 2 : groups <= 128 ? 4 : 8;
-    const int64_t most = 3 * kCUs;
+    // workgroups, each walking tiles of 16 weight rows (14336 x 4096, 256 / 512 / 768
+    // workgroups: M = 1 9.1 / 7.9 / 8.6 us, M = 4 10.1 / 10.9 / 11.0, M = 8 11.7 / 12.8 / 14.9)
+    const int64_t most = M <= 2 ? 2 * kCUs : kCUs;
     p->grid_n = tiles16 < most ? tiles16 : most;
     p->lds = (size_t)(M * (ng * kMx4Group / 2 + 16)) + align_up((size_t)groups * 4, 16) + (size_t)M * 512;
     return MM_OK;
@@ -46,37 +52,54 @@ int make_mx4_plan(int64_t M, int64_t N, int64_t K, bool given, Mx4Plan* p) {
     p->off_a = off; off = align_up(off + (size_t)M * (size_t)(K / 2), 256);
     p->off_as = off; off = align_up(off + scale_bytes(M, K), 256);
   }
-  if (M <= 32) {
+  // Few src1 rows on few weight rows: 16 weight rows per workgroup fill the device
+  // sooner than the tiled kernel's 32 or 64 (us, skinny / tiled: 4096 x 4096, M = 16
+  // 4.9 / 5.1, M = 32 6.2 / 5.0; 1000 x 4128, M = 32 4.4 / 5.4; 14336 x 4096, M = 4, 16
+  // 9.3 / 8.0, 11.8 / 8.0; 4096 x 14336, M = 16, 32 10.2 / 13.1, 14.9 / 13.1).
+  if ((M <= 16 && tiles16 <= 2 * kCUs) || (M <= 32 && tiles16 <= kCUs / 2)) {
     p->kind = MX4_SKINNY;
     p->nt = M <= 16 ? 1 : 2;
     p->waves = 8;
-    while (p->waves > 1 && (p->waves - 1) * 4 >= ng) p->waves /= 2;
+    while (p->waves > 1 && (p->waves / 2) * 4 >= ng) p->waves /= 2;
     p->grid_n = tiles16;
-    if (p->grid_n * p->waves > kMaxTiles * 8) return MM_ERR_SHAPE;
     p->lds = (size_t)p->waves * 1024 * p->nt;
-  } else {
-    p->kind = MX4_WIDE;
-    const bool low = M <= 64;
-    p->bm = low ? 64 : M <= 128 ? 128 : 128;
-    p->bn = low ? 128 : M <= 256 ? 128 : 256;
-    if (M > 256 && N > 16384) p->bm = 256;
-    p->tiles_m = ceil_div(M, p->bm);
-    p->tiles_n = ceil_div(N, p->bn);
-    const int64_t tiles = p->tiles_m * p->tiles_n, nst = ceil_div(K, 256);
-    if (tiles > kMaxTiles) return MM_ERR_SHAPE;
-    int64_t split = 1;
-    if (tiles < kCUs) {
-      split = kCUs / tiles;
-      if (split > nst / 4) split = nst / 4;
-      if (split > 16) split = 16;
-      if (split < 1) split = 1;
+    p->ws_bytes = off;
+    return MM_OK;
+  }
+  // Tiled: the tile, and the split of K over workgroups (with a second launch to join
+  // it), of the least time by what a workgroup of each takes per stage of 256 k where
+  // it has a CU to itself (hundredths of a us, from calls of at most 256 workgroups at
+  // K = 4096 less 2 us: 5.1, 6.9, 9.0, 9.0, 12.1, 18.3 and 28.5 us).  256 workgroups
+  // run at a time; those that share a CU take as long as one after the other.  Against
+  // the best of all tiles, measured: 64 x 14336 x 4096 9.7 us (64 x 64) of 9.7, 128 x
+  // 14336 x 4096 13.0 (128 x 64) of 13.0, 256 x 14336 x 4096 16.7 (128 x 128) of 16.7,
+  // 512 x 14336 x 4096 28.9 (256 x 128) of 28.9, 256 x 4096 x 4096 7.6 (64 x 64) of 7.6,
+  // 512 x 4096 x 4096 10.4 (128 x 64) of 10.4, 256 x 20000 x 1024 10.0 (256 x 128) of 9.6,
+  // 512 x 2000 x 1024 4.3 (64 x 64) of 4.3.
+  static const struct { int bm, bn, cost; } kTiles[] = {
+      {32, 32, 19}, {64, 64, 31}, {64, 128, 44}, {128, 64, 44}, {128, 128, 63}, {256, 128, 102}, {256, 256, 166}};
+  const int64_t nst = ceil_div(K, 256);
+  int64_t best = -1;
+  p->kind = MX4_WIDE;
+  for (const auto& t : kTiles) {
+    const int64_t tm = ceil_div(M, t.bm), tn = ceil_div(N, t.bn);
+    if (tm > kMaxTiles || tm * tn > kMaxTiles) continue;
+    for (int64_t split = 1; split <= 16; split *= 2) {
+      // a split: at least 4 stages each, no second round, about 6 us for the join
+      if (split > 1 && (nst < 4 * split || tm * tn * split > kCUs)) break;
+      const int64_t time = ceil_div(tm * tn * split, kCUs) * ceil_div(nst, split) * t.cost + (split > 1 ? 600 : 0);
+      if (best >= 0 && time >= best) continue;
+      best = time;
+      p->bm = t.bm; p->bn = t.bn;
+      p->tiles_m = tm; p->tiles_n = tn;
+      p->kchunk = ceil_div(nst, split);
+      p->split = (int)ceil_div(nst, p->kchunk);
     }
-    p->kchunk = ceil_div(nst, split);
-    p->split = (int)ceil_div(nst, p->kchunk);
-    if (p->split > 1) {
-      p->off_part = off;
-      off = align_up(off + (size_t)p->split * (size_t)M * (size_t)N * 4, 256);
-    }
+  }
+  if (best < 0) return MM_ERR_SHAPE;
+  if (p->split > 1) {
+    p->off_part = off;
+    off = align_up(off + (size_t)p->split * (size_t)M * (size_t)N * 4, 256);
   }
   p->ws_bytes = off;
   return MM_OK;
