@@ -308,12 +308,13 @@ def _public_stream(dev: int) -> int:
 
 # the same handle without a Stream object (a microsecond less); not in every build of torch
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _public_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 _F8_DTYPES = (torch.float8_e4m3fn, torch.uint8)
 
 
 def _launch(fn, what: str, dev: int, *args) -> None:
     """fn(*args, current stream of device dev), with dev current during the call."""
-    if dev == torch.cuda.current_device():
+    if dev == _current_device():
         status = fn(*args, _raw_stream(dev))
     else:
         with torch.cuda.device(dev):
@@ -324,6 +325,8 @@ def _launch(fn, what: str, dev: int, *args) -> None:
 
 def _on(t, name: str, shape, dtypes, dev: int) -> None:
     """t is a contiguous GPU tensor of this shape, one of dtypes, on device dev."""
+    if type(t) is torch.Tensor and t.dtype in dtypes and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+        return
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a GPU (HIP) tensor")
     if t.dtype not in dtypes:
@@ -334,6 +337,11 @@ def _on(t, name: str, shape, dtypes, dev: int) -> None:
         raise ValueError(f"{name} must be contiguous")
     if t.get_device() != dev:
         raise ValueError(f"{name} is on {t.device}, expected cuda:{dev}")
+
+
+def _new(rows: int, cols: int, dtype, device):
+    """An uninitialised tensor [rows, cols] (torch.empty takes half a microsecond longer)."""
+    return torch.empty_strided((rows, cols), (cols, 1), dtype=dtype, device=device)
 
 
 _F32 = (torch.float32,)
@@ -351,8 +359,8 @@ def quantize_f8(x: torch.Tensor, block_rows: int = 1, out=None):
     nb = rows if block_rows == 1 else _ceil128(rows)
     dev = x.get_device()
     if out is None:
-        codes = torch.empty((rows, k), dtype=torch.float8_e4m3fn, device=x.device)
-        scales = torch.empty((nb, _ceil128(k)), dtype=torch.float32, device=x.device)
+        codes = _new(rows, k, torch.float8_e4m3fn, x.device)
+        scales = _new(nb, _ceil128(k), torch.float32, x.device)
     else:
         codes, scales = out
         _on(codes, "out codes", (rows, k), _F8_DTYPES, dev)
@@ -379,7 +387,7 @@ def _f8_weights(w, w_scale, k: int, dev: int) -> int:
 def _buffers(m, n, device, dev, out, need, ws):
     """out (allocated if None, checked otherwise) and the workspace with its size."""
     if out is None:
-        out = torch.empty((m, n), dtype=torch.float32, device=device)
+        out = _new(m, n, torch.float32, device)
     else:
         _on(out, "out", (m, n), _F32, dev)
     if need == 0:
@@ -431,8 +439,8 @@ def quantize_mxfp4(x: torch.Tensor, out=None):
     rows, k = x.shape
     dev = x.get_device()
     if out is None:
-        codes = torch.empty((rows, k // 2), dtype=torch.uint8, device=x.device)
-        scales = torch.empty((rows, 4 * _ceil128(k)), dtype=torch.uint8, device=x.device)
+        codes = _new(rows, k // 2, torch.uint8, x.device)
+        scales = _new(rows, 4 * _ceil128(k), torch.uint8, x.device)
     else:
         codes, scales = out
         _on(codes, "out codes", (rows, k // 2), _MX_CODES, dev)
@@ -458,7 +466,7 @@ def dequantize_mxfp4(codes: torch.Tensor, scales: torch.Tensor, out: torch.Tenso
     dev = codes.get_device()
     rows, k = _mx_pair(codes, scales, "codes", dev)
     if out is None:
-        out = torch.empty((rows, k), dtype=torch.float32, device=codes.device)
+        out = _new(rows, k, torch.float32, codes.device)
     else:
         _on(out, "out", (rows, k), _F32, dev)
     _launch(lib.mm_dequantize_mxfp4, "mm_dequantize_mxfp4", dev, codes.data_ptr(), scales.data_ptr(), out.data_ptr(),
@@ -515,11 +523,11 @@ def rms_norm_f32(x: torch.Tensor, weight=None, eps: float = 1e-5, residual=None,
         if v is not None:
             _on(v, name, shape, _F32, dev)
     if sum_out is None and residual is not None:
-        sum_out = torch.empty((t, d), dtype=torch.float32, device=x.device)
+        sum_out = _new(t, d, torch.float32, x.device)
     scales = None
     if out_type == MM_TYPE_F32:
         if out is None:
-            out = torch.empty((t, d), dtype=torch.float32, device=x.device)
+            out = _new(t, d, torch.float32, x.device)
         else:
             _on(out, "out", (t, d), _F32, dev)
         y, got = out, out
@@ -529,8 +537,8 @@ def rms_norm_f32(x: torch.Tensor, weight=None, eps: float = 1e-5, residual=None,
             raise ValueError("out_type must be MM_TYPE_F32, MM_TYPE_F8 or MM_TYPE_MXFP4")
         shape, sshape = ((t, d), (t, _ceil128(d))) if f8 else ((t, d // 2), (t, 4 * _ceil128(d)))
         if out is None:
-            y = torch.empty(shape, dtype=torch.float8_e4m3fn if f8 else torch.uint8, device=x.device)
-            scales = torch.empty(sshape, dtype=torch.float32 if f8 else torch.uint8, device=x.device)
+            y = _new(*shape, torch.float8_e4m3fn if f8 else torch.uint8, x.device)
+            scales = _new(*sshape, torch.float32 if f8 else torch.uint8, x.device)
         else:
             y, scales = out
             _on(y, "out codes", shape, _F8_DTYPES if f8 else _MX_CODES, dev)
@@ -562,7 +570,7 @@ class Router:
             raise ValueError("score must be 'softmax' or 'sigmoid'")
         self.e, self.top_k, self.bias = int(e), int(top_k), bias
         if bias is not None:
-            _on(bias, "bias", (self.e,), _F32, bias.get_device() if isinstance(bias, torch.Tensor) else 0)
+            _on(_dev(bias, "bias"), "bias", (self.e,), _F32, bias.get_device())
         self.struct = _RouterStruct(_SCORES[score], self.top_k, int(bool(norm)), int(groups), int(group_k),
                                     int(group_top), self.e, float(scale), None)
         self._ref = ctypes.byref(self.struct)
@@ -581,11 +589,11 @@ def route_f32(router: Router, logits: torch.Tensor, ids=None, weights=None):
     t, dev, k = logits.shape[0], logits.get_device(), router.top_k
     _on(logits, "logits", (t, router.e), _F32, dev)
     if ids is None:
-        ids = torch.empty((t, k), dtype=torch.int32, device=logits.device)
+        ids = _new(t, k, torch.int32, logits.device)
     else:
         _on(ids, "ids", (t, k), _I32, dev)
     if weights is None:
-        weights = torch.empty((t, k), dtype=torch.float32, device=logits.device)
+        weights = _new(t, k, torch.float32, logits.device)
     else:
         _on(weights, "weights", (t, k), _F32, dev)
     _launch(lib.mm_route_f32, "mm_route_f32", dev, router._take(dev), logits.data_ptr(), ids.data_ptr(),
@@ -696,11 +704,11 @@ def moe_f32(layer: MoeLayer, x: torch.Tensor, out=None, ids=None, weights=None, 
     dev, k = layer.dev, layer.top_k
     _on(x, "x", (t, layer.d), _F32, dev)
     if ids is None:
-        ids = torch.empty((t, k), dtype=torch.int32, device=layer.device)
+        ids = _new(t, k, torch.int32, layer.device)
     else:
         _on(ids, "ids", (t, k), _I32, dev)
     if weights is None:
-        weights = torch.empty((t, k), dtype=torch.float32, device=layer.device)
+        weights = _new(t, k, torch.float32, layer.device)
     else:
         _on(weights, "weights", (t, k), _F32, dev)
     out, ws, nbytes = _buffers(t, layer.d, layer.device, dev, out, layer.workspace_size(t), ws)
