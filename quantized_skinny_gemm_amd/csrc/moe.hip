@@ -51,6 +51,8 @@
 //   16-byte access per lane, since neighbouring lanes belong to different rows:
 //   the address units were 67% busy and the gate / up launch at 2.9 TB/s (32
 //   tokens, 8 experts of 4096 x 14336).
+#include <type_traits>
+
 #include "device.h"
 #include "kernels.h"
 #include "../../include/mm.h"
@@ -62,6 +64,7 @@ namespace {
 typedef float v4f __attribute__((ext_vector_type(4)));
 typedef _Float16 v2h __attribute__((ext_vector_type(2)));
 typedef uint32_t v2u __attribute__((ext_vector_type(2)));
+typedef uint32_t v2ua __attribute__((ext_vector_type(2), aligned(4)));
 typedef uint32_t v4u __attribute__((ext_vector_type(4)));
 
 // ---------------------------------------------------------------- activations
@@ -286,6 +289,7 @@ struct Tile;
 template <>
 struct Tile<MM_TYPE_Q4_0R> {
   static constexpr int kLds = 0;
+  static constexpr int kPair = 1;
   const uint8_t* base;
   v4u c;                         // whole vectors, so that they stay in the registers that
   v2u d;                         // the loads fill
@@ -298,7 +302,7 @@ struct Tile<MM_TYPE_Q4_0R> {
   __device__ __forceinline__ void fetch(const uint8_t*, int) {
     asm volatile("" : "+v"(c), "+v"(d));
   }
-  __device__ __forceinline__ void load(int u, int, int lane, uint32_t) {
+  __device__ __forceinline__ void load(int u, int, int lane, uint32_t, bool) {
     const uint8_t* p = base + (int64_t)(u >> 1) * kQ4RChunk;
     c = *reinterpret_cast<const v4u*>(p + 1024 * (u & 1));
     d = *reinterpret_cast<const v2u*>(p - 16 * lane + 2048 + 16 * (lane & 15) + 8 * (u & 1));
@@ -327,6 +331,7 @@ struct Tile<MM_TYPE_Q4_0R> {
 template <>
 struct Tile<MM_TYPE_F8> {
   static constexpr int kLds = 2048;
+  static constexpr int kPair = 1;
   const uint8_t* base;           // uniform
   const float* sc;
   uint32_t off[2];               // the rows this lane copies
@@ -344,7 +349,7 @@ struct Tile<MM_TYPE_F8> {
     for (int q = 0; q < 2; ++q) off[q] = (uint32_t)(8 * q + (lane >> 3)) * (uint32_t)k;
     chunk = lane & 7;
   }
-  __device__ __forceinline__ void load(int u, int, int lane, uint32_t lds) {
+  __device__ __forceinline__ void load(int u, int, int lane, uint32_t lds, bool) {
     dnext = sc[u];
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
@@ -369,41 +374,82 @@ struct Tile<MM_TYPE_F8> {
   __device__ __forceinline__ float scale(int) const { return d; }
 };
 
-// MXFP4 goes through LDS too (16 rows of 64 bytes, a unit's four blocks of 16
-// bytes permuted by (row / 4) % 4): a lane's operand is 4 bytes of its row's block.
-// Its four scale bytes are one dword of its row.
-template <>
-struct Tile<MM_TYPE_MXFP4> {
-  static constexpr int kLds = 1024;
+// MXFP4 goes through LDS too, kPair units of neighbours at a time: with two, 16 rows
+// of whole 128-byte lines (a copy of 64 bytes per row takes the address units as
+// long): the even unit's load copies both, or the first one's where a wave begins
+// with the odd one (fresh).  The 16-byte blocks of a row are permuted by its index,
+// so that a column of blocks lies in all banks; a lane's operand is 4 bytes of its
+// row's block.  A unit's four scale bytes are one dword of the row.  (Loads straight
+// into registers, transposed there: 272 us against 261 with one unit and 237 with
+// two, 32 tokens on 8 experts of 4096 x 14336.)
+//
+// One unit at a time for few tokens, whose workgroups then share a CU (gate / up of 4
+// tokens, 16 experts of 2048 x 2048: 19 us against 22).
+constexpr int kMxfp4Few = 100;
+template <int kUnits>
+struct MxTile {
+  static constexpr int kLds = 1024 * kUnits;
+  static constexpr int kPair = kUnits;
   const uint8_t* base;           // uniform
   const uint32_t* sc;
-  uint32_t off;                  // the row and block this lane copies
-  int last, nb;
-  uint32_t c[4];
-  uint32_t d, dnext, keep;
+  uint32_t off[kUnits];          // the rows this lane copies
+  int last, nb, unit;
+  uint32_t c[4], dw[4];
+  std::conditional_t<kUnits == 2, v2u, uint32_t> dnext;
+  // where block b of row r lies among the row's 4 kUnits
+  static __device__ __forceinline__ int place(int b, int r) {
+    return kUnits == 2 ? b ^ ((r >> 1) & 7) : b ^ ((r >> 2) & 3);
+  }
   __device__ __forceinline__ void bind(const uint8_t* w, const void* s, int64_t e, int N, int k,
                                        int row0, int lane) {
     nb = k / 32;
     last = k / 2 - 16;
     base = w + (e * N + row0) * (k / 2);
     sc = (const uint32_t*)s + (e * N + row0 + (lane & 15)) * ((k + 127) / 128);
-    off = (uint32_t)(lane >> 2) * (uint32_t)(k / 2);
+#pragma unroll
+    for (int q = 0; q < kUnits; ++q)
+      off[q] = (uint32_t)((16 * q + lane / 4) / kUnits) * (uint32_t)(k / 2);
   }
-  __device__ __forceinline__ void load(int u, int, int lane, uint32_t lds) {
-    dnext = sc[u];
-    // blocks past K: the last one again, with scale 1 (they meet activations of scale 0)
-    const int left = nb - 4 * u;
-    keep = left >= 4 ? ~0u : (1u << (8 * left)) - 1;
-    const int at = 64 * u + 16 * ((lane & 3) ^ ((lane >> 4) & 3));
-    copy16(lds, base, off + (uint32_t)min(at, last));
+  __device__ __forceinline__ void load(int u, int, int lane, uint32_t lds, bool fresh) {
+    unit = u;
+    const int u0 = u & -kUnits;
+    if (u != u0 && !fresh) return;                   // uniform
+    if constexpr (kUnits == 2) {
+      if (4 * (u0 + 1) < nb) dnext = *reinterpret_cast<const v2ua*>(sc + u0);
+      else dnext.x = sc[u0];
+    } else {
+      dnext = sc[u0];
+    }
+#pragma unroll
+    for (int q = 0; q < kUnits; ++q) {
+      // blocks past K: the last one again
+      const int at = 64 * u0 + 16 * place(lane & (4 * kUnits - 1), (16 * q + lane / 4) / kUnits);
+      copy16(lds + 1024 * q, base, off[q] + (uint32_t)min(at, last));
+    }
   }
   __device__ __forceinline__ void fetch(const uint8_t* lds, int lane) {
-    const int r = lane & 15, g = lane >> 4;
+    const int r = lane & 15, g = lane >> 4, half = unit & (kUnits - 1);
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-      c[j] = *reinterpret_cast<const uint32_t*>(lds + 64 * r + 16 * (j ^ ((r >> 2) & 3)) + 4 * g);
+      c[j] = *reinterpret_cast<const uint32_t*>(lds + 64 * kUnits * r + 16 * place(4 * half + j, r) + 4 * g);
     asm volatile("" : "+v"(dnext));
-    d = (dnext & keep) | (0x7f7f7f7fu & ~keep);
+    // blocks past K: scale 1 (they meet activations of scale 0)
+    const int left = nb - 4 * unit;
+    const uint32_t keep = left >= 4 ? ~0u : (1u << (8 * left)) - 1;
+    uint32_t d;
+    if constexpr (kUnits == 2) d = half ? dnext.y : dnext.x;
+    else d = dnext;
+    d = (d & keep) | (0x7f7f7f7fu & ~keep);
+    // 2^(byte - 127): the byte as an exponent, but for 0 (2^-127 is subnormal) and 255
+    // (NaN), which take the fraction's top bit
+#pragma unroll
+    for (int j = 0; j < 4; ++j) dw[j] = (j == 3 ? d >> 1 : d << (23 - 8 * j)) & 0x7f800000u;
+    const uint32_t zero = (d - 0x01010101u) & ~d, ones = (~d - 0x01010101u) & d;
+    if (__any(((zero | ones) & 0x80808080u) != 0)) { // rare
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (!((dw[j] + 0x00800000u) & 0x7f000000u)) dw[j] |= 0x00400000u;
+    }
   }
   __device__ __forceinline__ v8h operand(int j) const {
     const v2h a = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(c[j], 1.0f, 0);
@@ -412,17 +458,17 @@ struct Tile<MM_TYPE_MXFP4> {
     const v2h f = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(c[j], 1.0f, 3);
     return (v8h){a[0], a[1], b[0], b[1], e[0], e[1], f[0], f[1]};
   }
-  // 2^(byte - 127): the byte as an exponent, but for 0 (2^-127 is subnormal) and 255
-  // (NaN), which take the fraction's top bit
-  __device__ __forceinline__ float scale(int j) const {
-    const uint32_t x = ((d >> (8 * j)) & 255) << 23;
-    return __builtin_bit_cast(float, ((x + 0x00800000u) & 0x7f000000u) ? x : x | 0x00400000u);
-  }
+  __device__ __forceinline__ float scale(int j) const { return __builtin_bit_cast(float, dw[j]); }
 };
+template <>
+struct Tile<MM_TYPE_MXFP4> : MxTile<2> {};
+template <>
+struct Tile<kMxfp4Few> : MxTile<1> {};
 
 template <>
 struct Tile<MM_TYPE_F16> {
   static constexpr int kLds = 0;
+  static constexpr int kPair = 1;
   const uint8_t* base;
   uint4 c[4];
   __device__ __forceinline__ void bind(const uint8_t* w, const void*, int64_t e, int N, int K,
@@ -433,7 +479,7 @@ struct Tile<MM_TYPE_F16> {
 #pragma unroll
     for (int j = 0; j < 4; ++j) asm volatile("" : "+v"(c[j].x), "+v"(c[j].y), "+v"(c[j].z), "+v"(c[j].w));
   }
-  __device__ __forceinline__ void load(int u, int nb, int, uint32_t) {
+  __device__ __forceinline__ void load(int u, int nb, int, uint32_t, bool) {
 #pragma unroll
     for (int j = 0; j < 4; ++j)
       c[j] = *reinterpret_cast<const uint4*>(base + 64 * (int64_t)min(4 * u + j, nb - 1));
@@ -529,10 +575,10 @@ template <int TY, int NR, int RT>
 __device__ __forceinline__ void run_units(Acts<NR>& x, Tile<TY> (&w0)[RT], int u, int end, int n,
                                           int nb, float (&acc)[RT][NR], uint8_t* lds, int lane) {
   const uint32_t at = lds_offset(lds), tat = at + Acts<NR>::kLds;
-  const auto issue = [&](Tile<TY> (&w)[RT], int v) {
+  const auto issue = [&](Tile<TY> (&w)[RT], int v, bool fresh) {
     x.load(v, n, lane, at);
 #pragma unroll
-    for (int i = 0; i < RT; ++i) w[i].load(v, nb, lane, tat + i * Tile<TY>::kLds);
+    for (int i = 0; i < RT; ++i) w[i].load(v, nb, lane, tat + i * Tile<TY>::kLds, fresh);
   };
   const auto take = [&](Tile<TY> (&w)[RT]) {
     wait_copies<0>();
@@ -542,11 +588,11 @@ __device__ __forceinline__ void run_units(Acts<NR>& x, Tile<TY> (&w0)[RT], int u
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
   };
   if (u >= end) return;
-  issue(w0, u);
+  issue(w0, u, true);
   if constexpr (Tile<TY>::kLds > 0) {
     for (; u < end; ++u) {
       take(w0);
-      if (u + 1 < end) issue(w0, u + 1);
+      if (u + 1 < end) issue(w0, u + 1, false);
       unit_product<TY, NR, RT>(x, w0, acc);
     }
   } else {
@@ -555,11 +601,11 @@ __device__ __forceinline__ void run_units(Acts<NR>& x, Tile<TY> (&w0)[RT], int u
     for (int i = 0; i < RT; ++i) w1[i] = w0[i];
     for (; u < end; u += 2) {
       take(w0);
-      if (u + 1 < end) issue(w1, u + 1);
+      if (u + 1 < end) issue(w1, u + 1, false);
       unit_product<TY, NR, RT>(x, w0, acc);
       if (u + 1 >= end) break;
       take(w1);
-      if (u + 2 < end) issue(w0, u + 2);
+      if (u + 2 < end) issue(w0, u + 2, false);
       unit_product<TY, NR, RT>(x, w1, acc);
     }
   }
@@ -572,7 +618,7 @@ constexpr int kUpWaves = 8;
 // Partial sums kept apart in the join: one per wave, or one per pair of waves
 // (w, w + 4) where e4m3's staging leaves no room for eight.
 template <int TY, bool kFew>
-constexpr int up_parts() { return Tile<TY>::kLds > 1024 && !kFew ? kUpWaves / 2 : kUpWaves; }
+constexpr int up_parts() { return Tile<TY>::kLds > 0 && !kFew ? kUpWaves / 2 : kUpWaves; }
 
 // Dynamic LDS of the gate / up kernel: the waves' staging, then their partial
 // sums (before both, the logits where it makes the selection).
@@ -608,7 +654,7 @@ __device__ __forceinline__ void up_pass(const MoeArgs& a, int e, int rg0, int st
     for (int i = 0; i < 4; ++i) {
       w[i].bind(i < 2 ? a.gate : a.up, i < 2 ? a.gate_scale : a.up_scale, e, a.F, a.D,
                 32 * rg + 16 * (i & 1), lane);
-      w[i].load(u, nb, lane, tat + i * Tile<TY>::kLds);
+      w[i].load(u, nb, lane, tat + i * Tile<TY>::kLds, false);   // begins with an even unit
     }
   };
   const auto fetch = [&](Tile<TY> (&w)[4]) {
@@ -653,12 +699,14 @@ __device__ __forceinline__ void up_pass(const MoeArgs& a, int e, int rg0, int st
     }
     lds_barrier();                                   // the partial sums are read
   };
-  if (wave >= units) {                               // no units: only the joins
+  // a wave's units: kPair neighbours, then W of those further
+  constexpr int P2 = Tile<TY>::kPair;
+  if (P2 * wave >= units) {                          // no units: only the joins
     for (int rg = rg0; rg < nfb; rg += step) join(rg);
     return;
   }
   // one unit of row group rg; the next one's loads; the join after the last
-  int rg = rg0, u = wave;
+  int rg = rg0, u = P2 * wave;
   const auto issue = [&](Tile<TY> (&w)[4], int r, int v) {
     x.load(v, n, lane, at);
     issue_w(w, r, v);
@@ -666,8 +714,9 @@ __device__ __forceinline__ void up_pass(const MoeArgs& a, int e, int rg0, int st
   const auto body = [&](Tile<TY> (&w)[4], Tile<TY> (&next)[4]) {
     wait_copies<0>();
     fetch(w);
-    const bool last = u + W >= units;
-    const int nrg = last ? rg + step : rg, nu = last ? wave : u + W;
+    const int further = P2 == 2 && !(u & 1) ? u + 1 : u + P2 * (W - 1) + 1;
+    const bool last = further >= units;
+    const int nrg = last ? rg + step : rg, nu = last ? P2 * wave : further;
     if (nrg < nfb) issue(next, nrg, nu);
     unit_product<TY, NR, 4>(x, w, acc);
     if (last) join(rg);
@@ -694,7 +743,7 @@ __device__ __forceinline__ void up_pass(const MoeArgs& a, int e, int rg0, int st
 // workgroup ranks the logits itself (a launch less), and one writes ids and
 // weights for the next launch.
 template <int TY, bool kFew>
-__global__ __launch_bounds__(64 * kUpWaves, 2) void k_moe_up(MoeArgs a) {
+__global__ __launch_bounds__(64 * kUpWaves, TY == kMxfp4Few ? 4 : 2) void k_moe_up(MoeArgs a) {
   constexpr int W = kUpWaves, kRows = kFew ? 4 : 16;
   constexpr int kStage = Acts<kFew ? 1 : 4>::kLds + 4 * Tile<TY>::kLds;
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
@@ -991,11 +1040,13 @@ hipError_t run(const MoePlan& p, const MoeArgs& a, float* part, hipStream_t s) {
   const int assigned = a.T * a.top_k;
   const dim3 grid(a.up_groups + (a.fold ? 1 : 0), assigned < a.E ? assigned : a.E);
   const bool few = a.T <= kMoeFewTokens;
-  e = few ? up<TY, true>(grid, a, s) : up<TY, false>(grid, a, s);
+  constexpr int kFewType = TY == MM_TYPE_MXFP4 ? kMxfp4Few : TY;
+  e = few ? up<kFewType, true>(grid, a, s) : up<TY, false>(grid, a, s);
   if (e != hipSuccess) return e;
   float* const out = p.slices > 1 ? part : a.dst;
-  if (few) e = down<TY, 1, 16, true>(p, a, out, s);
-  else if (TY != MM_TYPE_F8 && p.rt == 4) e = down<TY, TY == MM_TYPE_F8 ? 1 : 4, 8, false>(p, a, out, s);
+  if (few) e = down<kFewType, 1, 16, true>(p, a, out, s);
+  else if (Tile<TY>::kLds == 0 && p.rt == 4) e = down<TY, Tile<TY>::kLds ? 1 : 4, 8, false>(p, a, out, s);
+  else if (p.rt == 2 && TY == MM_TYPE_MXFP4 && a.T > kMoeMxPairTokens) e = down<kFewType, 2, 8, false>(p, a, out, s);
   else if (p.rt == 2) e = down<TY, 2, 8, false>(p, a, out, s);
   else e = down<TY, 1, 8, false>(p, a, out, s);
   if (e == hipSuccess && p.slices > 1) e = launch_join_slices(part, a.dst, (int64_t)a.T * a.D, p.slices, s);

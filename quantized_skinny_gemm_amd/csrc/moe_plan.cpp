@@ -54,10 +54,13 @@ int make_moe_plan(int type, int64_t T, int64_t D, int64_t F, int64_t E, int64_t 
   const bool many = T * top_k > 2 * used;
   const bool few = T <= kMoeFewTokens;
   // (the per-wave sums of T tokens x 16 rt rows, 8 waves, share the LDS with
-  // the staging, which e4m3 and MXFP4 weights need too)
-  const bool f8 = type == MM_TYPE_F8;
-  const int64_t most4 = type == MM_TYPE_MXFP4 ? 24 : 32;
-  p->rt = few || !many ? 1 : !f8 && D % 64 == 0 && T <= most4 ? 4 : D % 32 == 0 && T <= (f8 ? 32 : 64) ? 2 : 1;
+  // the staging, which e4m3 and MXFP4 weights need too: MXFP4 two units of it up to
+  // kMoeMxPairTokens, one beyond)
+  const bool f8 = type == MM_TYPE_F8, mx = type == MM_TYPE_MXFP4;
+  p->rt = few || !many                           ? 1
+          : !f8 && !mx && D % 64 == 0 && T <= 32 ? 4
+          : D % 32 == 0 && T <= (f8 ? 32 : 64)   ? 2
+                                                 : 1;
   const int64_t tiles = D / (16 * p->rt), units = used * ((F / kQK + 3) / 4);
   int64_t slices = few ? 1 : p->rt > 1 ? (2 * kCUs + tiles - 1) / tiles : kCUs / tiles;
   if (slices > units / 64) slices = units / 64;

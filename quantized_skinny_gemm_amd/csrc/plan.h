@@ -184,6 +184,7 @@ int validate_mx4_quantize(const void* x, const void* codes, const void* scales, 
 
 // Plan of the mixture-of-experts layer (moe.hip).
 constexpr int kMoeFewTokens = 4;      // up to this many tokens: kernels for passes of 4
+constexpr int kMoeMxPairTokens = 48;   // down, MXFP4: two units of weights in LDS up to this many tokens
 constexpr int kMoeMaxLds = 150528;     // dynamic LDS of the down kernel (160 KB less its static part)
 struct MoePlan {
   bool fold = false;       // the selection is made by the gate / up launch
