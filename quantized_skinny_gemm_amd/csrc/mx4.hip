@@ -322,12 +322,12 @@ __global__ __launch_bounds__(512) void k_mx4_fused(
 // codes and its last scales instead; src1's codes there are replaced by zeros and
 // all scales by 1 in registers (in a set's last stage, or last two of KW = 2, whose
 // second set may end a stage further).
-constexpr int kStageK = 256;
-
 //
 // KW = 2: two such sets of waves share the workgroup, each with half of the stages
 // and LDS of its own; the second one's sums are added through LDS at the end (small
 // grids, where a split over workgroups would need a second launch to join it).
+constexpr int kStageK = 256;
+
 template <int BM, int BN, int WAVES_M, int WAVES_N, int STAGES, int KW>
 __global__ __launch_bounds__(64 * WAVES_M * WAVES_N * KW, 1) void k_mx4_wide(
     const uint8_t* __restrict__ w, const uint8_t* __restrict__ wsc, const uint8_t* __restrict__ a,
@@ -344,6 +344,17 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N * KW, 1) void k_mx4_wide(
   constexpr int SP = (BM + BN) / 32;                           // pieces of 16 rows' scales in a half,
   constexpr int SL = (SP + NW - 1) / NW;                       // per wave (some copied twice, alike)
   constexpr int kCopies = WL + AL + SL;
+  // A stage's pieces (the scales are the last one).  The largest tiles' go in two
+  // parts, kPart of them after the barrier that frees their buffer, the others in the
+  // next stage's first step: the address units work through all of them for longer
+  // than a step takes, and waves that wait to hand them over issue no products
+  // (512 x 128256 x 4096, tile 256 x 256: 183 us against 193; 512 x 14336 x 4096, tile
+  // 256 x 128: 25.9 against 29.8).  Smaller tiles copy less and lose 1 to 8 % by it.
+  constexpr int kPieces = WL + AL + 1, kPart = STAGES == 2 ? kPieces - 2 * (kPieces / 4) : kPieces;
+  constexpr int kPartCopies = kPart < kPieces ? kPart : kCopies;
+  constexpr std::integral_constant<int, 0> first{};
+  constexpr std::integral_constant<int, kPart> part{};
+  constexpr std::integral_constant<int, kPieces> whole_stage{};
   static_assert(STAGES >= 2 && STAGES <= 4 && (STAGES - 1) * kCopies < 64, "wait counts");
   static_assert(BN % (8 * NW) == 0 && BM % (8 * NW) == 0 && BM % 32 == 0 && BN % 32 == 0,
                 "whole pieces");
@@ -407,20 +418,19 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N * KW, 1) void k_mx4_wide(
       copy4(base + 16 * r, r < BN ? wscale : ascale, 4 * ((soff[i] ^ (sdiff[i] & -(uint32_t)half)) + dword));
     }
   };
-  const auto copy_stage = [&](int s, int buf) {
+  // pieces from .. to - 1 of a stage: weights, src1, then a set of scales
+  const auto copy_pieces = [&](auto from, auto to, int s, int buf) {
     const uint32_t base = lds0 + buf * STAGE;
     const int kb = (st0 + s) * kRow;                 // bytes
 #pragma unroll
-    for (int i = 0; i < WL; ++i) {
-      const int at = kb + 16 * chunk[i];
-      copy16(base + (i * NW + wave) * 1024, wbase, woff[i] + (at < K / 2 ? at : 0));
+    for (int i = 0; i < WL + AL; ++i) {
+      if (i < from || i >= to) continue;
+      const int c = i < WL ? i : i - WL, at = kb + 16 * chunk[c];
+      const uint32_t in = at < K / 2 ? at : 0;
+      if (i < WL) copy16(base + (c * NW + wave) * 1024, wbase, woff[i < WL ? i : 0] + in);
+      else copy16(base + kA + (c * NW + wave) * 1024, abase, aoff[i < WL ? 0 : c] + in);
     }
-#pragma unroll
-    for (int i = 0; i < AL; ++i) {
-      const int at = kb + 16 * chunk[i];
-      copy16(base + kA + (i * NW + wave) * 1024, abase, aoff[i] + (at < K / 2 ? at : 0));
-    }
-    copy_scales(s + 1);                              // and 0 ahead of all
+    if (from < kPieces && to == kPieces) copy_scales(s + 1);   // and 0 ahead of all
   };
 
   v16f acc[TM][TN];
@@ -455,9 +465,10 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N * KW, 1) void k_mx4_wide(
 
   copy_scales(0);
 #pragma unroll
-  for (int s = 0; s < STAGES; ++s)
-    if (s < s1) copy_stage(s, s);
-  if (s1 >= STAGES) wait_copies<(STAGES - 1) * kCopies>();   // s1 >= 1
+  for (int s = 0; s < STAGES - 1; ++s)
+    if (s < s1) copy_pieces(first, whole_stage, s, s);
+  if (STAGES - 1 < s1) copy_pieces(first, part, STAGES - 1, STAGES - 1);
+  if (s1 >= STAGES) wait_copies<(STAGES - 2) * kCopies + kPartCopies>();   // s1 >= 1
   else wait_copies<0>();
   __builtin_amdgcn_s_barrier();
   read(lds, 0);
@@ -488,11 +499,13 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N * KW, 1) void k_mx4_wide(
       for (int j = 0; j < TN; ++j) wsq[j] = ws[j];
       if constexpr (q < 3) {
         read(base, q + 1);
+        if constexpr (q == 0 && kLeft >= STAGES)
+          copy_pieces(part, whole_stage, s + STAGES - 1, buf == 0 ? STAGES - 1 : buf - 1);
       } else if constexpr (kLeft > 1) {
         // the next stage is here and this wave's reads of this one are done
         wait_copies<(kLeft > STAGES ? STAGES - 2 : kLeft - 2) * kCopies>();
         __builtin_amdgcn_s_barrier();
-        if constexpr (kLeft > STAGES) copy_stage(s + STAGES, buf);
+        if constexpr (kLeft > STAGES) copy_pieces(first, part, s + STAGES, buf);
         read(lds + next * STAGE, 0);
         read_scales(s + 1);
       }
@@ -561,19 +574,20 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N * KW, 1) void k_mx4_wide(
   }
 
   // lane: weight row of column l32, src1 rows 8 (r / 4) + 4 h + r % 4
-  float* const out = dst + (int64_t)z * M * N;
+  const int mm = m0 + wm * WTM, nn = n0 + wn * WTN;
+  float* const out = dst + (int64_t)z * M * N + (int64_t)mm * N + nn;
+  const int64_t lane_off = (int64_t)(4 * h) * N + l32;
+  const bool whole = mm + WTM <= M && nn + WTN <= N;             // uniform
 #pragma unroll
-  for (int j = 0; j < TN; ++j) {
-    const int n = n0 + wn * WTN + 32 * j + l32;
-    if (n >= N) continue;
+  for (int i = 0; i < TM; ++i)
 #pragma unroll
-    for (int i = 0; i < TM; ++i)
+    for (int j = 0; j < TN; ++j)
 #pragma unroll
       for (int r = 0; r < 16; ++r) {
-        const int m = m0 + wm * WTM + 32 * i + 8 * (r / 4) + 4 * h + r % 4;
-        if (m < M) out[(int64_t)m * N + n] = acc[i][j][r];
+        const int m = 32 * i + 8 * (r / 4) + r % 4;
+        if (whole || (mm + m + 4 * h < M && nn + 32 * j + l32 < N))
+          (out + (int64_t)m * N + 32 * j)[lane_off] = acc[i][j][r];
       }
-  }
 }
 
 template <int NT>

@@ -68,16 +68,18 @@ int make_mx4_plan(int64_t M, int64_t N, int64_t K, bool given, Mx4Plan* p) {
   }
   // Tiled: the tile, and the split of K over workgroups (with a second launch to join
   // it), of the least time by what a workgroup of each takes per stage of 256 k where
-  // it has a CU to itself (hundredths of a us, from calls of at most 256 workgroups at
-  // K = 4096 less 2 us: 5.1, 6.9, 9.0, 9.0, 12.1, 18.3 and 28.5 us).  256 workgroups
-  // run at a time; those that share a CU take as long as one after the other.  Against
-  // the best of all tiles, measured: 64 x 14336 x 4096 9.7 us (64 x 64) of 9.7, 128 x
-  // 14336 x 4096 13.0 (128 x 64) of 13.0, 256 x 14336 x 4096 16.7 (128 x 128) of 16.7,
-  // 512 x 14336 x 4096 28.9 (256 x 128) of 28.9, 256 x 4096 x 4096 7.6 (64 x 64) of 7.6,
-  // 512 x 4096 x 4096 10.4 (128 x 64) of 10.4, 256 x 20000 x 1024 10.0 (256 x 128) of 9.6,
-  // 512 x 2000 x 1024 4.3 (64 x 64) of 4.3.
+  // it has a CU to itself (hundredths of a us; fitted to calls of at most 256 workgroups
+  // at K = 4096, which take 5, 7 to 10, 9.6 to 14, 9.6 to 14, 12 to 17, 18 to 25 and 27
+  // to 34 us from few workgroups to 256).  256 workgroups run at a time; those that share
+  // a CU take as long as one after the other.  The tile chosen and the best of all, in us:
+  // 64 x 14336 x 4096 8.3 (64 x 64, the best), 128 x 14336 x 4096 11.3 (128 x 64, the best),
+  // 256 x 14336 x 4096 16.5 (128 x 128, the best; 64 x 64 25.3, 256 x 128 24.2), 512 x
+  // 14336 x 4096 25.5 (256 x 128, the best; 256 x 256 34.1, 128 x 128 34.2), 1024 x 14336 x
+  // 4096 39 (256 x 256, the best; 256 x 128 53), 2048 x 4096 x 14336 80 (256 x 128, the best;
+  // 256 x 256 94), 512 x 128256 x 4096 182 (256 x 256, the best; 256 x 128 222), 256 x
+  // 4096 x 4096 7.9 (64 x 64, the best), 512 x 4096 x 4096 10.9 (128 x 64; 64 x 128 10.8).
   static const struct { int bm, bn, cost; } kTiles[] = {
-      {32, 32, 19}, {64, 64, 31}, {64, 128, 44}, {128, 64, 44}, {128, 128, 63}, {256, 128, 102}, {256, 256, 166}};
+      {32, 32, 19}, {64, 64, 31}, {64, 128, 44}, {128, 64, 44}, {128, 128, 63}, {256, 128, 90}, {256, 256, 155}};
   const int64_t nst = ceil_div(K, 256);
   int64_t best = -1;
   p->kind = MX4_WIDE;
