@@ -69,17 +69,17 @@ int make_mx4_plan(int64_t M, int64_t N, int64_t K, bool given, Mx4Plan* p) {
   // Tiled: the tile, and the split of K over workgroups (with a second launch to join
   // it), of the least time by what a workgroup of each takes per stage of 256 k where
   // it has a CU to itself (hundredths of a us; fitted to calls of at most 256 workgroups
-  // at K = 4096, which take 5, 7 to 10, 9.6 to 14, 9.6 to 14, 12 to 17, 18 to 25 and 27
+  // at K = 4096, which take 5, 7 to 10, 9.6 to 14, 12 to 17, 18 to 25 and 27
   // to 34 us from few workgroups to 256).  256 workgroups run at a time; those that share
   // a CU take as long as one after the other.  The tile chosen and the best of all, in us:
-  // 64 x 14336 x 4096 8.3 (64 x 64, the best), 128 x 14336 x 4096 11.3 (128 x 64, the best),
+  // 64 x 14336 x 4096 8.3 (64 x 64, the best), 128 x 14336 x 4096 11.3 (64 x 128, the best),
   // 256 x 14336 x 4096 16.5 (128 x 128, the best; 64 x 64 25.3, 256 x 128 24.2), 512 x
   // 14336 x 4096 25.5 (256 x 128, the best; 256 x 256 34.1, 128 x 128 34.2), 1024 x 14336 x
   // 4096 39 (256 x 256, the best; 256 x 128 53), 2048 x 4096 x 14336 80 (256 x 128, the best;
   // 256 x 256 94), 512 x 128256 x 4096 182 (256 x 256, the best; 256 x 128 222), 256 x
-  // 4096 x 4096 7.9 (64 x 64, the best), 512 x 4096 x 4096 10.9 (128 x 64; 64 x 128 10.8).
+  // 4096 x 4096 7.9 (64 x 64, the best), 512 x 4096 x 4096 10.8 (64 x 128, the best).
   static const struct { int bm, bn, cost; } kTiles[] = {
-      {32, 32, 19}, {64, 64, 31}, {64, 128, 44}, {128, 64, 44}, {128, 128, 63}, {256, 128, 90}, {256, 256, 155}};
+      {32, 32, 19}, {64, 64, 31}, {64, 128, 44}, {128, 128, 63}, {256, 128, 90}, {256, 256, 155}};
   const int64_t nst = ceil_div(K, 256);
   int64_t best = -1;
   p->kind = MX4_WIDE;
@@ -87,9 +87,13 @@ int make_mx4_plan(int64_t M, int64_t N, int64_t K, bool given, Mx4Plan* p) {
     const int64_t tm = ceil_div(M, t.bm), tn = ceil_div(N, t.bn);
     if (tm > kMaxTiles || tm * tn > kMaxTiles) continue;
     for (int64_t split = 1; split <= 16; split *= 2) {
-      // a split: at least 4 stages each, no second round, about 6 us for the join
+      // a split: at least 4 stages each, no second round; the join takes about 7 us and
+      // what writing and reading the partial sums does (us, split / not: 64 x 4096 x 28672
+      // 15.7 / 20.6, 300 x 300 x 65536 15 / 40, 128 x 4096 x 14336 14.2 / 18.8, 33 x 512 x
+      // 14336 12.5 / 11.0; of the largest tile that fills the device 8 times, which a cost
+      // without the bytes takes: 1024 x 1024 x 8192 24 / 12, 384 x 4096 x 14336 34 / 26)
       if (split > 1 && (nst < 4 * split || tm * tn * split > kCUs)) break;
-      const int64_t time = ceil_div(tm * tn * split, kCUs) * ceil_div(nst, split) * t.cost + (split > 1 ? 600 : 0);
+      const int64_t time = ceil_div(tm * tn * split, kCUs) * ceil_div(nst, split) * t.cost + (split > 1 ? 700 + split * M * N / 6000 : 0);
       if (best >= 0 && time >= best) continue;
       best = time;
       p->bm = t.bm; p->bn = t.bn;

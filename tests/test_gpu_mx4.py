@@ -114,6 +114,9 @@ SHAPES = [
     (25, 1100, 4096), (300, 16500, 2080), (600, 4200, 1056), (1100, 4200, 160), (40, 33000, 160), (1, 16500, 160),
     (4, 8200, 1056), (16, 12300, 2048), (2, 16500, 2080), (512, 20000, 544), (257, 20000, 1024), (1, 3000, 7168),
     (31, 5000, 352), (48, 4096, 4096), (64, 14336, 1024), (128, 4096, 4096), (256, 4096, 2048), (40, 40, 7200),
+    # several stages of the largest tiles, the last one ragged; K split evenly and unevenly
+    (500, 14300, 1120), (1000, 14200, 800), (33, 70, 19936), (40, 30, 16384), (129, 300, 16416), (200, 300, 24608),
+    (300, 1001, 28672), (300, 2048, 28928),
 ]
 
 
@@ -361,3 +364,19 @@ def test_product_of_more_src1_rows_than_a_grid_has_in_y():
     ref = qs.dequantize_mxfp4(a, a_s).double() @ qs.dequantize_mxfp4(w, ws).double().t()
     assert bool((y == ref).all())
     assert bool((qs.mul_mat_mxfp4_f32(w, ws, torch.zeros((m, k), device="cuda")) == 0).all())
+
+
+LARGE_SPLIT = (700, 3001, 32768)
+
+
+def test_product_split_over_the_largest_tile():
+    """Sums of multiples of 2^-4 below 2^20: exact in fp32, in whatever order they are joined."""
+    qs = _qs()
+    m, n, k = LARGE_SPLIT
+    say("mxfp4 split of the largest tile", m, n, k)
+    w, ws = _large(n, k, 5)
+    a, a_s = _large(m, k, 6)
+    y = qs.mul_mat_mxfp4_mxfp4(w, ws, a, a_s)
+    x, v = qs.dequantize_mxfp4(a, a_s).double(), qs.dequantize_mxfp4(w, ws).double()
+    assert float((x.abs() @ v.abs().t()).max()) < 2.0 ** 20
+    assert bool((y == x @ v.t()).all())

@@ -28,7 +28,8 @@ def _inputs(t, d, seed=0):
 
 
 SHAPES = [(1, 1), (1, 4096), (3, 7), (5, 33), (4, 64), (7, 511), (9, 513), (2, 1000), (17, 2049), (1, 8192), (6, 16391),
-          (3, 70001), (1, 262144), (600, 512), (513, 100), (700, 2056), (515, 5000), (520, 12288), (514, 40000), (4095, 128)]
+          (3, 70001), (1, 262144), (600, 512), (513, 100), (700, 2056), (515, 5000), (520, 12288), (514, 40000), (4095, 128),
+          (600, 1000), (2, 12000)]
 
 
 @pytest.mark.parametrize("t,d", SHAPES)
