@@ -99,6 +99,25 @@ __device__ __forceinline__ float split_store(uint8_t* blk, int c, float v, float
   return __builtin_amdgcn_ldexpf(1.0f, -shift);
 }
 
+// Four values, 4 q .. 4 q + 3, of a block at once.
+template <int TY>
+__device__ __forceinline__ float split_store4(uint8_t* blk, int q, float4 v, float amax) {
+  int shift = 15 - __builtin_amdgcn_frexp_expf(amax);
+  shift = shift > 126 ? 126 : shift;
+  const float x[4] = {v.x, TY == MM_TYPE_Q4_0R ? v.z : v.y, TY == MM_TYPE_Q4_0R ? v.y : v.z, v.w};
+  union { _Float16 h[4]; uint2 u; } hi, lo;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float xs = __builtin_amdgcn_ldexpf(x[i], shift);
+    hi.h[i] = (_Float16)xs;
+    lo.h[i] = (_Float16)(xs - (float)hi.h[i]);
+  }
+  uint8_t* const p = blk + split_pos<TY>(4 * q);
+  *reinterpret_cast<uint2*>(p) = hi.u;
+  *reinterpret_cast<uint2*>(p + 16) = lo.u;
+  return __builtin_amdgcn_ldexpf(1.0f, -shift);
+}
+
 // Maximum over each half wave (32 lanes), in every lane of it.
 __device__ __forceinline__ float half_wave_max(float v) {
   v = fmaxf(v, dpp_f<0xB1>(v));
@@ -136,6 +155,19 @@ __device__ __forceinline__ void split_rows(const float* __restrict__ x, uint8_t*
 // a token names several times is kept once, with the sum of its weights (so that
 // no expert has more rows than there are tokens, and no two rows of one job add
 // to the same sum).
+//
+// Slot i's expert, or -1, and its weight.
+__device__ __forceinline__ int taken(const int* ids, const float* weights, int i, int k, int E, float& w) {
+  const int first = i / k * k, id = ids[i];
+  w = weights[i];
+  if (id < 0 || id >= E) return -1;
+  for (int j = first; j < i; ++j)
+    if (ids[j] == id) return -1;
+  for (int j = i + 1; j < first + k; ++j)
+    if (ids[j] == id) w += weights[j];
+  return id;
+}
+
 template <int TY, int TT>
 __global__ __launch_bounds__(256) void k_moe_take(MoeArgs a, int splits) {
   if ((int)blockIdx.x < splits) {
@@ -143,19 +175,9 @@ __global__ __launch_bounds__(256) void k_moe_take(MoeArgs a, int splits) {
     return;
   }
   if (blockIdx.y) return;
-  const int k = a.top_k;
-  for (int i = threadIdx.x; i < a.T * k; i += 256) {
-    const int first = i / k * k;
-    int id = a.given_ids[i];
-    float w = a.given_weights[i];
-    if (id < 0 || id >= a.E) id = -1;
-    if (id >= 0) {
-      for (int j = first; j < i; ++j)
-        if (a.given_ids[j] == id) { id = -1; break; }
-      for (int j = i + 1; j < first + k && id >= 0; ++j)
-        if (a.given_ids[j] == id) w += a.given_weights[j];
-    }
-    a.ids[i] = id;
+  for (int i = threadIdx.x; i < a.T * a.top_k; i += 256) {
+    float w;
+    a.ids[i] = taken(a.given_ids, a.given_weights, i, a.top_k, a.E, w);
     a.weights[i] = w;
   }
 }
@@ -543,9 +565,40 @@ struct Acts {
   }
 };
 
+// The same for a pass of up to 4 tokens whose workgroup holds all of split x in LDS:
+// rows of held_pitch bytes (16 more than their blocks, so that four rows lie in
+// different banks), then the rows' scales.
+__host__ __device__ constexpr int held_pitch(int nbp) { return 128 * nbp + 16; }
+
+struct ActsHeld {
+  static constexpr int kLds = 0;
+  const uint8_t *row, *srow;
+  int unit;
+  uint4 hi[4], lo[4];
+  float4 s[1];
+  template <class F>
+  __device__ __forceinline__ void bind(const uint8_t* held, int T, int nbp, int n, int lane, F row_of) {
+    const int g = lane >> 4;
+    row = held + row_of(min((lane >> 2) & 3, n - 1)) * held_pitch(nbp) + 32 * g;
+    srow = held + T * held_pitch(nbp) + row_of(min(g, n - 1)) * 4 * nbp;
+  }
+  __device__ __forceinline__ void load(int u, int, int, uint32_t) { unit = u; }
+  __device__ __forceinline__ void fetch(const uint8_t*, int) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      hi[j] = *reinterpret_cast<const uint4*>(row + 512 * unit + 128 * j);
+      lo[j] = *reinterpret_cast<const uint4*>(row + 512 * unit + 128 * j + 16);
+    }
+    s[0] = *reinterpret_cast<const float4*>(srow + 16 * unit);
+  }
+  __device__ __forceinline__ float scale(int, int j) const {
+    return j == 0 ? s[0].x : j == 1 ? s[0].y : j == 2 ? s[0].z : s[0].w;
+  }
+};
+
 // acc[i][r] += the unit's contribution of RT weight tiles to token 4 r + g.
-template <int TY, int NR, int RT>
-__device__ __forceinline__ void unit_product(const Acts<NR>& x, const Tile<TY> (&w)[RT],
+template <int TY, int NR, int RT, class X>
+__device__ __forceinline__ void unit_product(const X& x, const Tile<TY> (&w)[RT],
                                              float (&acc)[RT][NR]) {
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
@@ -622,9 +675,9 @@ constexpr int up_parts() { return Tile<TY>::kLds > 0 && !kFew ? kUpWaves / 2 : k
 
 // Dynamic LDS of the gate / up kernel: the waves' staging, then their partial
 // sums (before both, the logits where it makes the selection).
-template <int TY, bool kFew>
+template <int TY, bool kFew, bool kHeld>
 constexpr int up_lds() {
-  return kUpWaves * (Acts<kFew ? 1 : 4>::kLds + 4 * Tile<TY>::kLds) +
+  return kUpWaves * ((kHeld ? 0 : Acts<kFew ? 1 : 4>::kLds) + 4 * Tile<TY>::kLds) +
          up_parts<TY, kFew>() * 4 * (kFew ? 4 : 16) * 64;
 }
 
@@ -633,22 +686,27 @@ constexpr int up_lds() {
 // first loads are under way while the one before is joined.  The join: partial
 // sums to part[wave][tile][token][16] (kRows tokens), added in wave order,
 // h = silu(g) u, split per block of 32 rows.
-template <int TY, int NR, int kRows>
-__device__ __forceinline__ void up_pass(const MoeArgs& a, int e, int rg0, int step, const int* list,
-                                        int n, uint8_t* lds, float* part, int lane, int wave) {
+// held: split x in LDS, where kHeld.
+template <int TY, int NR, int kRows, bool kHeld>
+__device__ __forceinline__ void up_pass(const MoeArgs& a, int e, int rg0, int step, const int* list, int n,
+                                        uint8_t* lds, float* part, const uint8_t* held, int lane, int wave) {
   constexpr int W = kUpWaves, P = up_parts<TY, kRows == 4>();
   asm volatile("" : "+v"(lane));                     // keep a pass's addresses inside the pass
   const int g = lane >> 4, i16 = lane & 15;
   const int nb = a.D / 32, units = (nb + 3) / 4;
   const int nfb = a.F / 32, nfp = (nfb + 3) & ~3;
-  Acts<NR> x;
-  x.bind(a.xp, a.xs, nb, n, lane, [&](int m) { return list[m] / a.top_k; });
+  static_assert(!kHeld || NR == 1, "four tokens");
+  using X = std::conditional_t<kHeld, ActsHeld, Acts<NR>>;
+  X x;
+  const auto token = [&](int m) { return list[m] / a.top_k; };
+  if constexpr (kHeld) x.bind(held, a.T, (nb + 3) & ~3, n, lane, token);
+  else x.bind(a.xp, a.xs, nb, n, lane, token);
   float acc[4][NR];
 #pragma unroll
   for (int i = 0; i < 4; ++i)
 #pragma unroll
     for (int r = 0; r < NR; ++r) acc[i][r] = 0.0f;
-  const uint32_t at = lds_offset(lds), tat = at + Acts<NR>::kLds;
+  const uint32_t at = lds_offset(lds), tat = at + X::kLds;
   const auto issue_w = [&](Tile<TY> (&w)[4], int rg, int u) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -660,7 +718,7 @@ __device__ __forceinline__ void up_pass(const MoeArgs& a, int e, int rg0, int st
   const auto fetch = [&](Tile<TY> (&w)[4]) {
     x.fetch(lds, lane);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) w[i].fetch(lds + Acts<NR>::kLds + i * Tile<TY>::kLds, lane);
+    for (int i = 0; i < 4; ++i) w[i].fetch(lds + X::kLds + i * Tile<TY>::kLds, lane);
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
   };
   const auto join = [&](int rg) {
@@ -741,11 +799,14 @@ __device__ __forceinline__ void up_pass(const MoeArgs& a, int e, int rg0, int st
 // tiles that share the activations), every a.up_groups-th group of the
 // blockIdx.y-th expert in use, over its tokens in passes of 16.  a.fold: every
 // workgroup ranks the logits itself (a launch less), and one writes ids and
-// weights for the next launch.
-template <int TY, bool kFew>
+// weights for the next launch.  kHeld: the choice is given, and every workgroup
+// makes it fit and splits x itself (a launch less, and no copies of x beside the
+// weights').
+template <int TY, bool kFew, bool kHeld>
 __global__ __launch_bounds__(64 * kUpWaves, TY == kMxfp4Few ? 4 : 2) void k_moe_up(MoeArgs a) {
+  static_assert(kFew || !kHeld, "few tokens");
   constexpr int W = kUpWaves, kRows = kFew ? 4 : 16;
-  constexpr int kStage = Acts<kFew ? 1 : 4>::kLds + 4 * Tile<TY>::kLds;
+  constexpr int kStage = (kHeld ? 0 : Acts<kFew ? 1 : 4>::kLds) + 4 * Tile<TY>::kLds;
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
   __shared__ uint16_t sids[kMoeMaxTokens * kMoeMaxTopK];
   __shared__ uint32_t bits[kMoeMaxExperts / 32];
@@ -754,7 +815,62 @@ __global__ __launch_bounds__(64 * kUpWaves, TY == kMxfp4Few ? 4 : 2) void k_moe_
   __shared__ int count;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int k = a.top_k, E = a.E, assigned = a.T * k;
-  if (a.fold) {
+  uint8_t* const held = lds + up_lds<TY, kFew, kHeld>();
+  if constexpr (kHeld) {
+    const bool outputs = blockIdx.x == gridDim.x - 1;   // one more column of workgroups
+    if (outputs && blockIdx.y) return;
+    // four values per thread, eight threads per block of 32
+    const int nb = a.D / 32, nbp = (nb + 3) & ~3, row = 8 * nbp;
+    float* const hs = reinterpret_cast<float*>(held + a.T * held_pitch(nbp));
+    int id = -1;
+    if (wave == 0 && lane < assigned) id = a.given_ids[lane];        // assigned <= 64
+    for (int i0 = tid; i0 < a.T * row && !outputs; i0 += 4 * 64 * W) {
+      float4 v[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int i = i0 + 64 * W * q, t = (i >= row) + (i >= 2 * row) + (i >= 3 * row), at = i - t * row;
+        v[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (t < a.T && at < 8 * nb) v[q] = *reinterpret_cast<const float4*>(a.x + t * a.D + 4 * at);
+      }
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int i = i0 + 64 * W * q, t = (i >= row) + (i >= 2 * row) + (i >= 3 * row), at = i - t * row;
+        if (64 * W * q + (i0 - tid) >= a.T * row) break;             // uniform
+        float amax = fmaxf(fmaxf(fabsf(v[q].x), fabsf(v[q].y)), fmaxf(fabsf(v[q].z), fabsf(v[q].w)));
+        amax = fmaxf(amax, dpp_f<0xB1>(amax));
+        amax = fmaxf(amax, dpp_f<0x4E>(amax));
+        amax = fmaxf(amax, dpp_f<0x141>(amax));      // eight lanes
+        if (t >= a.T) continue;
+        const float s = split_store4<TY>(held + t * held_pitch(nbp) + 128 * (at >> 3), at & 7, v[q], amax);
+        if ((at & 7) == 0) hs[t * nbp + (at >> 3)] = at < 8 * nb ? s : 0.0f;
+      }
+    }
+    if (wave == 0) {
+      if (id >= E) id = -1;
+      const float w = outputs && lane < assigned ? a.given_weights[lane] : 0.0f;
+      const int slot = lane % k;
+      float sum = w;
+      bool again = false;
+      for (int j = 1; j < k; ++j) {                  // the slots before and behind of the same token
+        const int before = __shfl_up(id, j, 64);
+        again |= j <= slot && before == id;
+        if (!outputs) continue;                      // uniform
+        const int behind = __shfl_down(id, j, 64);
+        const float more = __shfl_down(w, j, 64);
+        if (slot + j < k && behind == id) sum += more;
+      }
+      if (lane < assigned) {
+        const int kept = again ? -1 : max(id, -1);
+        sids[lane] = (uint16_t)kept;                 // -1: no expert's
+        if (outputs) {
+          a.ids[lane] = kept;
+          a.weights[lane] = sum;
+        }
+      }
+    }
+    if (outputs) return;
+    __syncthreads();
+  } else if (a.fold) {
     double* const l = reinterpret_cast<double*>(lds);
     if (tid < kMoeMaxTokens / 32) nans[tid] = 0;
     __syncthreads();
@@ -821,11 +937,11 @@ __global__ __launch_bounds__(64 * kUpWaves, TY == kMxfp4Few ? 4 : 2) void k_moe_
   for (int m0 = 0; m0 < n; m0 += 16) {
     const int rows = min(n - m0, 16), rg = blockIdx.x, step = a.up_groups;
     if constexpr (kFew) {
-      up_pass<TY, 1, kRows>(a, e, rg, step, list + m0, rows, stage, part, lane, wave);
+      up_pass<TY, 1, kRows, kHeld>(a, e, rg, step, list + m0, rows, stage, part, held, lane, wave);
     } else {
-      if (rows <= 4) up_pass<TY, 1, kRows>(a, e, rg, step, list + m0, rows, stage, part, lane, wave);
-      else if (rows <= 8) up_pass<TY, 2, kRows>(a, e, rg, step, list + m0, rows, stage, part, lane, wave);
-      else up_pass<TY, 4, kRows>(a, e, rg, step, list + m0, rows, stage, part, lane, wave);
+      if (rows <= 4) up_pass<TY, 1, kRows, kHeld>(a, e, rg, step, list + m0, rows, stage, part, held, lane, wave);
+      else if (rows <= 8) up_pass<TY, 2, kRows, false>(a, e, rg, step, list + m0, rows, stage, part, held, lane, wave);
+      else up_pass<TY, 4, kRows, false>(a, e, rg, step, list + m0, rows, stage, part, held, lane, wave);
     }
   }
 }
@@ -1007,13 +1123,18 @@ hipError_t down(const MoePlan& p, const MoeArgs& a, float* out, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <int TY, bool kFew>
+template <int TY, bool kFew, bool kHeld>
 hipError_t up(dim3 grid, const MoeArgs& a, hipStream_t s) {
-  constexpr int lds = up_lds<TY, kFew>();
-  auto* const kern = k_moe_up<TY, kFew>;
-  if (lds > 65536) {
+  const int nbp = (a.D / 32 + 3) & ~3;
+  if (kHeld && a.T * nbp > kMoeHeldBlocks) return hipErrorInvalidValue;   // the plan's rule
+  const int lds = up_lds<TY, kFew, kHeld>() + (kHeld ? a.T * (held_pitch(nbp) + 4 * nbp) : 0);
+  constexpr int most = up_lds<TY, kFew, kHeld>() +
+                       (kHeld ? kMoeHeldBlocks * 132 + kMoeFewTokens * held_pitch(0) : 0);
+  static_assert(most <= kMoeMaxLds, "LDS");
+  auto* const kern = k_moe_up<TY, kFew, kHeld>;
+  if (most > 65536) {
     static std::atomic<uint64_t> raised{0};
-    const hipError_t e = raise_lds(reinterpret_cast<const void*>(kern), lds, raised);
+    const hipError_t e = raise_lds(reinterpret_cast<const void*>(kern), most, raised);
     if (e != hipSuccess) return e;
   }
   hipLaunchKernelGGL(kern, grid, dim3(64 * kUpWaves), lds, s, a);
@@ -1023,7 +1144,9 @@ hipError_t up(dim3 grid, const MoeArgs& a, hipStream_t s) {
 template <int TY>
 hipError_t run(const MoePlan& p, const MoeArgs& a, float* part, hipStream_t s) {
   const int splits = (((a.D / 32 + 3) & ~3) + 7) / 8;
-  if (a.given_ids) {
+  if (p.held) {
+    // no launch: see k_moe_up
+  } else if (a.given_ids) {
     if (a.T == 1) hipLaunchKernelGGL((k_moe_take<TY, 1>), dim3(splits + 1, 1), dim3(256), 0, s, a, splits);
     else hipLaunchKernelGGL((k_moe_take<TY, 4>), dim3(splits + 1, (a.T + 3) / 4), dim3(256), 0, s, a, splits);
   } else if (a.T == 1)
@@ -1038,10 +1161,12 @@ hipError_t run(const MoePlan& p, const MoeArgs& a, float* part, hipStream_t s) {
     if (e != hipSuccess) return e;
   }
   const int assigned = a.T * a.top_k;
-  const dim3 grid(a.up_groups + (a.fold ? 1 : 0), assigned < a.E ? assigned : a.E);
+  const dim3 grid(a.up_groups + (a.fold || p.held ? 1 : 0), assigned < a.E ? assigned : a.E);
   const bool few = a.T <= kMoeFewTokens;
   constexpr int kFewType = TY == MM_TYPE_MXFP4 ? kMxfp4Few : TY;
-  e = few ? up<kFewType, true>(grid, a, s) : up<TY, false>(grid, a, s);
+  e = p.held ? up<kFewType, true, true>(grid, a, s)
+      : few  ? up<kFewType, true, false>(grid, a, s)
+             : up<TY, false, false>(grid, a, s);
   if (e != hipSuccess) return e;
   float* const out = p.slices > 1 ? part : a.dst;
   if (few) e = down<kFewType, 1, 16, true>(p, a, out, s);

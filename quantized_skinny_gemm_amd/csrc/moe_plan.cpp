@@ -38,6 +38,7 @@ int make_moe_plan(int type, int64_t T, int64_t D, int64_t F, int64_t E, int64_t 
   // The selection costs each workgroup of the next launch about T E^2 / 512
   // steps per thread where it makes it itself.
   p->fold = !routed && T * E * E <= 65536;
+  p->held = routed && T <= kMoeFewTokens && T * (int64_t)align_up((size_t)(D / kQK), 4) <= kMoeHeldBlocks;
   // Down: 16 rows per workgroup while an expert serves few tokens; with more,
   // 64 rows share each activation load (activations are 4 bytes a value, the
   // weights as few as half a byte) and the sequence of (expert, unit) pairs

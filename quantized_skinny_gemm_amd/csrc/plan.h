@@ -185,9 +185,11 @@ int validate_mx4_quantize(const void* x, const void* codes, const void* scales, 
 // Plan of the mixture-of-experts layer (moe.hip).
 constexpr int kMoeFewTokens = 4;      // up to this many tokens: kernels for passes of 4
 constexpr int kMoeMxPairTokens = 48;   // down, MXFP4: two units of weights in LDS up to this many tokens
+constexpr int kMoeHeldBlocks = 256;   // split x that the gate / up kernel holds: blocks of 32 values
 constexpr int kMoeMaxLds = 150528;     // dynamic LDS of the down kernel (160 KB less its static part)
 struct MoePlan {
   bool fold = false;       // the selection is made by the gate / up launch
+  bool held = false;       // a given choice: the gate / up launch makes it fit and splits x itself
   int up_groups = 1;       // gate / up: workgroups along F per expert
   int rt = 1, slices = 1;  // down: 16-row tiles per workgroup, workgroups sharing a tile's sum
   size_t off_logits = 0, off_ids = 0, off_weights = 0, off_xp = 0, off_xs = 0, off_hp = 0, off_hs = 0;

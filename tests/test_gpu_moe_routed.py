@@ -99,6 +99,8 @@ KINDS = ["mxfp4", "q4_0r", "f8", "f16"]
     (1, 256, 128, 4, 2), (1, 32, 32, 1, 1), (1, 2080, 1056, 12, 3), (2, 288, 160, 5, 5), (7, 416, 96, 12, 3),
     (16, 512, 256, 8, 2), (17, 256, 288, 3, 1), (24, 512, 1024, 2, 2), (33, 160, 64, 40, 8), (32, 512, 1024, 2, 2),
     (64, 128, 96, 2, 2), (100, 96, 128, 16, 4), (128, 64, 32, 512, 16),
+    # few tokens, on both sides of what the gate / up kernel holds of x
+    (1, 8192, 64, 3, 2), (1, 8224, 64, 3, 2), (2, 4096, 96, 5, 3), (4, 2048, 64, 16, 16), (4, 2080, 64, 6, 4), (3, 2752, 64, 4, 2),
 ])
 def test_routed(kind, t, d, f, e, top_k):
     say("moe routed", kind, t, d, f, e, top_k)
