@@ -9,10 +9,12 @@
 // A row belongs to 1 to 16 waves of one workgroup; a lane holds up to R pieces
 // of 8 consecutive values from the one read to the one write, 16 neighbouring
 // lanes a block of 128.  The sum of squares is held in fp64 (the kernel waits for
-// memory, so this costs nothing): it neither overflows nor depends on how a row is
-// cut among lanes in any bit that survives rstd's rounding to fp32, so a row
-// gives the same y, and the same codes, in every batch.  Bound: HBM (8 bytes per
-// value read, 4 written for v, 0.53 to 4 for y).
+// memory, so this costs nothing): it does not overflow, and how a row is cut among
+// lanes, which follows the number of rows, moves it by about 1e-16 only: rstd, rounded
+// to fp32, can differ in its last bit between batches for about one row in 10^8.
+// Bound: HBM (8 bytes per value read, 4 written for v, 0.53 to 4 for y).  2047 x 8192
+// into MXFP4, 210 MB: 45 us, 4.7 TB/s; 1 x 4096 into e4m3: 3.0 us, launch and the
+// latencies of one read, a join over LDS and one write.
 #include "f8.h"
 #include "kernels.h"
 #include "mx4.h"

@@ -6,8 +6,9 @@
 // an integer that orders as the number does (0: not to be had, 1: NaN), the upper
 // half first: a maximum over the wave by DPP, then the lanes that hold it; only
 // where several do (equal upper halves) the lower halves and the indices decide.
-// Bound: latency for a few tokens (about 170 cycles per expert chosen), the fp64
-// exponentials for many.
+// Bound: latency for a few tokens (about 170 cycles per expert chosen; 1 token, 256
+// experts in 8 groups, 8 chosen: 5.0 us), the fp64 exponentials for many (4095 tokens,
+// 64 experts, 6 chosen: 5.6 us).
 #include "device.h"
 #include "kernels.h"
 #include "../../include/mm.h"
