@@ -1,5 +1,5 @@
-"""The plans of the MXFP4 product and the norm's launch shapes, as their host source makes them (compiled here with g++,
-no GPU)."""
+"""The plans of the MXFP4 product and of the experts for a given routing, and the norm's launch shapes, as their host
+sources make them (compiled here with g++, no GPU)."""
 from __future__ import annotations
 
 import ctypes
@@ -25,9 +25,16 @@ extern "C" void probe_norm(int64_t T, int64_t D, int64_t* o) {
   qsg::norm_shape(T, D, &waves, &rows);
   o[0] = waves; o[1] = rows;
 }
+extern "C" int probe_routed(int64_t type, int64_t T, int64_t D, int64_t F, int64_t E, int64_t k, int64_t* o) {
+  qsg::MoePlan p;
+  const int st = qsg::make_moe_plan((int)type, T, D, F, E, k, &p, true);
+  o[0] = p.held; o[1] = p.up_groups; o[2] = p.rt; o[3] = p.slices;
+  return st;
+}
 """
 
 KIND = {0: "none", 1: "zero", 2: "fused", 3: "skinny", 4: "wide"}
+Routed = namedtuple("Routed", "held up_groups rt slices")
 Mx4 = namedtuple("Mx4", "kind nt waves grid_n bm bn split kchunk ws_bytes")
 
 
@@ -38,7 +45,7 @@ def _lib():
         with open(src, "w") as f:
             f.write(SOURCE)
         subprocess.run(["g++", "-std=c++17", "-shared", "-fPIC", f"-I{CSRC}", src, os.path.join(CSRC, "mx4_plan.cpp"),
-                        "-o", out], check=True)
+                        os.path.join(CSRC, "moe_plan.cpp"), "-o", out], check=True)
         return ctypes.CDLL(out)
 
 
@@ -55,3 +62,10 @@ def norm(t, d):
     out = (ctypes.c_int64 * 2)()
     _lib().probe_norm(ctypes.c_int64(t), ctypes.c_int64(d), out)
     return tuple(out)
+
+
+def routed(mm_type, t, d, f, e, top_k) -> Routed:
+    out = (ctypes.c_int64 * 4)()
+    st = _lib().probe_routed(*map(ctypes.c_int64, (mm_type, t, d, f, e, top_k)), out)
+    assert st == 0, st
+    return Routed(*out)

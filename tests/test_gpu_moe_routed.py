@@ -94,14 +94,17 @@ def _x(rng, t, d):
 KINDS = ["mxfp4", "q4_0r", "f8", "f16"]
 
 
-@pytest.mark.parametrize("kind", KINDS)
-@pytest.mark.parametrize("t,d,f,e,top_k", [
+ROUTED = [
     (1, 256, 128, 4, 2), (1, 32, 32, 1, 1), (1, 2080, 1056, 12, 3), (2, 288, 160, 5, 5), (7, 416, 96, 12, 3),
     (16, 512, 256, 8, 2), (17, 256, 288, 3, 1), (24, 512, 1024, 2, 2), (33, 160, 64, 40, 8), (32, 512, 1024, 2, 2),
     (64, 128, 96, 2, 2), (100, 96, 128, 16, 4), (128, 64, 32, 512, 16),
     # few tokens, on both sides of what the gate / up kernel holds of x
     (1, 8192, 64, 3, 2), (1, 8224, 64, 3, 2), (2, 4096, 96, 5, 3), (4, 2048, 64, 16, 16), (4, 2080, 64, 6, 4), (3, 2752, 64, 4, 2),
-])
+]
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("t,d,f,e,top_k", ROUTED)
 def test_routed(kind, t, d, f, e, top_k):
     say("moe routed", kind, t, d, f, e, top_k)
     m = Layer(kind, d, f, e, top_k, t * 100 + d + f + e)
@@ -110,10 +113,13 @@ def test_routed(kind, t, d, f, e, top_k):
 
 
 # the shapes of the layer with its own router: rows of gate / up walked, all output tiles, slices of down
-@pytest.mark.parametrize("t,d,f,e,top_k", [
+WITH_ROUTER = [
     (1, 256, 128, 4, 2), (1, 2080, 1056, 12, 3), (4, 160, 8256, 8, 2), (16, 160, 4128, 16, 2), (24, 512, 8192, 2, 2), (33, 160, 64, 40, 8),
     (40, 96, 33024, 2, 2), (70, 96, 16416, 2, 2), (128, 64, 32, 512, 16),
-])
+]
+
+
+@pytest.mark.parametrize("t,d,f,e,top_k", WITH_ROUTER)
 def test_mxfp4_experts_with_a_router(t, d, f, e, top_k):
     say("moe mxfp4", t, d, f, e, top_k)
     qs = _qs()
@@ -209,6 +215,22 @@ def test_nan_block_of_an_expert_that_is_not_used():
     assert np.isnan(dst[3]).any() and np.isfinite(np.delete(dst, 3, axis=0)).all()
 
 
+@pytest.mark.parametrize("t", [1, 5, 60])
+def test_smallest_scales_of_experts(t):
+    """Scale bytes 0 (2^-127, below fp32's normal range), 1 and 2 in gate and up, with activations of about 2^100."""
+    say("moe mxfp4 smallest scales", t)
+    m = Layer("mxfp4", 160, 96, 3, 2, 5)
+    rng = np.random.default_rng(t)
+    for i in (0, 1):
+        codes, scales = to_host(m.dev[i]), to_host(m.scales[i])
+        scales[:, :, :5] = rng.integers(0, 3, scales[:, :, :5].shape)
+        m.scales[i].copy_(to_dev(scales))
+        m.values[i] = np.stack([mx4.dequantize(c, s) for c, s in zip(codes, scales)])
+    x = _x(rng, t, 160) * np.float32(2.0 ** 100)
+    dst = m.check(x, *_choice(rng, t, 3, 2))
+    assert (np.abs(dst) > 0).mean() > 0.99
+
+
 @pytest.mark.parametrize("kind", ["mxfp4", "f16"])
 @pytest.mark.parametrize("t", [1, 6, 40])
 def test_graph_replays_follow_their_inputs(kind, t):
@@ -237,6 +259,29 @@ def test_graph_replays_follow_their_inputs(kind, t):
         torch.cuda.synchronize()
         assert torch.equal(out, y)
         assert torch.equal(ids, c[1]) and torch.equal(w, c[2])
+
+
+@pytest.mark.parametrize("t", [2, 20])
+def test_two_streams_at_once(t):
+    """Routing and experts on two streams, inputs of their own, workspaces of their own: the bits of one after the other."""
+    import torch
+    qs = _qs()
+    say("moe routed two streams", t)
+    m = Layer("mxfp4", 256, 512, 12, 3, 9)
+    rng = np.random.default_rng(t)
+    router = qs.Router(12, 3)
+    xs = [to_dev(_x(rng, t, 256)) for _ in range(2)]
+    logits = [to_dev(rng.standard_normal((t, 12)).astype(np.float32)) for _ in range(2)]
+    want = [qs.moe_routed_f32(m.layer, x, *qs.route_f32(router, l)) for x, l in zip(xs, logits)]
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream() for _ in range(2)], [[], []]
+    for _ in range(8):
+        for i, st in enumerate(streams):
+            with torch.cuda.stream(st):
+                got[i].append(qs.moe_routed_f32(m.layer, xs[i], *qs.route_f32(router, logits[i])))
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(y, want[i]) for y in got[i])
 
 
 def test_mxfp4_experts_past_4_gib():

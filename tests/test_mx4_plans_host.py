@@ -1,10 +1,11 @@
-"""Which kernel, tile and split a call of the MXFP4 product takes: every one of them is among the shapes that run on a GPU,
-and the plans hold what the kernels assume."""
+"""Which kernel, tile and split a call of the MXFP4 product takes, and which launches the experts for a given routing: every
+one of them is among the shapes that run on a GPU, and the plans hold what the kernels assume."""
 from __future__ import annotations
 
 import itertools
 
 from tests import mx4_plans
+from tests.test_gpu_moe_routed import ROUTED, WITH_ROUTER
 from tests.test_gpu_mx4 import LARGE_SPLIT, SHAPES
 from tests.test_gpu_norm import SHAPES as NORMS
 
@@ -66,3 +67,18 @@ def test_norm_shapes():
         assert waves in (1, 2, 4, 8, 16) and rows == max(1, 4 // waves)
         held.add(min(5, -(-(-(-d // 8)) // (64 * waves))))
     assert {1, 2, 5} <= held and held & {3, 4}, held
+
+
+def test_routed_experts():
+    """Few tokens on both sides of what the gate / up kernel holds of x; with MXFP4 experts down with one and two tiles, one and
+    two units of weights at a time, whole and in slices."""
+    held = {(t == 1, bool(mx4_plans.routed(6, t, d, f, e, k).held)) for t, d, f, e, k in ROUTED if t <= 4}
+    assert held == set(itertools.product((False, True), repeat=2))
+    for t, d, f, e, k in ROUTED + WITH_ROUTER:
+        for mm_type in (1, 4, 5, 6):
+            p = mx4_plans.routed(mm_type, t, d, f, e, k)
+            assert bool(p.held) == (t <= 4 and t * 4 * -(-d // 128) <= 256)
+    many = [(t, mx4_plans.routed(6, t, d, f, e, k)) for t, d, f, e, k in ROUTED + WITH_ROUTER if t > 4]
+    assert {p.rt for _, p in many} == {1, 2}
+    assert {t > 48 for t, p in many if p.rt == 2} == {False, True}
+    assert any(p.slices > 1 for _, p in many) and any(p.slices == 1 for _, p in many)
