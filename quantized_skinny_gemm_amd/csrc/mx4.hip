@@ -677,6 +677,7 @@ hipError_t launch_mx4_product(const Mx4Plan& p, const uint8_t* w, const uint8_t*
     return hipErrorInvalidValue;
   }
   if (p.bm == 32 && p.bn == 32) return wide<32, 32, 1, 1, 4, 2>(p, w, wsc, a, asc, dst, M, N, K, ws, s);
+  if (p.bm == 32 && p.bn == 64) return wide<32, 64, 1, 2, 4, 2>(p, w, wsc, a, asc, dst, M, N, K, ws, s);
   if (p.bm == 64 && p.bn == 64) return wide<64, 64, 2, 2, 3>(p, w, wsc, a, asc, dst, M, N, K, ws, s);
   if (p.bm == 64 && p.bn == 128) return wide<64, 128, 2, 4, 3>(p, w, wsc, a, asc, dst, M, N, K, ws, s);
   if (p.bm == 128 && p.bn == 128) return wide<128, 128, 4, 2, 3>(p, w, wsc, a, asc, dst, M, N, K, ws, s);

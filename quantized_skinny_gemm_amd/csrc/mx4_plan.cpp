@@ -69,7 +69,7 @@ int make_mx4_plan(int64_t M, int64_t N, int64_t K, bool given, Mx4Plan* p) {
   // Tiled: the tile, and the split of K over workgroups (with a second launch to join
   // it), of the least time by what a workgroup of each takes per stage of 256 k where
   // it has a CU to itself (hundredths of a us; fitted to calls of at most 256 workgroups
-  // at K = 4096, which take 5, 7 to 10, 9.6 to 14, 12 to 17, 18 to 25 and 27
+  // at K = 4096, which take 5, 6 to 8, 7 to 10, 9.6 to 14, 12 to 17, 18 to 25 and 27
   // to 34 us from few workgroups to 256).  256 workgroups run at a time; those that share
   // a CU take as long as one after the other.  The tile chosen and the best of all, in us:
   // 64 x 14336 x 4096 8.3 (64 x 64, the best), 128 x 14336 x 4096 11.3 (64 x 128, the best),
@@ -78,8 +78,11 @@ int make_mx4_plan(int64_t M, int64_t N, int64_t K, bool given, Mx4Plan* p) {
   // 4096 39 (256 x 256, the best; 256 x 128 53), 2048 x 4096 x 14336 80 (256 x 128, the best;
   // 256 x 256 94), 512 x 128256 x 4096 182 (256 x 256, the best; 256 x 128 222), 256 x
   // 4096 x 4096 7.9 (64 x 64, the best), 512 x 4096 x 4096 10.8 (64 x 128, the best).
-  static const struct { int bm, bn, cost; } kTiles[] = {
-      {32, 32, 19}, {64, 64, 31}, {64, 128, 44}, {128, 128, 63}, {256, 128, 90}, {256, 256, 155}};
+  // The 32 x 64 tile (two sets of waves, each with half of K) has half a us to join its
+  // sums: 32 x 14336 x 4096 8.3 (64 x 64 9.4, 32 x 32 8.9), 64 x 8192 x 4096 6.6 (7.6, 7.3),
+  // 128 x 4096 x 4096 6.3 (7.6, 7.1), but 20 x 16000 x 1056 5.3 (4.9, 5.3).
+  static const struct { int bm, bn, cost, fixed; } kTiles[] = {
+      {32, 32, 19}, {32, 64, 24, 50}, {64, 64, 31}, {64, 128, 44}, {128, 128, 63}, {256, 128, 90}, {256, 256, 155}};
   const int64_t nst = ceil_div(K, 256);
   int64_t best = -1;
   p->kind = MX4_WIDE;
@@ -93,7 +96,7 @@ int make_mx4_plan(int64_t M, int64_t N, int64_t K, bool given, Mx4Plan* p) {
       // 14336 12.5 / 11.0; of the largest tile that fills the device 8 times, which a cost
       // without the bytes takes: 1024 x 1024 x 8192 24 / 12, 384 x 4096 x 14336 34 / 26)
       if (split > 1 && (nst < 4 * split || tm * tn * split > kCUs)) break;
-      const int64_t time = ceil_div(tm * tn * split, kCUs) * ceil_div(nst, split) * t.cost + (split > 1 ? 700 + split * M * N / 6000 : 0);
+      const int64_t time = ceil_div(tm * tn * split, kCUs) * ceil_div(nst, split) * t.cost + t.fixed + (split > 1 ? 700 + split * M * N / 6000 : 0);
       if (best >= 0 && time >= best) continue;
       best = time;
       p->bm = t.bm; p->bn = t.bn;

@@ -116,7 +116,7 @@ SHAPES = [
     (31, 5000, 352), (48, 4096, 4096), (64, 14336, 1024), (128, 4096, 4096), (256, 4096, 2048), (40, 40, 7200),
     # several stages of the largest tiles, the last one ragged; K split evenly and unevenly
     (500, 14300, 1120), (1000, 14200, 800), (33, 70, 19936), (40, 30, 16384), (129, 300, 16416), (200, 300, 24608),
-    (300, 1001, 28672), (300, 2048, 28928),
+    (300, 1001, 28672), (300, 2048, 28928), (33, 300, 28704), (33, 4100, 2080), (20, 9001, 4128), (64, 8190, 2336), (128, 4000, 1888),
 ]
 
 

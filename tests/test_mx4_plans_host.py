@@ -10,7 +10,7 @@ from tests.test_gpu_mx4 import LARGE_SPLIT, SHAPES
 from tests.test_gpu_norm import SHAPES as NORMS
 
 PRODUCTS = SHAPES + [LARGE_SPLIT]
-TILES = [(32, 32), (64, 64), (64, 128), (128, 128), (256, 128), (256, 256)]
+TILES = [(32, 32), (32, 64), (64, 64), (64, 128), (128, 128), (256, 128), (256, 256)]
 
 
 def _variant(p):
