@@ -312,7 +312,7 @@ __global__ __launch_bounds__(512) void k_mx4_fused(
 // wave has read the whole stage, so the copy of the stage STAGES further can
 // start, and the next stage has arrived.
 //
-// Bound: the weights' bytes for a few rows (32 x 14336 x 4096 9.2 us as traced, 3.6
+// Bound: the weights' bytes for a few rows (32 x 14336 x 4096 8.2 us as traced, 4.0
 // TB/s); for many neither the matrix cores (34% busy at 512 x 128256 x 4096: 170 us,
 // 3.2 PFLOP/s) nor the address units (61%) but the latency of copies that two stages of
 // 256 x 256 do not cover and that a third one, past LDS, would.
