@@ -828,19 +828,19 @@ __global__ __launch_bounds__(64 * kUpWaves, TY == kMxfp4Few ? 4 : 2) void k_moe_
       float4 v[4];
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        const int i = i0 + 64 * W * q, t = (i >= row) + (i >= 2 * row) + (i >= 3 * row), at = i - t * row;
+        const int i = i0 + 64 * W * q, t = held_token(i, row, a.T), at = i - t * row;
         v[q] = make_float4(0.f, 0.f, 0.f, 0.f);
         if (t < a.T && at < 8 * nb) v[q] = *reinterpret_cast<const float4*>(a.x + t * a.D + 4 * at);
       }
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        const int i = i0 + 64 * W * q, t = (i >= row) + (i >= 2 * row) + (i >= 3 * row), at = i - t * row;
+        const int i = i0 + 64 * W * q, t = held_token(i, row, a.T), at = i - t * row;
         if (64 * W * q + (i0 - tid) >= a.T * row) break;             // uniform
         float amax = fmaxf(fmaxf(fabsf(v[q].x), fabsf(v[q].y)), fmaxf(fabsf(v[q].z), fabsf(v[q].w)));
         amax = fmaxf(amax, dpp_f<0xB1>(amax));
         amax = fmaxf(amax, dpp_f<0x4E>(amax));
         amax = fmaxf(amax, dpp_f<0x141>(amax));      // eight lanes
-        if (t >= a.T) continue;
+        if (t >= a.T) continue;                      // eight lanes alike: row % 8 == 0
         const float s = split_store4<TY>(held + t * held_pitch(nbp) + 128 * (at >> 3), at & 7, v[q], amax);
         if ((at & 7) == 0) hs[t * nbp + (at >> 3)] = at < 8 * nb ? s : 0.0f;
       }

@@ -186,6 +186,12 @@ int validate_mx4_quantize(const void* x, const void* codes, const void* scales, 
 constexpr int kMoeFewTokens = 4;      // up to this many tokens: kernels for passes of 4
 constexpr int kMoeMxPairTokens = 48;   // down, MXFP4: two units of weights in LDS up to this many tokens
 constexpr int kMoeHeldBlocks = 256;   // split x that the gate / up kernel holds: blocks of 32 values
+// Whose piece flat index i is where T <= 4 tokens have `row` pieces each, one after the other; T: nobody's
+// (the last round of a workgroup's threads may reach past the last token).
+constexpr int held_token(int i, int row, int T) {
+  return i < T * row ? (i >= row) + (i >= 2 * row) + (i >= 3 * row) : T;
+}
+static_assert(kMoeFewTokens == 4, "held_token");
 constexpr int kMoeMaxLds = 150528;     // dynamic LDS of the down kernel (160 KB less its static part)
 struct MoePlan {
   bool fold = false;       // the selection is made by the gate / up launch
