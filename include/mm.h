@@ -443,7 +443,9 @@ mm_status mm_route_f32(const mm_router* router, const float* logits, int32_t* id
  * The activations are not rounded to 8 bits (unlike the quantized products'
  * src1): x and h enter the products with an error of at most 2^-22 of the
  * value, or of 2^-39 of the largest of its block of 32 values where that is
- * more; every product is exact and sums are fp32.
+ * more; every product is exact and sums are fp32.  A block's sum is multiplied by
+ * the weights' scale first, then by the activations': that cannot overflow on the
+ * way with e4m3 scales up to 2^99 and MXFP4 scales up to 2^105.
  *
  * The layer (a host struct; the library keeps no reference to it):
  *   type    of the expert matrices:

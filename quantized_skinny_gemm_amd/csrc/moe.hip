@@ -31,7 +31,8 @@
 //   weights' scale and s the activations' block scale; the down product's w
 //   multiplies the sum over a run of blocks.  In this order no factor falls
 //   below fp32's normal range before the sum itself does: dw * s would (h of
-//   1e-33 and e4m3 weights: s is 2^-126).
+//   1e-33 and e4m3 weights: s is 2^-126).  Nor does C * dw overflow for dw up to 2^99
+//   (e4m3: |C| <= 32 * 448 * 2^15 < 2^28.9), 2^105 (e2m1: 32 * 6 * 2^15 < 2^22.6).
 //   Token m of a pass of up to 16 sits in row 4 (m % 4) + m / 4, so
 //   that a lane's four result registers are tokens g, 4 + g, 8 + g, 12 + g and
 //   a pass of n tokens scales and adds ceil(n / 4) of them only: this vector
