@@ -390,7 +390,11 @@ size_t mm_mul_mat_mxfp4_workspace_size(int64_t M, int64_t N, int64_t K, int src1
  *   D <= 2^23, a multiple of 32 for the 8- and 4-bit outputs.  f32 arrays and scales
  *   4-byte aligned, codes 16-byte.  No other overlap than sum's.
  * A row with an infinity or NaN yields NaN in that row only (an infinity: zeros in the
- * row's finite places), a row of zeros with eps = 0 too.
+ * row's finite places), a row of zeros with eps = 0 too.  rstd is infinite, as fp32,
+ * where sqrt(mean + eps) is below 2^-128, and subnormal (a multiple of 2^-149, fewer
+ * bits) past 2^126.
+ * The order of a row's fp64 sum depends on T (below 512 rows or not) and D: the same
+ * row in a call of another T may get the neighbouring rstd, about one row in 10^8.
  */
 mm_status mm_rms_norm_f32(const float* x, const float* residual, const float* weight, float eps,
                           float* sum, int out_type, void* y, void* scales, int64_t T, int64_t D,
@@ -408,11 +412,12 @@ mm_status mm_rms_norm_f32(const float* x, const float* residual, const float* we
  *   weights[t][j] = s[ids[t][j]], norm: divided by their sum over j (0 where that is
  *     0), times scale.
  * Scores and sums are fp64, weights rounded once to fp32.
- * An expert whose logit or bias is minus infinity is masked: it is never chosen.
+ * An expert whose logit or bias is minus infinity is masked: it is never chosen; one
+ * whose bias is NaN is chosen after all others.
  * Where fewer than top_k experts are left to choose from, the last slots get id -1
  * and weight 0 (mm_moe_routed_f32 skips them).  A NaN among a token's logits, or
- * under a softmax plus infinity, makes all of that token's weights NaN; its ids are
- * experts (or -1) all the same.
+ * under a softmax plus infinity, makes all of that token's weights NaN (those of slots
+ * without an expert too); its ids are experts (or -1) all the same.
  *   router: host struct (the library keeps no reference).  1 <= E <= 512, 1 <= top_k
  *   <= 64, E; groups <= 64 divides E; 1 <= group_k <= groups.  T <= 2^25.
  *   All arrays 4-byte aligned; ids and weights must not overlap anything.
