@@ -391,7 +391,7 @@ size_t mm_mul_mat_mxfp4_workspace_size(int64_t M, int64_t N, int64_t K, int src1
  *   4-byte aligned, codes 16-byte.  No other overlap than sum's.
  * A row with an infinity or NaN yields NaN in that row only (an infinity: zeros in the
  * row's finite places), a row of zeros with eps = 0 too.  rstd is infinite, as fp32,
- * where sqrt(mean + eps) is below 2^-128, and subnormal (a multiple of 2^-149, fewer
+ * where sqrt(mean + eps) is 2^-128 or less, and subnormal (a multiple of 2^-149, fewer
  * bits) past 2^126.
  * The order of a row's fp64 sum depends on T (below 512 rows or not) and D: the same
  * row in a call of another T may get the neighbouring rstd, about one row in 10^8.

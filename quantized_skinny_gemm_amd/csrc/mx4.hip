@@ -313,9 +313,10 @@ __global__ __launch_bounds__(512) void k_mx4_fused(
 // start, and the next stage has arrived.
 //
 // Bound: the weights' bytes for a few rows (32 x 14336 x 4096 8.2 us as traced, 4.0
-// TB/s); for many neither the matrix cores (34% busy at 512 x 128256 x 4096: 170 us,
-// 3.2 PFLOP/s) nor the address units (61%) but the latency of copies that two stages of
-// 256 x 256 do not cover and that a third one, past LDS, would.
+// TB/s); for many neither the matrix cores (34% busy at 512 x 128256 x 4096: 173 us as
+// traced, 3.1 PFLOP/s) nor the address units (61%) but the latency of copies: with 256 x
+// 256 one stage and a part of the next are under way while one is computed, and a third
+// stage of 256 k does not fit LDS.  (Four stages of 128 k would: not tried.)
 //
 // In LDS a row's eight 16-byte chunks are permuted by (row / 2) % 8, so that the
 // rows of an operand read lie in different banks.  Scales are copied for two stages

@@ -6,9 +6,13 @@
 // an integer that orders as the number does (0: not to be had, 1: NaN), the upper
 // half first: a maximum over the wave by DPP, then the lanes that hold it; only
 // where several do (equal upper halves) the lower halves and the indices decide.
-// Bound: latency for a few tokens (about 170 cycles per expert chosen; 1 token, 256
-// experts in 8 groups, 8 chosen: 5.0 us), the fp64 exponentials for many (4095 tokens,
-// 64 experts, 6 chosen: 5.6 us).
+// Bound: dependent latencies.  One token, 256 experts in 8 groups, sigmoid, 8 chosen:
+// 5.3 us as traced, of which 1.7 are what one choice among 64 experts takes (launch, read,
+// a score, write), 0.8 four experts per lane and their bias, 1.5 the groups, 1.4 the seven
+// further experts chosen (0.2 each); the wave waits for 72% of its time.  4095
+// tokens, 64 experts, 6 chosen: softmax 5.6 us, sigmoid 5.1; with one chosen 4.4 and
+// 3.7.  There vector instructions take about 2.5 us of a SIMD's time (one in seven is
+// fp64: the exponentials do not bound it), and a wave waits for 58% of its.
 #include "device.h"
 #include "kernels.h"
 #include "../../include/mm.h"
